@@ -74,6 +74,10 @@ extern "C" {
  * "Training and state saving", "Configure training backend"). */
 enum { RC_F32 = 0, RC_I32 = 1 };
 
+/* Further element types, of the row exchanges only (below): 16-bit floats for
+ * rows and router scores, 64-bit integers for token ids. */
+enum { RC_F16 = 2, RC_BF16 = 3, RC_I64 = 4 };
+
 /* Reduction operators: Sum and Mean (ruCCL README, "CUDA tensor example" and
  * section 6, ReduceOperation::Mean); Max (the ReduceOp of the Communicator's
  * all_reduce).  Mean is float32 only. */
@@ -322,6 +326,177 @@ int rc_finish(void);
  * the kernels that read the session's scratch before freeing it.  Always
  * returns RC_OK. */
 int rc_reset(void);
+
+/* ------------------------------------------------------------------------
+ * Row exchanges: whole-call operators that move rows between the ranks by an
+ * index computed on the GPU, where all_to_all_single has equal splits fixed
+ * by the host.  Expert routing, dispatch and combine (a router chooses
+ * experts, which are spread over the ranks; each token's row goes to the
+ * ranks of its experts and the results come back), and a vocabulary table
+ * sharded over the ranks with the gradient summed over all ranks' tokens.
+ *
+ * Rank r has tokens[r] >= 0 tokens, which may differ between ranks.  Arrays
+ * of R pointers hold one buffer per rank, dense and row-major, aligned to the
+ * element size; a buffer of zero elements may be NULL.  The arrays and
+ * descriptors are read during the call only.  Rows are RC_F32, RC_F16 or
+ * RC_BF16 (all ranks alike); sums are kept in float32 in the order given and
+ * rounded once, to nearest even.  Results depend on the inputs alone, not on
+ * launch shapes: there are no floating-point atomics.
+ *
+ * Indices on the GPU cannot be checked before the launch: an expert, slot or
+ * token id out of range is never followed, and counts as "none".
+ *
+ * Checks, in this order, before anything is enqueued: NOT_REGISTERED;
+ * INVALID_ARGUMENT for malformed fields, NULL or misaligned pointers, counts
+ * whose total passes 2^31 - 1, a workspace too small; INVALID_ARGUMENT for an
+ * output that overlaps another output or any input.  A call with nothing to
+ * do returns RC_OK.  Only kernels are enqueued, and all scratch is the
+ * caller's workspace, so every call can be captured into a HIP graph; calls
+ * that may run at the same time need workspaces of their own. */
+
+#define RC_MAX_EXPERTS 1024
+#define RC_MAX_TOP_K 16
+#define RC_MAX_EXPERT_GROUPS 64
+
+enum { RC_SCORE_SOFTMAX = 0, RC_SCORE_SIGMOID = 1 };
+enum { RC_GROUP_MAX = 0, RC_GROUP_TOP2 = 1 };
+
+/* Expert choice.  struct_size = sizeof(rc_route_desc).
+ *   dtype        of the logits (and of their gradient)
+ *   num_experts  E in [1, RC_MAX_EXPERTS]
+ *   top_k        K in [1, RC_MAX_TOP_K], at most top_groups * E / num_groups
+ *   score        s = softmax of the token's E logits, or sigmoid of each
+ *   num_groups   in [1, RC_MAX_EXPERT_GROUPS], divides E; consecutive experts
+ *   top_groups   in [1, num_groups]: groups whose experts may be chosen
+ *   group_by     a group's score: its largest s + bias, or the sum of its two
+ *                largest (the one of a group of one)
+ *   renormalize  nonzero: divide the K scores by their sum
+ *   scale        factor of the weights
+ *   bias         NULL, or E float32 on the GPU: added to the scores for the
+ *                choice of groups and experts only, not in the weights */
+typedef struct rc_route_desc {
+    uint32_t struct_size;
+    int32_t dtype;
+    int32_t num_experts;
+    int32_t top_k;
+    int32_t score;
+    int32_t num_groups;
+    int32_t top_groups;
+    int32_t group_by;
+    int32_t renormalize;
+    float scale;
+    const float* bias;
+} rc_route_desc;
+
+/* Chooses K experts for every token.  logits[r]: [tokens[r], E]; weights[r]
+ * and experts[r]: [tokens[r], K], by falling s + bias, equal ones by rising
+ * index.  The comparison is that of the values in 64 bits, however close.
+ * weights = scale * s, or scale * s / (sum of the K s).  An expert whose
+ * logit is -inf, or whose s + bias is -inf or NaN, is never chosen; a token
+ * with fewer than K others has expert -1 and weight 0 in the rest, and a sum
+ * of zero gives weights of zero. */
+int rc_route(const rc_route_desc* desc, const int64_t* tokens, const void* const* logits, float* const* weights,
+             int32_t* const* experts, void* stream);
+
+/* The gradient of rc_route's weights: d_logits[r] ([tokens[r], E]) from
+ * d_weights[r] and the experts rc_route chose ([tokens[r], K]); an expert
+ * outside [0, E) has no part.  The choice itself has no gradient; desc's
+ * groups, group_by and bias are not used. */
+int rc_route_grad(const rc_route_desc* desc, const int64_t* tokens, const void* const* logits,
+                  const int32_t* const* experts, const float* const* d_weights, void* const* d_logits, void* stream);
+
+/* The exchange of one batch of tokens with their experts' ranks.
+ * struct_size = sizeof(rc_exchange_desc).
+ *   dtype        of the rows
+ *   num_experts  E in [1, RC_MAX_EXPERTS], divisible by R; rank d has the
+ *                experts [d*E/R, (d+1)*E/R)
+ *   top_k        K in [1, RC_MAX_TOP_K]
+ *   width        elements of a row, >= 1
+ *   tokens       [R]
+ *   capacity     [R] >= 0: rows that rank d's row buffer holds
+ *   experts      [R]: [tokens[r], K]
+ *   slots        [R]: [tokens[r], K], the row of rank d = expert / (E/R) that
+ *                (token, k) has, or -1; written by rc_dispatch_plan */
+typedef struct rc_exchange_desc {
+    uint32_t struct_size;
+    int32_t dtype;
+    int32_t num_experts;
+    int32_t top_k;
+    int64_t width;
+    const int64_t* tokens;
+    const int64_t* capacity;
+    const int32_t* const* experts;
+    int32_t* const* slots;
+} rc_exchange_desc;
+
+/* Places every (rank, token, k): each rank's rows are ordered by expert, then
+ * rank, token and k.  offsets[d] ([E/R + 1]): the first row of each of rank
+ * d's experts, then the end, none past capacity[d]; counts[d] ([E/R]): the
+ * entries that chose each expert, also those that found no room.  An entry
+ * with no expert, or whose row would lie past the capacity, has slot -1.
+ * dtype and width are not used. */
+int rc_dispatch_plan_workspace(const rc_exchange_desc* desc, int64_t* bytes);
+int rc_dispatch_plan(const rc_exchange_desc* desc, int32_t* const* offsets, int32_t* const* counts, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/* rows[d][slot] = xs[r][token] for every placed entry, bit for bit.  Rows
+ * behind offsets' end are left as they were. */
+int rc_dispatch(const rc_exchange_desc* desc, const void* const* xs, void* const* rows, void* stream);
+
+/* outs[r][token] = sum over k = 0, 1, ... of weights[r][token, k] *
+ * rows[d][slot]; entries without a slot add nothing.  weights may be NULL (all
+ * one): that is rc_dispatch's gradient. */
+int rc_combine(const rc_exchange_desc* desc, const void* const* rows, const float* const* weights,
+               void* const* outs, void* stream);
+
+/* The gradients of rc_combine: d_rows[d][slot] = weights * d_outs[r][token]
+ * (rows without an entry are left as they were) and d_weights[r][token, k] =
+ * the dot product of d_outs[r][token] and rows[d][slot] (0 without a slot). */
+int rc_combine_grad(const rc_exchange_desc* desc, const void* const* d_outs, const void* const* rows,
+                    const float* const* weights, void* const* d_rows, float* const* d_weights, void* stream);
+
+/* A vocabulary table split over the ranks as ring segments are: with S =
+ * ceil(vocab / R), rank c holds the rows [c*S, min((c+1)*S, vocab)).
+ * struct_size = sizeof(rc_embedding_desc).
+ *   dtype       of the table and the looked-up rows (gradient: of d_outs)
+ *   id_dtype    RC_I32 or RC_I64
+ *   grad_dtype  of the table's gradient: RC_F32 or dtype
+ *   accumulate  gradient: nonzero adds to what d_tables hold
+ *   vocab       in [1, 2^31 - 2]
+ *   width       elements of a row, >= 1
+ *   scale       factor of the looked-up rows
+ *   tokens      [R]
+ *   ids         [R]: [tokens[r]]; an id outside [0, vocab) names no row */
+typedef struct rc_embedding_desc {
+    uint32_t struct_size;
+    int32_t dtype;
+    int32_t id_dtype;
+    int32_t grad_dtype;
+    int32_t accumulate;
+    float scale;
+    int64_t vocab;
+    int64_t width;
+    const int64_t* tokens;
+    const void* const* ids;
+} rc_embedding_desc;
+
+/* outs[r][t] = scale * table[ids[r][t]] (bit for bit with a scale of 1); zeros
+ * for an id that names no row. */
+int rc_embedding(const rc_embedding_desc* desc, const void* const* tables, void* const* outs, void* stream);
+
+/* The table's gradient, summed over the tokens of all ranks: row v of
+ * d_tables is scale times the sum of d_outs[r][t] over ids[r][t] == v, taken
+ * in order of rank and t: pieces of 64 are summed from zero, runs of 64
+ * pieces likewise, and the runs added in order.  With accumulate the row's
+ * old value is added once at the end, and rows that no id names are not
+ * touched; without, they are set to zero. */
+int rc_embedding_grad_workspace(const rc_embedding_desc* desc, int64_t* bytes);
+int rc_embedding_grad(const rc_embedding_desc* desc, const void* const* d_outs, void* const* d_tables,
+                      void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The open session's rank count and GPU (-1 in a validate_only session opened
+ * without one).  RC_ERR_NOT_REGISTERED if no session is open. */
+int rc_session_info(int* num_ranks, int* device);
 
 /* ------------------------------------------------------------------------
  * Per-rank front end.  Each logical rank registers itself and issues its own

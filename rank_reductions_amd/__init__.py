@@ -36,7 +36,8 @@ __all__ = [
     "rank_broadcast", "rank_reduce_scatter", "rank_all_gather", "rank_all_reduce_params",
     "all_gather_list", "all_to_all_single", "send_recv", "barrier", "rank_all_gather_list",
     "rank_all_to_all_single", "rank_send", "rank_recv", "rank_barrier", "rank_split", "rank_split_all",
-    "Communicator",
+    "Communicator", "route", "route_grad", "DispatchPlan", "dispatch_plan", "dispatch", "combine", "combine_grad",
+    "embedding", "embedding_grad",
 ]
 
 RC_MAX_RANKS = 16
@@ -192,6 +193,7 @@ def _load():
     lib.rc_rank_split.restype = ctypes.c_int
     lib.rc_rank_finish.argtypes = [ctypes.c_int]
     lib.rc_rank_finish.restype = ctypes.c_int
+    rows.declare(lib)
     return lib
 
 
@@ -824,3 +826,9 @@ class Communicator:
 
     def finish(self):
         rank_finish(self._ep)
+
+
+from . import rows  # noqa: E402 - it uses this module's names
+from .rows import (  # noqa: E402,F401
+    DispatchPlan, combine, combine_grad, dispatch, dispatch_plan, embedding, embedding_grad, route, route_grad,
+)

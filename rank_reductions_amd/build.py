@@ -20,7 +20,7 @@ INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = PKG / "librankred.so"
 
-HOST_SOURCES = ["session.cpp", "validate.cpp", "plan.cpp"]
+HOST_SOURCES = ["session.cpp", "validate.cpp", "plan.cpp", "rows.cpp"]
 # (source, object, defines): the fold and batch kernels are built once per
 # element type and cache hint, so that their instantiations compile in parallel
 RC_F32, RC_I32 = 0, 1
@@ -32,6 +32,9 @@ HIP_SOURCES = [
     ("kernels_batch.hip", "kernels_batch_nt", {"RC_KNT": 1}),
     ("kernels_batch.hip", "kernels_batch_cached", {"RC_KNT": 0}),
     ("kernels_copy.hip", "kernels_copy", {}),
+    ("rows_route.hip", "rows_route", {}),
+    ("rows_exchange.hip", "rows_exchange", {}),
+    ("rows_embedding.hip", "rows_embedding", {}),
     ("device.hip", "device", {}),
 ]
 
@@ -84,7 +87,7 @@ def build(verbose=False, extra_hip_flags=()):
         jobs.append([hipcc, *HIP_FLAGS, *extra_hip_flags, *dflags, *inc, "-c", CSRC / src, "-o", obj])
         objs.append(obj)
     # the largest objects first, so the pool ends together
-    jobs.sort(key=lambda c: 0 if "kernels_fold.hip" in str(c) else 1)
+    jobs.sort(key=lambda c: 0 if "kernels_fold.hip" in str(c) or "rows_route.hip" in str(c) else 1)
     with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 8, 16)) as ex:
         list(ex.map(lambda c: _run(c, verbose), jobs))
     tmp = LIB.with_suffix(".so.tmp")

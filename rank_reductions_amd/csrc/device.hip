@@ -369,6 +369,14 @@ Error device_launch_batch(const BatchPlan& p, void* stream) {
     return {};
 }
 
+Error device_run(const std::function<int()>& launch) {
+    DeviceGuard guard;
+    if (guard.err != hipSuccess) return hip_fail("hipSetDevice", guard.err);
+    const hipError_t e = static_cast<hipError_t>(launch());
+    if (e != hipSuccess) return hip_fail("kernel launch", e);
+    return {};
+}
+
 Error device_finish() {
     DeviceGuard guard;
     if (guard.err != hipSuccess) return hip_fail("hipSetDevice", guard.err);

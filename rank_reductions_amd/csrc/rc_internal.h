@@ -5,6 +5,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <functional>
 #include <string>
 #include <vector>
 
@@ -121,6 +122,12 @@ Error validate_batch(int nranks, int num_tensors, const rc_buf* bufs,
 Error match_params(int nranks, const int* counts, const rc_param* const* params,
                    std::vector<rc_buf>* bufs, std::vector<const void*>* accs, std::vector<uint64_t>* order);
 int64_t element_size(int dtype);
+
+// ---------------------------------------------------------------- session.cpp
+// One whole-call entry point kept in another file: `body` runs under the
+// session lock once the session is known to be open for whole calls, and its
+// Error becomes the entry point's status and message.
+int whole_call(const std::function<Error(int nranks, bool validate_only)>& body);
 
 // ---------------------------------------------------------------- plan.cpp
 // Unroll (16-byte vectors per lane per round) of a fold of `nin` inputs: about
@@ -431,6 +438,8 @@ Error device_launch_batch(const BatchPlan& p, void* stream);
 constexpr size_t kStaticScratchBytes = size_t(1) << 20;
 size_t batch_table_bytes(const BatchPlan& p);
 Error device_launch_batch_static(const BatchPlan& p, void* stream);
+// Runs `launch` (which returns a hipError_t) with the session's GPU current.
+Error device_run(const std::function<int()>& launch);
 Error device_finish();   // wait for the GPU, free scratch
 void device_reset();     // wait for kernels reading scratch, free scratch
 // Events that order the per-rank front end's streams around a launch.

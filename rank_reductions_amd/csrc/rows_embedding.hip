@@ -1,0 +1,532 @@
+// The sharded embedding: lookup of rows by token id, and the table's gradient
+// by sorted ids.
+//
+// Lookup: one wave per piece of a token's row; bound by memory.
+//
+// Gradient: dW[v] = scale * sum of dy over the tokens whose id is v.  The ids
+// of all ranks are sorted (stably, with their positions), so that the rows of
+// one id lie side by side in the list.  The list is cut into windows of
+// kPiece entries, one workgroup each (and per piece of the columns): it sums
+// the ids that begin in its window, running on past the window's end, so no
+// workgroup takes more than two windows' entries.  An id with more than
+// kPiece entries is cut into pieces of kPiece from its first entry on; the
+// workgroup in whose window a piece begins leaves its sum in the workspace
+// and a second kernel joins them.  What an id's sum adds, and in what order,
+// thus depends on its own tokens only.  Other workgroups of the same launch
+// clear the table's rows that no id names.  Bound by memory: dy is read once
+// and the table written once.
+#include "rows_sort.h"
+
+namespace rc {
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowVecs = 2;  // 16-byte vectors per lane and piece
+
+__device__ __forceinline__ int64_t id_of(const void* ids, int32_t id64, int32_t i) {
+    return id64 ? static_cast<const int64_t*>(ids)[i] : (int64_t) static_cast<const int32_t*>(ids)[i];
+}
+
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void embedding_kernel(EmbeddingArgs a) {
+    using E = typename T::E;
+    const int64_t item = group_index() * (kRowThreads / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if (item >= (int64_t)a.tokens.total() * a.chunks) return;
+    const int32_t n = (int32_t)(item / a.chunks);
+    int32_t token;
+    const int rank = rank_of(a.tokens, n, &token);
+    const int64_t first = (item - (int64_t)n * a.chunks) * (kWave * T::n * kRowVecs) + lane_id() * T::n;
+    const int64_t id = id_of(a.ids[rank], a.id64, token);
+    const bool named = id >= 0 && id < a.vocab;
+    const int32_t shard = named ? (int32_t)id / (int32_t)a.shard : 0;
+    const E* src = static_cast<const E*>(a.table[shard]) + (named ? id - shard * a.shard : 0) * a.width;
+    E* dst = static_cast<E*>(a.out[rank]) + (int64_t)token * a.width;
+    const bool copy = a.scale == 1.0f;
+    u32x4 v[kRowVecs];
+#pragma unroll
+    for (int u = 0; u < kRowVecs; ++u) {
+        const int64_t col = first + u * (kWave * T::n);
+        v[u] = u32x4{0, 0, 0, 0};
+        if (named && col + T::n <= a.width) v[u] = load16<T>(src + col);
+    }
+#pragma unroll
+    for (int u = 0; u < kRowVecs; ++u) {
+        const int64_t col = first + u * (kWave * T::n);
+        if (col + T::n <= a.width) {
+            if (!copy && named) {
+                float f[T::n];
+                T::unpack(v[u], f);
+#pragma unroll
+                for (int i = 0; i < T::n; ++i) f[i] *= a.scale;
+                v[u] = T::pack(f);
+            }
+            store16<T>(dst + col, v[u]);
+        } else {
+            for (int64_t c = col; c < a.width; ++c) {
+                if (!named) dst[c] = T::store(0.0f);
+                else dst[c] = copy ? src[c] : T::store(T::load(src[c]) * a.scale);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- sorting the ids
+
+// One pass's places over one block.
+template <bool FIRST>
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortPass s) {
+    __shared__ int32_t count[kSortWaves * kSortBins];
+    __shared__ int32_t start[kSortBins];
+    __shared__ int32_t carry[kSortWaves];
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const int32_t* total = s.hist + (int64_t)s.blocks.total() * s.bins;
+    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) {
+        start[d] = total[d];
+        for (int w = 0; w < kSortWaves; ++w) count[w * kSortBins + d] = 0;
+    }
+    __syncthreads();
+    exclusive_sum<kSortThreads>(start, s.bins, carry);
+    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) start[d] += s.hist[(int64_t)blockIdx.x * s.bins + d];
+    int32_t block;
+    const int rank = rank_of(s.blocks, blockIdx.x, &block);
+    const int at = wave * kStrips * kWave + lane;
+    const int32_t ones = (1 << s.bits) - 1;
+    int32_t key[kStrips], val[kStrips];
+#pragma unroll
+    for (int k = 0; k < kStrips; ++k) {
+        if (!sort_entry<FIRST>(s, rank, block, at + k * kWave, &key[k], &val[k])) key[k] = -1;
+        else atomicAdd(&count[wave * kSortBins + ((key[k] >> s.shift) & ones)], 1);
+    }
+    wave_starts<kSortWaves>(count, start, s.bins);
+#pragma unroll
+    for (int k = 0; k < kStrips; ++k) {
+        const bool has = key[k] >= 0;
+        const int32_t place = strip_rank((key[k] >> s.shift) & ones, s.bits, has, &count[wave * kSortBins]);
+        if (has) {
+            s.out_keys[place] = key[k];
+            s.out_vals[place] = val[k];
+        }
+    }
+}
+
+// All passes in one workgroup, for few ids: each pass reads what the one
+// before wrote (the first the ids) and the last writes to `to`, so the
+// buffers alternate from there.
+constexpr int kSmallWaves = 8;
+constexpr int kSmallIds = 8192;
+constexpr int kSmallStrips = kSmallIds / (kSmallWaves * kWave);
+struct SmallSort {
+    SortPass first;    // spans, ids, id64, key_limit
+    int32_t* keys[2];  // pass p writes to [(passes - 1 - p) & 1]
+    int32_t* vals[2];
+    int32_t passes;
+    int32_t bits;      // of each pass
+};
+__global__ __launch_bounds__(kSmallWaves* kWave) void sort_small_kernel(SmallSort a) {
+    __shared__ int32_t count[kSmallWaves * kSortBins];
+    __shared__ int32_t start[kSortBins];
+    __shared__ int32_t carry[kSmallWaves];
+    constexpr int kThreads = kSmallWaves * kWave;
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const int32_t n = a.first.spans.total();
+    const int strips = (n + kThreads - 1) / kThreads;
+    const int32_t at = wave * strips * kWave + lane;
+    const int bins = 1 << a.bits;
+    for (int p = 0; p < a.passes; ++p) {
+        const int shift = p * a.bits;
+        for (int d = threadIdx.x; d < bins; d += kThreads)
+            for (int w = 0; w < kSmallWaves; ++w) count[w * kSortBins + d] = 0;
+        __syncthreads();
+        const int from = (a.passes - p) & 1, to = from ^ 1;
+        int32_t key[kSmallStrips], val[kSmallStrips];
+#pragma unroll
+        for (int k = 0; k < kSmallStrips; ++k) {
+            const int32_t j = at + k * kWave;
+            key[k] = -1;
+            val[k] = j;
+            if (k < strips && j < n) {
+                if (p == 0) {
+                    int32_t i;
+                    const int rank = rank_of(a.first.spans, j, &i);
+                    key[k] = first_key(a.first, rank, i);
+                } else {
+                    key[k] = a.keys[from][j];
+                    val[k] = a.vals[from][j];
+                }
+                atomicAdd(&count[wave * kSortBins + ((key[k] >> shift) & (bins - 1))], 1);
+            }
+        }
+        __syncthreads();
+        for (int d = threadIdx.x; d < bins; d += kThreads) {
+            int32_t sum = 0;
+            for (int w = 0; w < kSmallWaves; ++w) sum += count[w * kSortBins + d];
+            start[d] = sum;
+        }
+        __syncthreads();
+        exclusive_sum<kThreads>(start, bins, carry);
+        wave_starts<kSmallWaves>(count, start, bins);
+#pragma unroll
+        for (int k = 0; k < kSmallStrips; ++k) {
+            if (k < strips) {  // alike in all lanes
+                const bool has = key[k] >= 0;
+                const int32_t place = strip_rank((key[k] >> shift) & (bins - 1), a.bits, has, &count[wave * kSortBins]);
+                if (has) {
+                    a.keys[to][place] = key[k];
+                    a.vals[to][place] = val[k];
+                }
+            }
+        }
+        __threadfence_block();
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- summing
+
+constexpr int kSumThreads = 256;
+constexpr int kAhead = 4;  // rows of dy in flight per lane
+
+// First of the sorted keys in [lo, hi) that is not below `key`.
+__device__ __forceinline__ int32_t lower_bound(const int32_t* keys, int32_t lo, int32_t hi, int64_t key) {
+    while (lo < hi) {
+        const int32_t mid = lo + (hi - lo) / 2;
+        if (keys[mid] < key) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// The gradient's row v in its shard.
+template <class G>
+__device__ __forceinline__ typename G::E* table_row(const EmbeddingGradArgs& a, int64_t v) {
+    const int32_t shard = (int32_t)v / (int32_t)a.shard;
+    return static_cast<typename G::E*>(a.table[shard]) + (v - shard * a.shard) * a.width;
+}
+
+template <class G, int N>
+__device__ __forceinline__ void finish_row(const EmbeddingGradArgs& a, int64_t v, int64_t col, int rem, const float* sum) {
+    typename G::E* row = table_row<G>(a, v) + col;
+    float f[N];
+    if (rem == N) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = sum[i] * a.scale;
+        if (a.accumulate) {
+#pragma unroll
+            for (int i = 0; i < N; i += G::n) {
+                float old[G::n];
+                G::unpack(load16<G>(row + i), old);
+#pragma unroll
+                for (int j = 0; j < G::n; ++j) f[i + j] += old[j];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; i += G::n) store16<G>(row + i, G::pack(f + i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < rem) row[i] = G::store((a.accumulate ? G::load(row[i]) : 0.0f) + sum[i] * a.scale);
+    }
+}
+
+// T: type of dy; G: type of the table's gradient.
+template <class T, class G>
+__global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGradArgs a) {
+    using E = typename T::E;
+    __shared__ int32_t keys[3 * kPiece];  // of the positions p0 - 1 .. p0 + 2 kPiece
+    __shared__ const E* rows[2 * kPiece];
+    const int lane = lane_id();
+    const int32_t n = a.tokens.total();
+    const int64_t group = group_index();
+    if (group >= (int64_t)a.windows + a.fill_groups) return;
+    if (group >= a.windows) {
+        // clear the rows of 64 ids that no token names
+        const int64_t first = (group - a.windows) * kWave;
+        const int32_t at = first + lane < a.vocab ? lower_bound(a.keys, 0, n, first + lane) : n;
+        const bool hit = at < n && a.keys[at] == first + lane;
+        uint64_t clear = __ballot(first + lane < a.vocab && !hit);
+        const int64_t lo = (int64_t)blockIdx.z * (kSumThreads * T::n), hi = min(lo + kSumThreads * T::n, a.width);
+        while (clear) {
+            const int j = __builtin_ctzll(clear);
+            clear &= clear - 1;
+            typename G::E* row = table_row<G>(a, first + j);
+            for (int64_t c = lo + threadIdx.x * G::n; c < hi; c += kSumThreads * G::n) {
+                if (c + G::n <= hi) store16<G>(row + c, u32x4{0, 0, 0, 0});
+                else
+                    for (int64_t i = c; i < hi; ++i) row[i] = G::store(0.0f);
+            }
+        }
+        return;
+    }
+    const int32_t p0 = (int32_t)(group * kPiece);
+    for (int t = threadIdx.x; t < 2 * kPiece + 2; t += kSumThreads) {
+        const int64_t p = (int64_t)p0 - 1 + t;
+        keys[t] = p >= 0 && p < n ? a.keys[p] : -1;
+        if (t >= 1 && t <= 2 * kPiece) {
+            const E* src = nullptr;
+            if (p < n) {
+                int32_t token;
+                const int rank = rank_of(a.tokens, a.vals[p], &token);
+                src = static_cast<const E*>(a.d_out[rank]) + (int64_t)token * a.width;
+            }
+            rows[t - 1] = src;
+        }
+    }
+    __syncthreads();
+    // positions from here on count from p0; key(i) of position i
+    const int32_t* key = keys + 1;
+    const int32_t none = (int32_t)a.vocab;  // ids that name no row sort last
+    const bool real = key[lane] >= 0 && key[lane] < none;
+    const uint64_t begins = __ballot(real && key[lane] != key[lane - 1]);
+    const uint64_t longs = __ballot(real && key[lane] != key[lane - 1] && key[lane] == key[lane + kPiece]);
+    const int valid = __popcll(__ballot(real)) + __popcll(__ballot(key[lane + kPiece] >= 0 && key[lane + kPiece] < none));
+    // first position past the window that is not of the window's last id
+    const uint64_t other = __ballot(key[lane + kPiece] != key[kPiece - 1]);
+    const int last_end = min(valid, kPiece + (other ? (int)__builtin_ctzll(other) : kPiece));
+    int begin = begins ? (int)__builtin_ctzll(begins) : 2 * kPiece;
+    int carried = 0;  // positions below it belong to a piece of an id that began earlier
+    if (key[0] >= 0 && key[0] < none && key[0] == key[-1]) {
+        const int32_t s = lower_bound(a.keys, 0, p0, key[0]);
+        if (s + (int64_t)kPiece < n && a.keys[s + kPiece] == key[0]) {
+            const int ps = (int)(((int64_t)p0 - s + kPiece - 1) / kPiece * kPiece + s - p0);
+            const int end = begins ? begin : last_end;  // of the id, or two windows on
+            if (ps < kPiece && ps < end) {
+                carried = min(ps + kPiece, end);
+                begin = ps;
+            }
+        }
+    }
+    int end;
+    const int hot = longs ? (int)__builtin_ctzll(longs) : 2 * kPiece;
+    if (longs) end = hot + kPiece;
+    else if (begins) end = last_end;
+    else end = carried;
+    if (begin >= end) return;
+
+    const int64_t col = ((int64_t)blockIdx.z * kSumThreads + threadIdx.x) * T::n;
+    const int rem = (int)max((int64_t)0, min((int64_t)T::n, a.width - col));
+    if (rem == 0) return;
+    auto fetch = [&](int j, float* f) {
+        const E* src = rows[j] + col;
+        if (rem == T::n) T::unpack(load16<T>(src), f);
+        else {
+#pragma unroll
+            for (int i = 0; i < T::n; ++i) f[i] = i < rem ? T::load(src[i]) : 0.0f;
+        }
+    };
+    float acc[T::n] = {};
+    for (int j0 = begin; j0 < end; j0 += kAhead) {
+        float f[kAhead][T::n];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (j0 + u < end) fetch(j0 + u, f[u]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int j = j0 + u;
+            if (j >= end) break;
+#pragma unroll
+            for (int i = 0; i < T::n; ++i) acc[i] += f[u][i];
+            // an id's last entry, or a piece's
+            if (j + 1 == end || j + 1 == carried || key[j + 1] != key[j]) {
+                if (j < carried || j >= hot) {
+                    float* out = a.partial + (2 * group + (j < carried ? 0 : 1)) * a.width + col;
+#pragma unroll
+                    for (int i = 0; i < T::n; ++i)
+                        if (i < rem) out[i] = acc[i];
+                } else {
+                    finish_row<G, T::n>(a, key[j], col, rem, acc);
+                }
+#pragma unroll
+                for (int i = 0; i < T::n; ++i) acc[i] = 0.0f;
+            }
+        }
+    }
+}
+
+// Joins the pieces of the long id that begins in the window, if there is one:
+// runs of kPiece pieces, one wave each, added in order.
+constexpr int kJoinWaves = 4;
+constexpr int kJoinCols = kWave * 4;
+template <class G>
+__global__ __launch_bounds__(kJoinWaves* kWave) void embedding_join_kernel(EmbeddingGradArgs a) {
+    __shared__ float run[kJoinWaves][kJoinCols];
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const int32_t n = a.tokens.total();
+    const int64_t group = group_index();
+    if (group >= a.windows) return;
+    const int32_t p0 = (int32_t)(group * kPiece);
+    const int64_t p = (int64_t)p0 + lane;
+    const int32_t key = p < n ? a.keys[p] : -1;
+    const bool first = key >= 0 && key < a.vocab && (p == 0 || a.keys[p - 1] != key);
+    const uint64_t longs = __ballot(first && p + kPiece < n && a.keys[p + kPiece] == key);
+    if (!longs) return;
+    const int32_t s = p0 + (int)__builtin_ctzll(longs);
+    const int32_t id = a.keys[s];
+    const int32_t stop = lower_bound(a.keys, s, n, (int64_t)id + 1);
+    const int64_t pieces = ((int64_t)stop - s + kPiece - 1) / kPiece;
+    const int64_t runs = (pieces + kPiece - 1) / kPiece;
+    const int64_t col = (int64_t)blockIdx.z * kJoinCols + lane * 4;
+    const int rem = (int)max((int64_t)0, min((int64_t)4, a.width - col));
+    float total[4] = {};
+    for (int64_t r0 = 0; r0 < runs; r0 += kJoinWaves) {
+        float sum[4] = {};
+        const int64_t lo = (r0 + wave) * kPiece, hi = min(lo + kPiece, pieces);
+#pragma unroll 8
+        for (int64_t i = lo; i < hi; ++i) {
+            // the first piece is the second kind of the window it begins in
+            const float* src = a.partial + (2 * (group + i) + (i == 0)) * a.width + col;
+            if (rem == 4) {
+                float f[4];
+                F32::unpack(load16<F32>(src), f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sum[c] += f[c];
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c < rem) sum[c] += src[c];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) run[wave][lane * 4 + c] = sum[c];
+        __syncthreads();
+        for (int w = 0; w < kJoinWaves && r0 + w < runs; ++w)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) total[c] += run[w][lane * 4 + c];
+        __syncthreads();
+    }
+    if (wave != 0 || rem == 0) return;
+    typename G::E* row = table_row<G>(a, id) + col;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (c < rem) row[c] = G::store((a.accumulate ? G::load(row[c]) : 0.0f) + total[c] * a.scale);
+}
+
+int bits_of(int64_t values) {
+    int b = 0;
+    while ((int64_t(1) << b) < values) ++b;
+    return b;
+}
+
+// The sort's passes over keys in [0, vocab]: as few as kSortBins allows, of
+// equal width.
+void passes_of(int64_t vocab, int* passes, int* bits) {
+    const int all = bits_of(vocab + 1), most = bits_of(kSortBins);
+    *passes = (all + most - 1) / most;
+    *bits = (all + *passes - 1) / *passes;
+}
+
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// Where the gradient's workspace keeps what.
+struct Layout {
+    int64_t keys[2], vals[2], hist, partial, bytes;
+};
+Layout layout_of(const RankSpans& tokens, int64_t vocab, int64_t width) {
+    Layout l{};
+    const int64_t n = tokens.total(), list = align256(n * 4);
+    if (n == 0) return l;
+    l.keys[0] = 0;
+    l.keys[1] = list;
+    l.vals[0] = 2 * list;
+    l.vals[1] = 3 * list;
+    l.hist = 4 * list;
+    int passes, bits;
+    passes_of(vocab, &passes, &bits);
+    // the first pass cuts each rank's ids into blocks of their own
+    const int64_t hist = n <= kSmallIds ? 0 : ((int64_t)sort_blocks(tokens).total() + 1) * (int64_t(1) << bits) * 4;
+    l.partial = l.hist + align256(hist);
+    l.bytes = l.partial + (n + kPiece - 1) / kPiece * 2 * width * 4;
+    return l;
+}
+
+template <class T>
+int run_embedding(EmbeddingArgs a, hipStream_t s) {
+    const int64_t piece = kWave * T::n * kRowVecs;
+    a.chunks = (int32_t)((a.width + piece - 1) / piece);
+    const int64_t items = (int64_t)a.tokens.total() * a.chunks, per = kRowThreads / kWave;
+    hipLaunchKernelGGL(embedding_kernel<T>, grid_of((items + per - 1) / per), dim3(kRowThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+template <class T, class G>
+int run_sum(EmbeddingGradArgs a, hipStream_t s) {
+    const int64_t cols = kSumThreads * T::n;
+    const int64_t groups = (int64_t)a.windows + a.fill_groups;
+    if (groups)
+        hipLaunchKernelGGL((embedding_grad_kernel<T, G>), grid_of(groups, (a.width + cols - 1) / cols), dim3(kSumThreads), 0, s, a);
+    if (a.tokens.total() > kPiece)
+        hipLaunchKernelGGL(embedding_join_kernel<G>, grid_of(a.windows, (a.width + kJoinCols - 1) / kJoinCols),
+                           dim3(kJoinWaves * kWave), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int launch_embedding(const EmbeddingArgs& a, int dtype, void* stream) {
+    return RC_BY_TYPE(run_embedding, a, static_cast<hipStream_t>(stream));
+}
+
+int64_t embedding_grad_workspace_bytes(const RankSpans& tokens, int64_t vocab, int64_t width) {
+    return layout_of(tokens, vocab, width).bytes;
+}
+
+int launch_embedding_grad(EmbeddingGradArgs a, SortPass sort, int dtype, int grad_dtype, void* workspace, void* stream) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int32_t n = a.tokens.total();
+    const Layout l = layout_of(a.tokens, a.vocab, a.width);
+    char* ws = static_cast<char*>(workspace);
+    int32_t *keys[2], *vals[2];
+    for (int i = 0; i < 2; ++i) {
+        keys[i] = reinterpret_cast<int32_t*>(ws + l.keys[i]);
+        vals[i] = reinterpret_cast<int32_t*>(ws + l.vals[i]);
+    }
+    int passes, bits;
+    passes_of(a.vocab, &passes, &bits);
+    sort.drop = 0;
+    if (n > 0 && n <= kSmallIds) {
+        SmallSort m{};
+        m.first = sort;
+        for (int i = 0; i < 2; ++i) {
+            m.keys[i] = keys[i];
+            m.vals[i] = vals[i];
+        }
+        m.passes = passes;
+        m.bits = bits;
+        hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(kSmallWaves * kWave), 0, s, m);
+    } else if (n > 0) {
+        sort.bits = bits;
+        sort.bins = 1 << bits;
+        sort.hist = reinterpret_cast<int32_t*>(ws + l.hist);
+        for (int p = 0; p < passes; ++p) {
+            const int to = (passes - 1 - p) & 1;
+            sort.shift = p * bits;
+            sort.out_keys = keys[to];
+            sort.out_vals = vals[to];
+            if (p == 1) {  // one list from here on
+                for (int r = 1; r <= kMaxRanks; ++r) sort.spans.first[r] = n;
+                sort.spans.nranks = 1;
+            }
+            if (p >= 1) {
+                sort.keys = keys[to ^ 1];
+                sort.vals = vals[to ^ 1];
+            }
+            sort.blocks = sort_blocks(sort.spans);
+            const int32_t blocks = sort.blocks.total();
+            if (p == 0) hipLaunchKernelGGL(sort_count_kernel<true>, dim3(blocks), dim3(kSortThreads), 0, s, sort);
+            else hipLaunchKernelGGL(sort_count_kernel<false>, dim3(blocks), dim3(kSortThreads), 0, s, sort);
+            hipLaunchKernelGGL(sort_scan_kernel, dim3((sort.bins + kWave - 1) / kWave), dim3(kScanWaves * kWave), 0, s,
+                               sort.hist, blocks, sort.bins);
+            if (p == 0) hipLaunchKernelGGL(sort_place_kernel<true>, dim3(blocks), dim3(kSortThreads), 0, s, sort);
+            else hipLaunchKernelGGL(sort_place_kernel<false>, dim3(blocks), dim3(kSortThreads), 0, s, sort);
+        }
+    }
+    a.keys = keys[0];
+    a.vals = vals[0];
+    a.partial = reinterpret_cast<float*>(ws + l.partial);
+    a.windows = (int32_t)(((int64_t)n + kPiece - 1) / kPiece);
+    a.fill_groups = a.accumulate ? 0 : (int32_t)((a.vocab + kWave - 1) / kWave);
+    if (dtype == RC_F32) return run_sum<F32, F32>(a, s);
+    if (dtype == RC_F16) return grad_dtype == RC_F32 ? run_sum<F16, F32>(a, s) : run_sum<F16, F16>(a, s);
+    return grad_dtype == RC_F32 ? run_sum<BF16, F32>(a, s) : run_sum<BF16, BF16>(a, s);
+}
+
+}  // namespace rc

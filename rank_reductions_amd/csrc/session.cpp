@@ -18,6 +18,8 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
+#include <functional>
 #include <map>
 #include <memory>
 #include <mutex>
@@ -349,6 +351,23 @@ Error whole_call_session() {
         return Error{RC_ERR_INVALID_ARGUMENT, "the session was opened per rank: use the rc_rank_* entry points"};
     return {};
 }
+
+}  // namespace
+
+int whole_call(const std::function<Error(int, bool)>& body) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    Error e = whole_call_session();
+    if (!e.code) {
+        try {
+            e = body(g_s.nranks, g_s.cfg.validate_only);
+        } catch (const std::exception& ex) {  // out of host memory: nothing was enqueued
+            e = Error{RC_ERR_INVALID_ARGUMENT, ex.what()};
+        }
+    }
+    return report(e);
+}
+
+namespace {
 
 int collective(Coll coll, const rc_buf* bufs, void* stream, void* const* recv_list = nullptr) {
     std::lock_guard<std::mutex> lock(g_mu);
@@ -847,6 +866,15 @@ int rc_all_reduce_params(const int* num_params, const rc_param* const* params, v
     if (e.code) return report(e);
     if (g_s.cfg.validate_only) return ok();
     return report(launch_batch(cks, stream));
+}
+
+int rc_session_info(int* num_ranks, int* device) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (g_s.mode == Mode::None)
+        return report(Error{RC_ERR_NOT_REGISTERED, "no session: call rc_register first"});
+    if (num_ranks) *num_ranks = g_s.nranks;
+    if (device) *device = g_s.cfg.validate_only ? g_s.cfg.device : g_s.dev.device;
+    return ok();
 }
 
 int rc_finish(void) {
