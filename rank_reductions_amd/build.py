@@ -1,4 +1,5 @@
-"""Builds librankred.so in-tree: host-only C++ with g++, HIP with hipcc for gfx950.
+"""Builds librankred.so in-tree: host-only C++ with g++, HIP with hipcc for gfx950;
+and _rows.so, the Python module that marshals the row exchanges' tensors.
 
     python -m rank_reductions_amd.build        # or: python rank_reductions_amd/build.py
 
@@ -19,6 +20,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = PKG / "librankred.so"
+BINDING = PKG / "_rows.so"
 
 HOST_SOURCES = ["session.cpp", "validate.cpp", "plan.cpp", "rows.cpp"]
 # (source, object, defines): the fold and batch kernels are built once per
@@ -69,8 +71,28 @@ def _run(cmd, verbose):
     return res
 
 
+def _binding_jobs(inc, cxx):
+    """Compile and link commands of _rows.so, against the installed torch."""
+    import sysconfig
+
+    import torch
+
+    home = Path(torch.__file__).resolve().parent
+    obj = BUILD / "binding.o"
+    system = [home / "include", home / "include" / "torch" / "csrc" / "api" / "include",
+              sysconfig.get_path("include"), Path(_hipcc()).resolve().parent.parent / "include"]
+    compile_ = [cxx, *HOST_FLAGS, "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+                *(a for d in system for a in ("-isystem", d)), "-c", CSRC / "binding.cpp", "-o", obj]
+    tmp = BINDING.with_suffix(".so.tmp")
+    # librankred.so from the same folder; torch's libraries are loaded by then
+    link = [cxx, "-shared", "-fPIC", obj, f"-L{PKG}", f"-l:{LIB.name}", "-Wl,-rpath,$ORIGIN",
+            f"-L{home / 'lib'}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-o", tmp]
+    return compile_, link, tmp
+
+
 def build(verbose=False, extra_hip_flags=()):
-    """Compile every source and link librankred.so.  Always recompiles."""
+    """Compile every source, link librankred.so and _rows.so.  Always recompiles."""
     BUILD.mkdir(exist_ok=True)
     hipcc = _hipcc()
     cxx = os.environ.get("CXX", "g++")
@@ -86,6 +108,8 @@ def build(verbose=False, extra_hip_flags=()):
         dflags = [f"-D{k}={v}" for k, v in defines.items()]
         jobs.append([hipcc, *HIP_FLAGS, *extra_hip_flags, *dflags, *inc, "-c", CSRC / src, "-o", obj])
         objs.append(obj)
+    binding, link_binding, binding_tmp = _binding_jobs(inc, cxx)
+    jobs.append(binding)
     # the largest objects first, so the pool ends together
     jobs.sort(key=lambda c: 0 if "kernels_fold.hip" in str(c) or "rows_route.hip" in str(c) else 1)
     with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 8, 16)) as ex:
@@ -93,6 +117,8 @@ def build(verbose=False, extra_hip_flags=()):
     tmp = LIB.with_suffix(".so.tmp")
     _run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)
+    _run(link_binding, verbose)
+    os.replace(binding_tmp, BINDING)
     return LIB
 
 
