@@ -174,6 +174,15 @@ void* stream_on(const Session& s, const at::Device& device, const char* what) {
 
 at::TensorOptions options(ScalarType type, const at::Device& device) { return at::TensorOptions().dtype(type).device(device); }
 
+// A dense tensor within another's storage, from element `at` on: what
+// as_strided gives, without a pass through the dispatcher for each.
+Tensor part_of(const Tensor& all, int64_t at, at::IntArrayRef sizes) {
+    auto impl = c10::make_intrusive<at::TensorImpl>(at::Storage(all.storage()), all.key_set(), all.dtype());
+    impl->set_storage_offset(at);
+    impl->set_sizes_contiguous(sizes);
+    return Tensor(std::move(impl));
+}
+
 // ---------------------------------------------------------------- arguments
 
 long long to_int(PyObject* o) {
@@ -420,11 +429,11 @@ PyObject* dispatch_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
         counts.make(R);
         int64_t at_ = 0, one[RC_MAX_RANKS];
         for (int r = 0; r < R; ++r) {
-            p.slots.made[r] = all.as_strided({p.tokens[r], p.K}, {p.K, 1}, at_);
+            p.slots.made[r] = part_of(all, at_, {p.tokens[r], p.K});
             at_ += p.tokens[r] * p.K;
         }
-        for (int r = 0; r < R; ++r, at_ += per + 1) offsets.made[r] = all.as_strided({per + 1}, {1}, at_);
-        for (int r = 0; r < R; ++r, at_ += per) counts.made[r] = all.as_strided({per}, {1}, at_);
+        for (int r = 0; r < R; ++r, at_ += per + 1) offsets.made[r] = part_of(all, at_, {per + 1});
+        for (int r = 0; r < R; ++r, at_ += per) counts.made[r] = part_of(all, at_, {per});
         p.slots.expect(ScalarType::Int, dev, p.tokens, p.K, what);
         for (int r = 0; r < R; ++r) one[r] = per + 1;
         offsets.expect(ScalarType::Int, dev, one, -1, what);

@@ -49,7 +49,7 @@ struct RouteArgs {
 // ---------------------------------------------------------------- counting sort
 // Entries per workgroup of the sort kernels, and the most digits one pass
 // tells apart.
-constexpr int kSortBlock = 4096;
+constexpr int kSortBlock = 1024;
 constexpr int kSortBins = 1024;
 
 // One pass of a stable counting sort over `spans.total()` entries cut into
@@ -68,7 +68,8 @@ struct SortPass {
     int32_t shift;
     int32_t bits;
     int32_t bins;          // digits in use
-    int32_t* hist;         // [blocks][bins], then bins totals
+    int32_t* hist;         // [blocks][bins] counts; scanned: sums of the blocks before, then bins totals
+    int32_t scanned;
 };
 
 struct PlanArgs {
@@ -124,13 +125,14 @@ struct EmbeddingGradArgs {
     RankSpans tokens;
     const int32_t* keys;   // sorted ids; vocab for those outside the table
     const int32_t* vals;   // position in the sequence of all ranks' tokens
-    float* partial;        // [windows][2][width]
+    float* partial;        // [blocks of kPiece entries][2][width]
     int64_t vocab;
     int64_t shard;
     int64_t width;
     float scale;
     int32_t accumulate;
-    int32_t windows;       // windows of kPiece sorted entries
+    int32_t window;        // sorted entries per workgroup, a power of two up to kPiece
+    int32_t windows;
     int32_t fill_groups;   // groups of 64 table rows to be cleared where no id names them
     int32_t chunks;        // column pieces of a row, one workgroup each
 };

@@ -5,10 +5,10 @@
 //
 // Gradient: dW[v] = scale * sum of dy over the tokens whose id is v.  The ids
 // of all ranks are sorted (stably, with their positions), so that the rows of
-// one id lie side by side in the list.  The list is cut into windows of
+// one id lie side by side in the list.  The list is cut into windows of up to
 // kPiece entries, one workgroup each (and per piece of the columns): it sums
 // the ids that begin in its window, running on past the window's end, so no
-// workgroup takes more than two windows' entries.  An id with more than
+// workgroup takes more than a window and a piece.  An id with more than
 // kPiece entries is cut into pieces of kPiece from its first entry on; the
 // workgroup in whose window a piece begins leaves its sum in the workspace
 // and a second kernel joins them.  What an id's sum adds, and in what order,
@@ -77,26 +77,28 @@ template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortPass s) {
     __shared__ int32_t count[kSortWaves * kSortBins];
     __shared__ int32_t start[kSortBins];
+    __shared__ int32_t before[kSortBins];
     __shared__ int32_t carry[kSortWaves];
     const int lane = lane_id(), wave = threadIdx.x / kWave;
-    const int32_t* total = s.hist + (int64_t)s.blocks.total() * s.bins;
-    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) {
-        start[d] = total[d];
-        for (int w = 0; w < kSortWaves; ++w) count[w * kSortBins + d] = 0;
-    }
-    __syncthreads();
-    exclusive_sum<kSortThreads>(start, s.bins, carry);
-    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) start[d] += s.hist[(int64_t)blockIdx.x * s.bins + d];
     int32_t block;
     const int rank = rank_of(s.blocks, blockIdx.x, &block);
     const int at = wave * kStrips * kWave + lane;
     const int32_t ones = (1 << s.bits) - 1;
     int32_t key[kStrips], val[kStrips];
 #pragma unroll
-    for (int k = 0; k < kStrips; ++k) {
+    for (int k = 0; k < kStrips; ++k)
         if (!sort_entry<FIRST>(s, rank, block, at + k * kWave, &key[k], &val[k])) key[k] = -1;
-        else atomicAdd(&count[wave * kSortBins + ((key[k] >> s.shift) & ones)], 1);
+    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) {
+        before[d] = start[d] = 0;
+        for (int w = 0; w < kSortWaves; ++w) count[w * kSortBins + d] = 0;
     }
+    __syncthreads();
+    block_sums(s, before, start);
+    exclusive_sum<kSortThreads>(start, s.bins, carry);
+    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) start[d] += before[d];
+#pragma unroll
+    for (int k = 0; k < kStrips; ++k)
+        if (key[k] >= 0) atomicAdd(&count[wave * kSortBins + ((key[k] >> s.shift) & ones)], 1);
     wave_starts<kSortWaves>(count, start, s.bins);
 #pragma unroll
     for (int k = 0; k < kStrips; ++k) {
@@ -185,6 +187,7 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void sort_small_kernel(SmallSor
 
 constexpr int kSumThreads = 256;
 constexpr int kAhead = 4;  // rows of dy in flight per lane
+constexpr int64_t kSumGroups = 2048;  // summing workgroups that keep the GPU busy
 
 // First of the sorted keys in [lo, hi) that is not below `key`.
 __device__ __forceinline__ int32_t lower_bound(const int32_t* keys, int32_t lo, int32_t hi, int64_t key) {
@@ -232,7 +235,7 @@ __device__ __forceinline__ void finish_row(const EmbeddingGradArgs& a, int64_t v
 template <class T, class G>
 __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGradArgs a) {
     using E = typename T::E;
-    __shared__ int32_t keys[3 * kPiece];  // of the positions p0 - 1 .. p0 + 2 kPiece
+    __shared__ int32_t keys[2 * kPiece + 2];  // of the positions p0 - 1 .. p0 + window + kPiece
     __shared__ const E* rows[2 * kPiece];
     const int lane = lane_id();
     const int32_t n = a.tokens.total();
@@ -257,11 +260,12 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
         }
         return;
     }
-    const int32_t p0 = (int32_t)(group * kPiece);
-    for (int t = threadIdx.x; t < 2 * kPiece + 2; t += kSumThreads) {
+    const int W = a.window;
+    const int32_t p0 = (int32_t)(group * W);
+    for (int t = threadIdx.x; t < W + kPiece + 2; t += kSumThreads) {
         const int64_t p = (int64_t)p0 - 1 + t;
         keys[t] = p >= 0 && p < n ? a.keys[p] : -1;
-        if (t >= 1 && t <= 2 * kPiece) {
+        if (t >= 1 && t <= W + kPiece) {
             const E* src = nullptr;
             if (p < n) {
                 int32_t token;
@@ -272,24 +276,26 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
         }
     }
     __syncthreads();
-    // positions from here on count from p0; key(i) of position i
+    // positions from here on count from p0; key[i] is position i's
     const int32_t* key = keys + 1;
     const int32_t none = (int32_t)a.vocab;  // ids that name no row sort last
-    const bool real = key[lane] >= 0 && key[lane] < none;
-    const uint64_t begins = __ballot(real && key[lane] != key[lane - 1]);
-    const uint64_t longs = __ballot(real && key[lane] != key[lane - 1] && key[lane] == key[lane + kPiece]);
-    const int valid = __popcll(__ballot(real)) + __popcll(__ballot(key[lane + kPiece] >= 0 && key[lane + kPiece] < none));
+    const int32_t mine = lane < W ? key[lane] : -1, after = key[W + lane];
+    const bool real = mine >= 0 && mine < none;
+    const bool first = real && mine != key[lane - 1];
+    const uint64_t begins = __ballot(first);
+    const uint64_t longs = __ballot(first && mine == key[lane + kPiece]);
+    const int valid = __popcll(__ballot(real)) + __popcll(__ballot(after >= 0 && after < none));
     // first position past the window that is not of the window's last id
-    const uint64_t other = __ballot(key[lane + kPiece] != key[kPiece - 1]);
-    const int last_end = min(valid, kPiece + (other ? (int)__builtin_ctzll(other) : kPiece));
+    const uint64_t other = __ballot(after != key[W - 1]);
+    const int last_end = min(valid, W + (other ? (int)__builtin_ctzll(other) : kPiece));
     int begin = begins ? (int)__builtin_ctzll(begins) : 2 * kPiece;
     int carried = 0;  // positions below it belong to a piece of an id that began earlier
     if (key[0] >= 0 && key[0] < none && key[0] == key[-1]) {
         const int32_t s = lower_bound(a.keys, 0, p0, key[0]);
         if (s + (int64_t)kPiece < n && a.keys[s + kPiece] == key[0]) {
             const int ps = (int)(((int64_t)p0 - s + kPiece - 1) / kPiece * kPiece + s - p0);
-            const int end = begins ? begin : last_end;  // of the id, or two windows on
-            if (ps < kPiece && ps < end) {
+            const int end = begins ? begin : last_end;  // of the id, or past the piece
+            if (ps < W && ps < end) {
                 carried = min(ps + kPiece, end);
                 begin = ps;
             }
@@ -301,6 +307,9 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
     else if (begins) end = last_end;
     else end = carried;
     if (begin >= end) return;
+    // where the sums of the carried piece and of the long id's first go
+    float* const carried_out = a.partial + 2 * (int64_t)((p0 + begin) / kPiece) * a.width;
+    float* const hot_out = a.partial + (2 * (int64_t)((p0 + hot) / kPiece) + 1) * a.width;
 
     const int64_t col = ((int64_t)blockIdx.z * kSumThreads + threadIdx.x) * T::n;
     const int rem = (int)max((int64_t)0, min((int64_t)T::n, a.width - col));
@@ -328,7 +337,7 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
             // an id's last entry, or a piece's
             if (j + 1 == end || j + 1 == carried || key[j + 1] != key[j]) {
                 if (j < carried || j >= hot) {
-                    float* out = a.partial + (2 * group + (j < carried ? 0 : 1)) * a.width + col;
+                    float* out = (j < carried ? carried_out : hot_out) + col;
 #pragma unroll
                     for (int i = 0; i < T::n; ++i)
                         if (i < rem) out[i] = acc[i];
@@ -342,58 +351,59 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
     }
 }
 
-// Joins the pieces of the long id that begins in the window, if there is one:
-// runs of kPiece pieces, one wave each, added in order.
-constexpr int kJoinWaves = 4;
-constexpr int kJoinCols = kWave * 4;
+// Joins the pieces of the long id that begins in the block of kPiece entries,
+// if there is one: runs of kPiece pieces, added in order.  Piece i is there if
+// the entry kPiece i past the id's first is still the id's; it lies i blocks on.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinCols = kJoinThreads * 4;
+constexpr int kJoinAhead = 16;
 template <class G>
-__global__ __launch_bounds__(kJoinWaves* kWave) void embedding_join_kernel(EmbeddingGradArgs a) {
-    __shared__ float run[kJoinWaves][kJoinCols];
-    const int lane = lane_id(), wave = threadIdx.x / kWave;
+__global__ __launch_bounds__(kJoinThreads) void embedding_join_kernel(EmbeddingGradArgs a) {
+    const int lane = lane_id();
     const int32_t n = a.tokens.total();
-    const int64_t group = group_index();
-    if (group >= a.windows) return;
-    const int32_t p0 = (int32_t)(group * kPiece);
-    const int64_t p = (int64_t)p0 + lane;
+    const int64_t block = group_index(), p = block * kPiece + lane;
     const int32_t key = p < n ? a.keys[p] : -1;
-    const bool first = key >= 0 && key < a.vocab && (p == 0 || a.keys[p - 1] != key);
-    const uint64_t longs = __ballot(first && p + kPiece < n && a.keys[p + kPiece] == key);
+    const int32_t before = p > 0 && p < n ? a.keys[p - 1] : -1;
+    const int32_t past = p + kPiece < n ? a.keys[p + kPiece] : -1;
+    const uint64_t longs = __ballot(key >= 0 && key < a.vocab && before != key && past == key);
     if (!longs) return;
-    const int32_t s = p0 + (int)__builtin_ctzll(longs);
-    const int32_t id = a.keys[s];
-    const int32_t stop = lower_bound(a.keys, s, n, (int64_t)id + 1);
-    const int64_t pieces = ((int64_t)stop - s + kPiece - 1) / kPiece;
-    const int64_t runs = (pieces + kPiece - 1) / kPiece;
-    const int64_t col = (int64_t)blockIdx.z * kJoinCols + lane * 4;
+    const int at = (int)__builtin_ctzll(longs);
+    const int32_t id = __shfl(key, at);
+    const int64_t s = block * kPiece + at;
+    const int64_t col = (int64_t)blockIdx.z * kJoinCols + threadIdx.x * 4;
     const int rem = (int)max((int64_t)0, min((int64_t)4, a.width - col));
     float total[4] = {};
-    for (int64_t r0 = 0; r0 < runs; r0 += kJoinWaves) {
+    for (int64_t base = 0;; base += kPiece) {
+        const int64_t q = s + (base + lane) * kPiece;
+        const int pieces = __popcll(__ballot(q < n && a.keys[q] == id));  // of this run
+        // the first piece of all is the second kind of its block
+        const float* src = a.partial + 2 * (block + base) * a.width + col;
         float sum[4] = {};
-        const int64_t lo = (r0 + wave) * kPiece, hi = min(lo + kPiece, pieces);
-#pragma unroll 8
-        for (int64_t i = lo; i < hi; ++i) {
-            // the first piece is the second kind of the window it begins in
-            const float* src = a.partial + (2 * (group + i) + (i == 0)) * a.width + col;
-            if (rem == 4) {
-                float f[4];
-                F32::unpack(load16<F32>(src), f);
+        for (int i0 = 0; i0 < pieces; i0 += kJoinAhead) {
+            float f[kJoinAhead][4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) sum[c] += f[c];
-            } else {
+            for (int u = 0; u < kJoinAhead; ++u) {
+                if (i0 + u < pieces) {
+                    const float* row = src + (2 * (int64_t)(i0 + u) + (base + i0 + u == 0)) * a.width;
+                    if (rem == 4) F32::unpack(load16<F32>(row), f[u]);
+                    else
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c < rem) sum[c] += src[c];
+                        for (int c = 0; c < 4; ++c) f[u][c] = c < rem ? row[c] : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinAhead; ++u) {
+                if (i0 + u < pieces) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sum[c] += f[u][c];
+                }
             }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) run[wave][lane * 4 + c] = sum[c];
-        __syncthreads();
-        for (int w = 0; w < kJoinWaves && r0 + w < runs; ++w)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) total[c] += run[w][lane * 4 + c];
-        __syncthreads();
+        for (int c = 0; c < 4; ++c) total[c] += sum[c];
+        if (pieces < kPiece) break;
     }
-    if (wave != 0 || rem == 0) return;
+    if (rem == 0) return;
     typename G::E* row = table_row<G>(a, id) + col;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -449,13 +459,18 @@ int run_embedding(EmbeddingArgs a, hipStream_t s) {
 
 template <class T, class G>
 int run_sum(EmbeddingGradArgs a, hipStream_t s) {
-    const int64_t cols = kSumThreads * T::n;
+    const int64_t cols = kSumThreads * T::n, chunks = (a.width + cols - 1) / cols, n = a.tokens.total();
+    // shorter windows where whole pieces would leave the GPU idle
+    a.window = kPiece;
+    while (a.window > 4 && n / a.window * chunks < kSumGroups) a.window /= 2;
+    a.windows = (int32_t)((n + a.window - 1) / a.window);
     const int64_t groups = (int64_t)a.windows + a.fill_groups;
     if (groups)
-        hipLaunchKernelGGL((embedding_grad_kernel<T, G>), grid_of(groups, (a.width + cols - 1) / cols), dim3(kSumThreads), 0, s, a);
+        hipLaunchKernelGGL((embedding_grad_kernel<T, G>), grid_of(groups, chunks), dim3(kSumThreads), 0, s, a);
     if (a.tokens.total() > kPiece)
-        hipLaunchKernelGGL(embedding_join_kernel<G>, grid_of(a.windows, (a.width + kJoinCols - 1) / kJoinCols),
-                           dim3(kJoinWaves * kWave), 0, s, a);
+        hipLaunchKernelGGL(embedding_join_kernel<G>,
+                           grid_of(((int64_t)a.tokens.total() + kPiece - 1) / kPiece, (a.width + kJoinCols - 1) / kJoinCols),
+                           dim3(kJoinThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -511,10 +526,8 @@ int launch_embedding_grad(EmbeddingGradArgs a, SortPass sort, int dtype, int gra
             }
             sort.blocks = sort_blocks(sort.spans);
             const int32_t blocks = sort.blocks.total();
-            if (p == 0) hipLaunchKernelGGL(sort_count_kernel<true>, dim3(blocks), dim3(kSortThreads), 0, s, sort);
-            else hipLaunchKernelGGL(sort_count_kernel<false>, dim3(blocks), dim3(kSortThreads), 0, s, sort);
-            hipLaunchKernelGGL(sort_scan_kernel, dim3((sort.bins + kWave - 1) / kWave), dim3(kScanWaves * kWave), 0, s,
-                               sort.hist, blocks, sort.bins);
+            if (p == 0) launch_counts<true>(sort, s);
+            else launch_counts<false>(sort, s);
             if (p == 0) hipLaunchKernelGGL(sort_place_kernel<true>, dim3(blocks), dim3(kSortThreads), 0, s, sort);
             else hipLaunchKernelGGL(sort_place_kernel<false>, dim3(blocks), dim3(kSortThreads), 0, s, sort);
         }
@@ -522,7 +535,6 @@ int launch_embedding_grad(EmbeddingGradArgs a, SortPass sort, int dtype, int gra
     a.keys = keys[0];
     a.vals = vals[0];
     a.partial = reinterpret_cast<float*>(ws + l.partial);
-    a.windows = (int32_t)(((int64_t)n + kPiece - 1) / kPiece);
     a.fill_groups = a.accumulate ? 0 : (int32_t)((a.vocab + kWave - 1) / kWave);
     if (dtype == RC_F32) return run_sum<F32, F32>(a, s);
     if (dtype == RC_F16) return grad_dtype == RC_F32 ? run_sum<F16, F32>(a, s) : run_sum<F16, F16>(a, s);

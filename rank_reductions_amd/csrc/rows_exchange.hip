@@ -26,25 +26,15 @@ __device__ __forceinline__ void write_slot(const PlanArgs& a, int rank, int32_t 
     a.slots[rank][i] = fits ? slot : -1;
 }
 
-// Places of the entries of one block, with the blocks' starts in hist.
+// Places of the entries of one block.
 __global__ __launch_bounds__(kSortThreads) void plan_place_kernel(PlanArgs a) {
     __shared__ int32_t count[kSortWaves * kSortBins];
     __shared__ int32_t start[kSortBins];
+    __shared__ int32_t total[kSortBins];
     __shared__ int32_t base[kSortBins];
     __shared__ int32_t carry[kSortWaves];
     const SortPass& s = a.sort;
     const int lane = lane_id(), wave = threadIdx.x / kWave;
-    const int32_t* total = s.hist + (int64_t)s.blocks.total() * s.bins;
-    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) {
-        start[d] = total[d];
-        for (int w = 0; w < kSortWaves; ++w) count[w * kSortBins + d] = 0;
-    }
-    __syncthreads();
-    exclusive_sum<kSortThreads>(start, s.bins, carry);
-    for (int e = threadIdx.x; e < s.bins; e += kSortThreads) {
-        base[e] = start[e] - start[e / a.per_rank * a.per_rank] + s.hist[(int64_t)blockIdx.x * s.bins + e];
-        if (blockIdx.x == 0) write_offsets(a, start, e, total[e]);
-    }
     int32_t block;
     const int rank = rank_of(s.blocks, blockIdx.x, &block);
     const int at = wave * kStrips * kWave + lane;
@@ -52,10 +42,24 @@ __global__ __launch_bounds__(kSortThreads) void plan_place_kernel(PlanArgs a) {
 #pragma unroll
     for (int k = 0; k < kStrips; ++k) {
         int32_t val;
-        const bool in = sort_entry<true>(s, rank, block, at + k * kWave, &key[k], &val);
-        if (!in) key[k] = -1;
-        else if (key[k] < a.num_experts) atomicAdd(&count[wave * kSortBins + key[k]], 1);
+        if (!sort_entry<true>(s, rank, block, at + k * kWave, &key[k], &val)) key[k] = -1;
     }
+    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) {
+        base[d] = total[d] = 0;
+        for (int w = 0; w < kSortWaves; ++w) count[w * kSortBins + d] = 0;
+    }
+    __syncthreads();
+    block_sums(s, base, total);
+    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) start[d] = total[d];
+    __syncthreads();
+    exclusive_sum<kSortThreads>(start, s.bins, carry);
+    for (int e = threadIdx.x; e < s.bins; e += kSortThreads) {
+        base[e] += start[e] - start[e / a.per_rank * a.per_rank];
+        if (blockIdx.x == 0) write_offsets(a, start, e, total[e]);
+    }
+#pragma unroll
+    for (int k = 0; k < kStrips; ++k)
+        if (key[k] >= 0 && key[k] < a.num_experts) atomicAdd(&count[wave * kSortBins + key[k]], 1);
     wave_starts<kSortWaves>(count, base, s.bins);
 #pragma unroll
     for (int k = 0; k < kStrips; ++k) {
@@ -65,9 +69,10 @@ __global__ __launch_bounds__(kSortThreads) void plan_place_kernel(PlanArgs a) {
     }
 }
 
-// The whole plan in one workgroup, for few entries.
+// The whole plan in one workgroup, for few entries: one launch instead of two.
 constexpr int kSmallWaves = 8;
-constexpr int kSmallEntries = 8192;
+constexpr int kSmallStrips = 8;
+constexpr int kSmallEntries = kSmallWaves * kSmallStrips * kWave;
 __global__ __launch_bounds__(kSmallWaves* kWave) void plan_small_kernel(PlanArgs a) {
     __shared__ int32_t count[kSmallWaves * kSortBins];
     __shared__ int32_t start[kSortBins];
@@ -78,17 +83,23 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void plan_small_kernel(PlanArgs
     const int lane = lane_id(), wave = threadIdx.x / kWave;
     const int32_t n = s.spans.total();
     const int strips = (n + kThreads - 1) / kThreads;  // of each wave
+    const int32_t at = wave * strips * kWave + lane;
+    int32_t key[kSmallStrips], index[kSmallStrips], rank[kSmallStrips];
+#pragma unroll
+    for (int k = 0; k < kSmallStrips; ++k) {
+        key[k] = -1;
+        index[k] = rank[k] = 0;
+        if (k < strips && at + k * kWave < n) {
+            rank[k] = rank_of(s.spans, at + k * kWave, &index[k]);
+            key[k] = first_key(s, rank[k], index[k]);
+        }
+    }
     for (int d = threadIdx.x; d < s.bins; d += kThreads)
         for (int w = 0; w < kSmallWaves; ++w) count[w * kSortBins + d] = 0;
     __syncthreads();
-    const int32_t at = wave * strips * kWave + lane;
-    for (int k = 0; k < strips; ++k) {
-        int32_t i;
-        const bool in = at + k * kWave < n;
-        const int rank = rank_of(s.spans, in ? at + k * kWave : 0, &i);
-        const int32_t key = in ? first_key(s, rank, i) : a.num_experts;
-        if (key < a.num_experts) atomicAdd(&count[wave * kSortBins + key], 1);
-    }
+#pragma unroll
+    for (int k = 0; k < kSmallStrips; ++k)
+        if (key[k] >= 0 && key[k] < a.num_experts) atomicAdd(&count[wave * kSortBins + key[k]], 1);
     __syncthreads();
     for (int d = threadIdx.x; d < s.bins; d += kThreads) {
         int32_t sum = 0;
@@ -97,26 +108,62 @@ __global__ __launch_bounds__(kSmallWaves* kWave) void plan_small_kernel(PlanArgs
     }
     __syncthreads();
     exclusive_sum<kThreads>(start, s.bins, carry);
-    for (int e = threadIdx.x; e < s.bins; e += kThreads) write_offsets(a, start, e, total[e]);
-    // total becomes the start of each expert within its rank
+    for (int e = threadIdx.x; e < s.bins; e += kThreads) {
+        write_offsets(a, start, e, total[e]);
+        // the start of each expert within its rank, then of each wave's part
+        int32_t run = start[e] - start[e / a.per_rank * a.per_rank];
+        for (int w = 0; w < kSmallWaves; ++w) {
+            const int32_t c = count[w * kSortBins + e];
+            count[w * kSortBins + e] = run;
+            run += c;
+        }
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e < s.bins; e += kThreads) total[e] = start[e] - start[e / a.per_rank * a.per_rank];
-    wave_starts<kSmallWaves>(count, total, s.bins);
-    for (int k = 0; k < strips; ++k) {
-        int32_t i;
-        const bool in = at + k * kWave < n;
-        const int rank = rank_of(s.spans, in ? at + k * kWave : 0, &i);
-        const int32_t key = in ? first_key(s, rank, i) : a.num_experts;
-        const bool has = key < a.num_experts;
-        const int32_t slot = strip_rank(key, s.bits, has, &count[wave * kSortBins]);
-        if (in) write_slot(a, rank, i, has, key, slot);
+#pragma unroll
+    for (int k = 0; k < kSmallStrips; ++k) {
+        if (k < strips) {  // alike in all lanes
+            const bool has = key[k] >= 0 && key[k] < a.num_experts;
+            const int32_t slot = strip_rank(key[k], s.bits, has, &count[wave * kSortBins]);
+            if (key[k] >= 0) write_slot(a, rank[k], index[k], has, key[k], slot);
+        }
     }
 }
 
 // ---------------------------------------------------------------- row moves
 
 constexpr int kRowThreads = 256;
-constexpr int kRowVecs = 2;  // 16-byte vectors per lane and piece
+
+// The ranks' tables of a launch, one entry per lane (lane l holds rank
+// l mod kMaxRanks): the argument block is read in one round of independent
+// loads, and entries picked with lane moves, where indexing it by a rank that
+// was itself just loaded takes a dependent trip to memory each time.
+struct Tables {
+    const int32_t* experts;
+    const int32_t* slots;
+    const void* near;   // the ranks' buffers by token
+    const void* far;    // the ranks' row buffers
+    int64_t capacity;
+    int32_t first;      // the rank's first token
+};
+
+__device__ __forceinline__ Tables tables_of(const ExchangeArgs& a, const void* const* near, const void* const* far) {
+    const int r = lane_id() & (kMaxRanks - 1);
+    return {a.experts[r], a.slots[r], near[r], far[r], a.capacity[r], a.tokens.first[r]};
+}
+
+template <class P>
+__device__ __forceinline__ P* lane_ptr(P* p, int lane) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane), hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+    return reinterpret_cast<P*>((uint64_t)hi << 32 | lo);
+}
+
+// The rank of token n of all (alike in all lanes), and the token within it.
+__device__ __forceinline__ int rank_by_lane(const Tables& t, int nranks, int32_t n, int32_t* token) {
+    const int rank = __popcll(__ballot(lane_id() < nranks && t.first <= n)) - 1;
+    *token = n - __builtin_amdgcn_readlane(t.first, rank);
+    return rank;
+}
 
 // One wave's piece of one token's row.
 struct Piece {
@@ -125,56 +172,66 @@ struct Piece {
     int64_t col;     // first element of the lane's first vector
 };
 
-template <class T>
-__device__ __forceinline__ bool piece_of(const RankSpans& tokens, int32_t chunks, Piece* p) {
+template <class T, int U>
+__device__ __forceinline__ bool piece_of(const ExchangeArgs& a, const Tables& t, Piece* p) {
     const int64_t item = group_index() * (kRowThreads / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    if (item >= (int64_t)tokens.total() * chunks) return false;
-    const int32_t token = (int32_t)(item / chunks);
-    p->rank = rank_of(tokens, token, &p->token);
-    p->col = (item - (int64_t)token * chunks) * (kWave * T::n * kRowVecs) + lane_id() * T::n;
+    if (item >= (int64_t)a.tokens.total() * a.chunks) return false;
+    const int32_t n = (int32_t)(item / a.chunks);
+    p->rank = rank_by_lane(t, a.tokens.nranks, n, &p->token);
+    p->col = (item - (int64_t)n * a.chunks) * (kWave * T::n * U) + lane_id() * T::n;
     return true;
 }
 
-// Lane k's choice k of the token: the address of its row, or NULL.  `base` is
-// the table of the experts' ranks' row buffers.
+// Lane k's choice k of the token: the rank of its expert, or -1, and its row there.
+struct Choice {
+    int rank;
+    int32_t slot;
+};
+__device__ __forceinline__ Choice choice_of(const ExchangeArgs& a, const Tables& t, int rank, int32_t token) {
+    Choice c{-1, 0};
+    int32_t expert = -1;
+    const int lane = lane_id();
+    const int32_t* slots = lane_ptr(t.slots, rank);
+    const int32_t* experts = lane_ptr(t.experts, rank);
+    if (lane < a.top_k) {
+        c.slot = slots[(int64_t)token * a.top_k + lane];
+        expert = experts[(int64_t)token * a.top_k + lane];
+    }
+    const bool has = expert >= 0 && expert < a.num_experts && c.slot >= 0;
+    const int d = has ? (int)((uint32_t)expert / (uint32_t)a.per_rank) : 0;
+    const int64_t capacity = __shfl(t.capacity, d);
+    if (has && c.slot < capacity) c.rank = d;
+    return c;
+}
+// The address of the row in the buffers that the lanes hold, or NULL.
 template <class E>
-__device__ __forceinline__ E* place_of(const ExchangeArgs& a, const void* const* base, int rank, int32_t token, int k) {
-    const int32_t slot = a.slots[rank][(int64_t)token * a.top_k + k];
-    const int32_t expert = a.experts[rank][(int64_t)token * a.top_k + k];
-    if (expert < 0 || expert >= a.num_experts || slot < 0) return nullptr;
-    const int d = expert / a.per_rank;
-    if (slot >= a.capacity[d]) return nullptr;
-    return static_cast<E*>(const_cast<void*>(base[d])) + slot * a.width;
+__device__ __forceinline__ E* row_at(const Choice& c, const void* buffers, int64_t width) {
+    const int d = c.rank < 0 ? 0 : c.rank;
+    const uint64_t base = __shfl(reinterpret_cast<unsigned long long>(buffers), d);
+    return c.rank < 0 ? nullptr : reinterpret_cast<E*>(base) + c.slot * width;
 }
 
-template <class E>
-__device__ __forceinline__ E* from_lane(E* p, int lane) {
-    const uint64_t v = reinterpret_cast<uint64_t>(p);
-    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane), hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
-    return reinterpret_cast<E*>((uint64_t)hi << 32 | lo);
-}
-
-template <class T>
+template <class T, int U>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(ExchangeArgs a) {
     using E = typename T::E;
+    const Tables t = tables_of(a, a.in, a.out);
     Piece p;
-    if (!piece_of<T>(a.tokens, a.chunks, &p)) return;
-    const int lane = lane_id();
-    E* mine = lane < a.top_k ? place_of<E>(a, a.out, p.rank, p.token, lane) : nullptr;
-    const E* src = static_cast<const E*>(a.in[p.rank]) + (int64_t)p.token * a.width;
-    u32x4 v[kRowVecs];
-    bool full[kRowVecs];
+    if (!piece_of<T, U>(a, t, &p)) return;
+    const E* src = static_cast<const E*>(lane_ptr(t.near, p.rank)) + (int64_t)p.token * a.width;
+    u32x4 v[U];
+    bool full[U];
 #pragma unroll
-    for (int u = 0; u < kRowVecs; ++u) {
+    for (int u = 0; u < U; ++u) {
         const int64_t col = p.col + u * (kWave * T::n);
         full[u] = col + T::n <= a.width;
         if (full[u]) v[u] = load16<T>(src + col);
     }
+    E* mine = row_at<E>(choice_of(a, t, p.rank, p.token), t.far, a.width);
     for (int k = 0; k < a.top_k; ++k) {
-        E* dst = from_lane(mine, k);
+        E* dst = lane_ptr(mine, k);
         if (!dst) continue;
 #pragma unroll
-        for (int u = 0; u < kRowVecs; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int64_t col = p.col + u * (kWave * T::n);
             if (full[u]) store16<T>(dst + col, v[u]);
             else
@@ -183,25 +240,30 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(ExchangeArgs a) {
     }
 }
 
-template <class T, int KP>
+template <class T, int KP, int U>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(ExchangeArgs a) {
     using E = typename T::E;
+    const Tables t = tables_of(a, a.out, a.in);
+    const float* weights = a.weights[lane_id() & (kMaxRanks - 1)];
     Piece p;
-    if (!piece_of<T>(a.tokens, a.chunks, &p)) return;
+    if (!piece_of<T, U>(a, t, &p)) return;
     const int lane = lane_id();
-    E* mine = lane < a.top_k ? place_of<E>(a, a.in, p.rank, p.token, lane) : nullptr;
     float weight = 1.0f;
-    if (a.weighted && lane < a.top_k) weight = a.weights[p.rank][(int64_t)p.token * a.top_k + lane];
+    if (a.weighted) {
+        const float* of_rank = lane_ptr(weights, p.rank);
+        if (lane < a.top_k) weight = of_rank[(int64_t)p.token * a.top_k + lane];
+    }
+    E* mine = row_at<E>(choice_of(a, t, p.rank, p.token), t.far, a.width);
     const E* src[KP];
     float w[KP];
 #pragma unroll
     for (int k = 0; k < KP; ++k) {
-        src[k] = from_lane(mine, k);
+        src[k] = lane_ptr(mine, k);
         w[k] = lane_value(weight, k);
     }
-    E* dst = static_cast<E*>(a.out[p.rank]) + (int64_t)p.token * a.width;
+    E* dst = static_cast<E*>(const_cast<void*>(lane_ptr(t.near, p.rank))) + (int64_t)p.token * a.width;
 #pragma unroll
-    for (int u = 0; u < kRowVecs; ++u) {
+    for (int u = 0; u < U; ++u) {
         const int64_t col = p.col + u * (kWave * T::n);
         if (col + T::n <= a.width) {
             u32x4 v[KP];
@@ -237,21 +299,26 @@ template <class T, int KP>
 __global__ __launch_bounds__(kGradThreads) void combine_grad_kernel(ExchangeArgs a) {
     using E = typename T::E;
     __shared__ float part[kGradThreads / kWave][KP];
+    const Tables t = tables_of(a, a.d_out, a.in);
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const float* weights = a.weights[lane & (kMaxRanks - 1)];
+    const void* d_rows = a.out[lane & (kMaxRanks - 1)];
     if (group_index() >= a.tokens.total()) return;
     int32_t token;
-    const int rank = rank_of(a.tokens, (int32_t)group_index(), &token);
-    const int lane = lane_id(), wave = threadIdx.x / kWave;
-    E* row = lane < a.top_k ? place_of<E>(a, a.in, rank, token, lane) : nullptr;
-    E* d_row = lane < a.top_k ? place_of<E>(a, a.out, rank, token, lane) : nullptr;
-    const float weight = lane < a.top_k ? a.weights[rank][(int64_t)token * a.top_k + lane] : 0.0f;
-    const E* src = static_cast<const E*>(a.d_out[rank]) + (int64_t)token * a.width;
+    const int rank = rank_by_lane(t, a.tokens.nranks, (int32_t)group_index(), &token);
+    const float* of_rank = lane_ptr(weights, rank);
+    const float weight = lane < a.top_k ? of_rank[(int64_t)token * a.top_k + lane] : 0.0f;
+    const Choice c = choice_of(a, t, rank, token);
+    E* row = row_at<E>(c, t.far, a.width);
+    E* d_row = row_at<E>(c, d_rows, a.width);
+    const E* src = static_cast<const E*>(lane_ptr(t.near, rank)) + (int64_t)token * a.width;
     const E* at[KP];
     E* to[KP];
     float w[KP], dot[KP] = {};
 #pragma unroll
     for (int k = 0; k < KP; ++k) {
-        at[k] = from_lane(row, k);
-        to[k] = from_lane(d_row, k);
+        at[k] = lane_ptr(row, k);
+        to[k] = lane_ptr(d_row, k);
         w[k] = lane_value(weight, k);
     }
     for (int64_t col = (int64_t)threadIdx.x * T::n; col < a.width; col += kGradThreads * T::n) {
@@ -276,13 +343,13 @@ __global__ __launch_bounds__(kGradThreads) void combine_grad_kernel(ExchangeArgs
                 store16<T>(to[k] + col, T::pack(g));
             }
         } else {
-            for (int64_t c = col; c < a.width; ++c) {
-                const float dy = T::load(src[c]);
+            for (int64_t i = col; i < a.width; ++i) {
+                const float dy = T::load(src[i]);
 #pragma unroll
                 for (int k = 0; k < KP; ++k) {
                     if (!at[k]) continue;
-                    dot[k] = __builtin_fmaf(dy, T::load(at[k][c]), dot[k]);
-                    to[k][c] = T::store(w[k] * dy);
+                    dot[k] = __builtin_fmaf(dy, T::load(at[k][i]), dot[k]);
+                    to[k][i] = T::store(w[k] * dy);
                 }
             }
         }
@@ -296,7 +363,7 @@ __global__ __launch_bounds__(kGradThreads) void combine_grad_kernel(ExchangeArgs
     __syncthreads();
     if (threadIdx.x < (unsigned)a.top_k) {
         float sum = 0.0f;
-        for (int w = 0; w < kGradThreads / kWave; ++w) sum += part[w][threadIdx.x];
+        for (int w2 = 0; w2 < kGradThreads / kWave; ++w2) sum += part[w2][threadIdx.x];
         a.d_weights[rank][(int64_t)token * a.top_k + threadIdx.x] = row ? sum : 0.0f;
     }
 }
@@ -309,29 +376,40 @@ int bits_of(int64_t values) {
     return b;
 }
 
+// 16-byte vectors per lane and piece: two, or one where that gives too few
+// waves to fill the GPU.
+constexpr int64_t kFillWaves = 4096;
 template <class T>
-int32_t chunks_of(int64_t width) {
-    const int64_t piece = kWave * T::n * kRowVecs;
-    return (int32_t)((width + piece - 1) / piece);
+int vectors_of(const ExchangeArgs& a) {
+    const int64_t two = kWave * T::n * 2;
+    return (a.width + two - 1) / two * a.tokens.total() >= kFillWaves ? 2 : 1;
+}
+template <class T>
+dim3 pieces_of(ExchangeArgs* a, int vectors) {
+    const int64_t piece = kWave * T::n * vectors, per = kRowThreads / kWave;
+    a->chunks = (int32_t)((a->width + piece - 1) / piece);
+    return grid_of(((int64_t)a->tokens.total() * a->chunks + per - 1) / per);
 }
 
 template <class T>
 int run_dispatch(ExchangeArgs a, hipStream_t s) {
-    a.chunks = chunks_of<T>(a.width);
-    const int64_t items = (int64_t)a.tokens.total() * a.chunks, per = kRowThreads / kWave;
-    hipLaunchKernelGGL(dispatch_kernel<T>, grid_of((items + per - 1) / per), dim3(kRowThreads), 0, s, a);
+    const int u = vectors_of<T>(a);
+    const dim3 grid = pieces_of<T>(&a, u);
+    hipLaunchKernelGGL((u == 2 ? dispatch_kernel<T, 2> : dispatch_kernel<T, 1>), grid, dim3(kRowThreads), 0, s, a);
     return last();
 }
 
-template <class T>
-int run_combine(ExchangeArgs a, hipStream_t s) {
-    a.chunks = chunks_of<T>(a.width);
-    const int64_t items = (int64_t)a.tokens.total() * a.chunks, per = kRowThreads / kWave;
-    const dim3 grid = grid_of((items + per - 1) / per);
-    auto fn = a.top_k <= 2 ? combine_kernel<T, 2> : a.top_k <= 4 ? combine_kernel<T, 4>
-            : a.top_k <= 8 ? combine_kernel<T, 8> : combine_kernel<T, 16>;
+template <class T, int U>
+int run_combine_u(ExchangeArgs a, hipStream_t s) {
+    const dim3 grid = pieces_of<T>(&a, U);
+    auto fn = a.top_k <= 2 ? combine_kernel<T, 2, U> : a.top_k <= 4 ? combine_kernel<T, 4, U>
+            : a.top_k <= 8 ? combine_kernel<T, 8, U> : combine_kernel<T, 16, U>;
     hipLaunchKernelGGL(fn, grid, dim3(kRowThreads), 0, s, a);
     return last();
+}
+template <class T>
+int run_combine(const ExchangeArgs& a, hipStream_t s) {
+    return vectors_of<T>(a) == 2 ? run_combine_u<T, 2>(a, s) : run_combine_u<T, 1>(a, s);
 }
 
 template <class T>
@@ -363,10 +441,8 @@ int launch_plan(PlanArgs a, void* workspace, void* stream) {
         return last();
     }
     p.blocks = sort_blocks(p.spans);
-    const int32_t blocks = p.blocks.total();
-    hipLaunchKernelGGL(sort_count_kernel<true>, dim3(blocks), dim3(kSortThreads), 0, s, p);
-    hipLaunchKernelGGL(sort_scan_kernel, dim3((p.bins + kWave - 1) / kWave), dim3(kScanWaves * kWave), 0, s, p.hist, blocks, p.bins);
-    hipLaunchKernelGGL(plan_place_kernel, dim3(blocks), dim3(kSortThreads), 0, s, a);
+    launch_counts<true>(p, s);
+    hipLaunchKernelGGL(plan_place_kernel, dim3(p.blocks.total()), dim3(kSortThreads), 0, s, a);
     return last();
 }
 

@@ -2,13 +2,20 @@
 // base of the dispatch plan (one pass over the experts) and of the embedding
 // gradient (one pass per digit of the token ids).
 //
-// Three launches: digit counts of each block of kSortBlock entries, an
-// exclusive sum over the blocks for each digit, and the places - an entry's
-// place is the start of its digit, plus the entries of that digit in earlier
-// blocks, earlier waves of the block, earlier strips of the wave and lower
-// lanes.  The lanes of a strip that hold the same digit find each other with
-// one ballot per digit bit.  Counts are integers, so atomics on them do not
-// touch the order, which is the entries' own.
+// Launches: digit counts of each block of kSortBlock entries, and the places -
+// an entry's place is the start of its digit, plus the entries of that digit
+// in earlier blocks, earlier waves of the block, earlier strips of the wave
+// and lower lanes.  The lanes of a strip that hold the same digit find each
+// other with one ballot per digit bit.  While blocks * digits stay under
+// kFusedCounts every block adds the blocks before it up by itself; a launch
+// between the two does so beyond.  Counts are integers, so atomics on them do
+// not touch the order, which is the entries' own.
+//
+// Bound by latency, not by bytes: a launch and two or three dependent loads
+// each.  Blocks of 1024 entries rather than 4096, all loads of a lane issued
+// together and no scan launch between took the plan of 131072 entries over 64
+// experts from 35.5 us to 16.6 us, the two passes over 65536 ids from 62 us to
+// 34 us.
 #pragma once
 
 #include "rows_impl.h"
@@ -70,19 +77,27 @@ __device__ __forceinline__ int32_t strip_rank(int digit, int bits, bool has, vol
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortPass s) {
     __shared__ int32_t count[kSortBins];
-    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) count[d] = 0;
-    __syncthreads();
     int32_t block;
     const int rank = rank_of(s.blocks, blockIdx.x, &block);
+    int32_t key[kStrips];
+#pragma unroll
     for (int k = 0; k < kStrips; ++k) {
-        int32_t key, val;
-        if (sort_entry<FIRST>(s, rank, block, k * kSortThreads + threadIdx.x, &key, &val) &&
-            !(s.drop && key == s.key_limit))
-            atomicAdd(&count[(key >> s.shift) & ((1 << s.bits) - 1)], 1);
+        int32_t val;
+        if (!sort_entry<FIRST>(s, rank, block, k * kSortThreads + threadIdx.x, &key[k], &val)) key[k] = -1;
     }
+    for (int d = threadIdx.x; d < s.bins; d += kSortThreads) count[d] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kStrips; ++k)
+        if (key[k] >= 0 && !(s.drop && key[k] == s.key_limit)) atomicAdd(&count[(key[k] >> s.shift) & ((1 << s.bits) - 1)], 1);
     __syncthreads();
     for (int d = threadIdx.x; d < s.bins; d += kSortThreads) s.hist[(int64_t)blockIdx.x * s.bins + d] = count[d];
 }
+
+// Up to this many counts, each block adds them up itself: at 16384 a lane
+// reads 64 of them, eight at a time, about 3 us; the launch between took 4.7.
+constexpr int64_t kFusedCounts = 16384;
+constexpr int kBatch = 8;
 
 // Exclusive sums over the blocks, for 64 digits per workgroup; the totals
 // follow the last block's row.
@@ -94,19 +109,70 @@ __global__ __launch_bounds__(kScanWaves* kWave) void sort_scan_kernel(int32_t* h
     const int per = (blocks + kScanWaves - 1) / kScanWaves;
     const int lo = min(wave * per, blocks), hi = min(lo + per, blocks);
     int32_t sum = 0;
-    if (d < bins)
+    if (d < bins) {
+#pragma unroll 8
         for (int b = lo; b < hi; ++b) sum += hist[(int64_t)b * bins + d];
+    }
     part[wave][lane] = sum;
     __syncthreads();
     if (d >= bins) return;
     int32_t run = 0;
     for (int w = 0; w < wave; ++w) run += part[w][lane];
-    for (int b = lo; b < hi; ++b) {
-        const int32_t c = hist[(int64_t)b * bins + d];
-        hist[(int64_t)b * bins + d] = run;
-        run += c;
+    for (int b0 = lo; b0 < hi; b0 += kBatch) {
+        int32_t c[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) c[u] = b0 + u < hi ? hist[(int64_t)(b0 + u) * bins + d] : 0;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (b0 + u < hi) hist[(int64_t)(b0 + u) * bins + d] = run;
+            run += c[u];
+        }
     }
     if (wave == kScanWaves - 1) hist[(int64_t)blocks * bins + d] = run;
+}
+
+// before[d]: entries of digit d in the blocks before this one; total[d]: in
+// all.  Both are cleared LDS; ends with a barrier.
+__device__ __forceinline__ void block_sums(const SortPass& s, int32_t* before, int32_t* total) {
+    const int32_t blocks = s.blocks.first[kMaxRanks];
+    const int32_t me = blockIdx.x;
+    if (s.scanned) {
+        for (int d = threadIdx.x; d < s.bins; d += kSortThreads) {
+            before[d] = s.hist[(int64_t)me * s.bins + d];
+            total[d] = s.hist[(int64_t)blocks * s.bins + d];
+        }
+        __syncthreads();
+        return;
+    }
+    // lanes past the digits take further blocks: thread t the digit t mod
+    // width, every `parts`-th block
+    int width = 1;
+    while (width < s.bins && width < kSortThreads) width *= 2;
+    const int parts = kSortThreads / width, part = threadIdx.x / width;
+    for (int d = threadIdx.x & (width - 1); d < s.bins; d += width) {
+        int32_t lower = 0, all = 0;
+        for (int b0 = part; b0 < blocks; b0 += parts * kBatch) {
+            int32_t c[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int b = b0 + u * parts;
+                c[u] = b < blocks ? s.hist[(int64_t)b * s.bins + d] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                all += c[u];
+                lower += b0 + u * parts < me ? c[u] : 0;
+            }
+        }
+        if (parts == 1) {
+            before[d] = lower;
+            total[d] = all;
+        } else {
+            atomicAdd(&before[d], lower);
+            atomicAdd(&total[d], all);
+        }
+    }
+    __syncthreads();
 }
 
 // In-place exclusive sum of v[0..bins) by a workgroup of THREADS; `carry`
@@ -139,6 +205,18 @@ __device__ __forceinline__ void exclusive_sum(int32_t* v, int bins, int32_t* car
         before += own[i];
     }
     __syncthreads();
+}
+
+// Runs the counting half of a pass (and the sums between, where they are a
+// launch of their own).  s.blocks, bins, bits and shift are set.
+template <bool FIRST>
+void launch_counts(SortPass& s, hipStream_t stream) {
+    const int32_t blocks = s.blocks.total();
+    hipLaunchKernelGGL(sort_count_kernel<FIRST>, dim3(blocks), dim3(kSortThreads), 0, stream, s);
+    s.scanned = (int64_t)blocks * s.bins > kFusedCounts;
+    if (s.scanned)
+        hipLaunchKernelGGL(sort_scan_kernel, dim3((s.bins + kWave - 1) / kWave), dim3(kScanWaves * kWave), 0, stream,
+                           s.hist, blocks, s.bins);
 }
 
 // Counts of each wave's digits: count[w][d] over the wave's own contiguous
