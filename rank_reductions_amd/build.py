@@ -34,7 +34,9 @@ HIP_SOURCES = [
     ("kernels_batch.hip", "kernels_batch_nt", {"RC_KNT": 1}),
     ("kernels_batch.hip", "kernels_batch_cached", {"RC_KNT": 0}),
     ("kernels_copy.hip", "kernels_copy", {}),
-    ("rows_route.hip", "rows_route", {}),
+    ("rows_route.hip", "rows_route_f32", {"RC_ROW_TYPE": "F32"}),
+    ("rows_route.hip", "rows_route_f16", {"RC_ROW_TYPE": "F16"}),
+    ("rows_route.hip", "rows_route_bf16", {"RC_ROW_TYPE": "BF16"}),
     ("rows_exchange.hip", "rows_exchange", {}),
     ("rows_embedding.hip", "rows_embedding", {}),
     ("device.hip", "device", {}),

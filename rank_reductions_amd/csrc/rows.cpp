@@ -255,6 +255,7 @@ int rc_route(const rc_route_desc* desc, const int64_t* tokens, const void* const
         }
         RC_TRY(b.check());
         a.vec = rows_of_four(logits, tokens, R, E, es) && a.group_size % 4 == 0;
+        a.bias_vec = a.group_size % 4 == 0 && reinterpret_cast<uintptr_t>(desc->bias) % 16 == 0;
         if (validate_only || !a.tokens.total()) return {};
         return device_run([&] { return launch_route(a, desc->dtype, stream); });
     });

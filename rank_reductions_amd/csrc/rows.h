@@ -43,7 +43,8 @@ struct RouteArgs {
     float scale;
     int32_t group_size;   // num_experts / groups
     int32_t group_lanes;  // lanes of a token that share a group
-    int32_t vec;          // every row starts on a 4-element boundary
+    int32_t vec;          // every row starts on a 4-element boundary, and so does every group
+    int32_t bias_vec;     // and the bias
 };
 
 // ---------------------------------------------------------------- counting sort
@@ -139,8 +140,20 @@ struct EmbeddingGradArgs {
 
 // ---------------------------------------------------------------- launches (rows_*.hip)
 // Each returns a hipError_t as int; the session's device is current.
-int launch_route(const RouteArgs& a, int dtype, void* stream);
-int launch_route_grad(const RouteArgs& a, int dtype, void* stream);
+int launch_route_F32(const RouteArgs& a, void* stream);
+int launch_route_F16(const RouteArgs& a, void* stream);
+int launch_route_BF16(const RouteArgs& a, void* stream);
+int launch_route_grad_F32(const RouteArgs& a, void* stream);
+int launch_route_grad_F16(const RouteArgs& a, void* stream);
+int launch_route_grad_BF16(const RouteArgs& a, void* stream);
+inline int launch_route(const RouteArgs& a, int dtype, void* stream) {
+    return dtype == RC_F32 ? launch_route_F32(a, stream)
+         : dtype == RC_F16 ? launch_route_F16(a, stream) : launch_route_BF16(a, stream);
+}
+inline int launch_route_grad(const RouteArgs& a, int dtype, void* stream) {
+    return dtype == RC_F32 ? launch_route_grad_F32(a, stream)
+         : dtype == RC_F16 ? launch_route_grad_F16(a, stream) : launch_route_grad_BF16(a, stream);
+}
 int launch_plan(PlanArgs a, void* workspace, void* stream);
 int launch_dispatch(const ExchangeArgs& a, int dtype, void* stream);
 int launch_combine(const ExchangeArgs& a, int dtype, void* stream);

@@ -3,14 +3,22 @@
 //
 // L lanes share a token; lane l of a group of `group_lanes` holds the group's
 // experts 4 (l + group_lanes i) .. + 3.  The choice runs on 64-bit keys: the
-// score (in 64 bits; the logit itself where its order is the score's) with the
-// low ten bits of its significand replaced by the expert's index, reversed
-// where that makes the lower index the larger key.  So keys never tie, equal
-// scores go to the lower index, and scores further apart than 2^-42 of their
-// size are told apart.  Each lane runs its experts through a sorted list of
-// the KP largest keys, two instructions per level (max and min), and the
-// lanes' lists are merged pairwise: the larger of a[i] and b[KP - 1 - i] are
-// the KP largest of both, in bitonic order.
+// score with the low ten bits of its significand replaced by the expert's
+// index, reversed where that makes the lower index the larger key.  So keys
+// never tie and equal scores go to the lower index.  Each lane sorts its
+// experts' keys KP at a time, a comparator being two instructions (max and
+// min), and merges them: the larger of a[i] and b[KP - 1 - i] are the KP
+// largest of both, in bitonic order.  The lanes' lists are merged likewise.
+// Sorting takes 9 instructions per expert for KP = 8; running each expert
+// through a sorted list takes 16.
+//
+// The choice has to be that of the values in 64 bits.  Where the logits'
+// order is the scores' (no bias), the keys are made from the logits, exactly.
+// Otherwise the scores are computed in float32, with a bound on their error;
+// where two of them that decide something are closer than that, the wave takes
+// the same path again on scores in 64 bits (kept apart to 2^-42 of their
+// size).  A double exp and division per expert cost more than all the rest:
+// FIGROUTE.
 #include "rows_impl.h"
 
 namespace rc {
@@ -18,28 +26,48 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 constexpr double kNone = -__builtin_inf();
-constexpr double kHuge = 1e300;
+constexpr float kNone32 = -__builtin_inff();
+constexpr double kNoKey = -1e300;  // keys of what cannot be chosen lie below
+constexpr float kU = 0x1p-24f;
 
-// v_max_f64 / v_min_f64 as they are: keys are never NaN, so the quieting that
-// fmax would add has nothing to do.
-__device__ __forceinline__ double max64(double a, double b) {
+// v_max / v_min as they are: no operand is ever NaN, so the quieting that fmax
+// and fmin would add has nothing to do.
+__device__ __forceinline__ double max_of(double a, double b) {
     double r;
     asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
     return r;
 }
-__device__ __forceinline__ double min64(double a, double b) {
+__device__ __forceinline__ double min_of(double a, double b) {
     double r;
     asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
     return r;
 }
+__device__ __forceinline__ float max_of(float a, float b) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ float min_of(float a, float b) {
+    float r;
+    asm("v_min_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
 
-// Key of a score: kNone stays; the index takes the low ten bits.
-__device__ __forceinline__ double key_of(double score, int expert) {
-    const double v = score + 0.0;  // one zero
-    if (v == kNone) return kNone;
-    const uint64_t u = __builtin_bit_cast(uint64_t, v < kHuge ? v : kHuge);
-    const uint64_t index = (u >> 63) ? (uint64_t)expert : (uint64_t)(RC_MAX_EXPERTS - 1 - expert);
-    return __builtin_bit_cast(double, (u & ~uint64_t(RC_MAX_EXPERTS - 1)) | index);
+// Key of a score that is not NaN or +inf, for `reversed` = RC_MAX_EXPERTS - 1
+// - expert.
+__device__ __forceinline__ double key_of(double score, uint32_t reversed) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, score);
+    const uint32_t hi = score == kNone ? 0xffe00000u : (uint32_t)(u >> 32);
+    const uint32_t index = reversed ^ ((uint32_t)((int32_t)hi >> 31) & (RC_MAX_EXPERTS - 1));
+    const uint32_t lo = ((uint32_t)u & ~(uint32_t)(RC_MAX_EXPERTS - 1)) | index;
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double key_of(float score, uint32_t reversed) {
+    // a float's double has 29 zeros at its end
+    const uint64_t u = __builtin_bit_cast(uint64_t, max_of((double)score, __builtin_bit_cast(double, 0xffe0000000000000ull)));
+    const uint32_t hi = (uint32_t)(u >> 32);
+    const uint32_t lo = (uint32_t)u | (reversed ^ ((uint32_t)((int32_t)hi >> 31) & (RC_MAX_EXPERTS - 1)));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 __device__ __forceinline__ int expert_of(double key) {
     const uint64_t u = __builtin_bit_cast(uint64_t, key);
@@ -49,20 +77,52 @@ __device__ __forceinline__ int expert_of(double key) {
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
+// exp(x) for x <= 0 within (1.25 |x| + 2) kU of itself, and the sigmoid within
+// 5 kU: the exponent's rounding and the constant's, one step of v_exp and of
+// v_rcp, and one sum.
+constexpr float kLog2e = 1.44269504088896341f;
+__device__ __forceinline__ float exp32(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+__device__ __forceinline__ float sigmoid32(float x) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e)); }
+
+// The value that lane (l ^ O) holds, in a step of a butterfly: from O = 4 on,
+// all lanes of the O below hold the same, so that any lane of the other half
+// will do.
+template <int O>
+__device__ __forceinline__ uint32_t across(uint32_t v) {
+    if constexpr (O == 1) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true);       // quad_perm 1 0 3 2
+    else if constexpr (O == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true);  // quad_perm 2 3 0 1
+    else if constexpr (O == 4) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true); // row_half_mirror
+    else if constexpr (O == 8) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true); // row_mirror
+    else return (uint32_t)__shfl_xor((int)v, O);
+}
+template <int O>
+__device__ __forceinline__ float across(float v) {
+    return __builtin_bit_cast(float, across<O>(__builtin_bit_cast(uint32_t, v)));
+}
+template <int O>
+__device__ __forceinline__ double across(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = across<O>((uint32_t)u), hi = across<O>((uint32_t)(u >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <int O>
+__device__ __forceinline__ int across(int v) {
+    return (int)across<O>((uint32_t)v);
+}
+
+// f(mine, other's) over the L lanes of a token, a step of the butterfly at a time.
+template <int L, int O = 1, class V, class F>
+__device__ __forceinline__ V all_lanes(V v, F f) {
+    if constexpr (O < L) return all_lanes<L, O * 2>(f(v, across<O>(v)), f);
+    else return v;
+}
 template <int L, class V>
 __device__ __forceinline__ V sum_lanes(V v) {
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) v += __shfl_xor(v, o);
-    return v;
+    return all_lanes<L>(v, [](V a, V b) { return a + b; });
 }
 template <int L, class V>
 __device__ __forceinline__ V max_lanes(V v) {
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) {
-        const V w = __shfl_xor(v, o);
-        v = w > v ? w : v;
-    }
-    return v;
+    return all_lanes<L>(v, [](V a, V b) { return a > b ? a : b; });
 }
 
 // The rank and row of this lane's token; false past the last.
@@ -74,45 +134,213 @@ __device__ __forceinline__ bool token_of(const RankSpans& tokens, int* rank, int
     return true;
 }
 
+// Where a lane's V experts lie: expert base + at(j) for j < V, at(j) < size.
+struct Part {
+    int group, base, size, lanes, part;
+    bool in_group;
+    __device__ __forceinline__ int at(int j) const { return (j / 4 * lanes + part) * 4 + j % 4; }
+};
+
+__device__ __forceinline__ void order(double& hi, double& lo) {
+    const double m = max_of(hi, lo);
+    lo = min_of(hi, lo);
+    hi = m;
+}
+
+// Sorts N values (a power of two), the largest first: Batcher's odd-even merge
+// sort, 5, 19 and 63 comparators for 4, 8 and 16.
+template <int N>
+__device__ __forceinline__ void sort_values(double* v) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2) {
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2) {
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k) {
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order(v[i + j], v[i + j + k]);
+            }
+        }
+    }
+}
+
+// list (sorted) becomes the KP largest of it and of m (sorted), sorted.
+template <int KP>
+__device__ __forceinline__ void merge_into(double* list, const double* m) {
+#pragma unroll
+    for (int k = 0; k < KP; ++k) list[k] = max_of(list[k], m[KP - 1 - k]);
+#pragma unroll
+    for (int h = KP / 2; h > 0; h >>= 1) {
+#pragma unroll
+        for (int k = 0; k < KP; ++k)
+            if (!(k & h)) order(list[k], list[k + h]);
+    }
+}
+
+// Merges the lanes' sorted lists: all L lanes end with the KP largest.
+template <int L, int KP, int O = 1>
+__device__ __forceinline__ void merge_lists(double* list) {
+    if constexpr (O < L) {
+        double m[KP];
+#pragma unroll
+        for (int k = 0; k < KP; ++k) m[k] = across<O>(list[k]);
+        merge_into<KP>(list, m);
+        merge_lists<L, KP, O * 2>(list);
+    }
+}
+
+// The largest two of what has been seen, with c.
+__device__ __forceinline__ void best_two(float& first, float& second, float c) {
+    second = __builtin_amdgcn_fmed3f(first, second, c);
+    first = max_of(first, c);
+}
+__device__ __forceinline__ void best_two(double& first, double& second, double c) {
+    second = max_of(second, min_of(first, c));
+    first = max_of(first, c);
+}
+
+// The value of the lane mirrored within four.
+__device__ __forceinline__ float quad_mirror(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x1b, 0xf, 0xf, true));
+}
+__device__ __forceinline__ double quad_mirror(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, 0x1b, 0xf, 0xf, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), 0x1b, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// f(j) for j in [0, V): unrolled, or as a loop where its code is long and rarely run.
+template <int V, bool ROLLED, class F>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (ROLLED) {
+#pragma unroll 1
+        for (int j = 0; j < V; ++j) f(j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f(j);
+    }
+}
+
+// The token's best keys.  group_score(j) and score(j): of the lane's expert j,
+// neither NaN nor +inf, kNone where it cannot be chosen; margin: group scores
+// (of type C) closer than this set *doubt.  *kept: whether the lane's group is
+// among the best, and the row not `broken`.
+template <class C, int L, int V, int KP, bool ROLLED, class G, class F>
+__device__ __forceinline__ void pick(const RouteArgs& a, const Part& p, bool broken, G group_score, F score, C margin,
+                                     double* list, bool* kept, bool* doubt) {
+    *kept = true;
+    if (a.groups > 1) {
+        C first = (C)kNone, second = (C)kNone;
+        each<V, ROLLED>([&](int j) { best_two(first, second, group_score(j)); });
+        for (int o = 1; o < p.lanes; o <<= 1) {
+            const C f = __shfl_xor(first, o), s = __shfl_xor(second, o);
+            second = max_of(min_of(first, f), max_of(second, s));
+            first = max_of(first, f);
+        }
+        const C of_group = a.top2 && a.group_size > 1 ? first + second : first;
+        int better = 0;
+        auto against = [&](C other, bool lower) {
+            better += other > of_group || (other == of_group && lower);
+            const C apart = other > of_group ? other - of_group : of_group - other;  // NaN: both kNone
+            *doubt |= apart <= margin;
+        };
+        const int lane = threadIdx.x & (L - 1);
+        if constexpr (L == 8) {
+            // the token's seven other lanes, of those the ones that stand for a group in this lane's place
+            const C other[8] = {of_group, across<1>(of_group), across<2>(of_group), quad_mirror(of_group),
+                                quad_mirror(across<4>(of_group)), across<2>(across<4>(of_group)),
+                                across<1>(across<4>(of_group)), across<4>(of_group)};
+#pragma unroll
+            for (int k = 1; k < 8; ++k) {
+                const int from = lane ^ k;
+                if ((from & (p.lanes - 1)) == p.part && from < a.groups * p.lanes && p.in_group) against(other[k], from < lane);
+            }
+        } else {
+            for (int g = 0; g < a.groups; ++g) {
+                const C other = __shfl(of_group, (threadIdx.x & (kWave - 1) & ~(L - 1)) + g * p.lanes);
+                if (g != p.group && p.in_group) against(other, g < p.group);
+            }
+        }
+        *kept = better < a.top_groups;
+    }
+    *kept &= !broken;
+    const bool open = *kept;
+    auto key = [&](int j) {
+        return key_of(open ? score(j) : (decltype(score(j)))kNone, (uint32_t)(RC_MAX_EXPERTS - 1 - (p.base + p.at(j))));
+    };
+    if constexpr (ROLLED || V < KP) {
+#pragma unroll
+        for (int k = 0; k < KP; ++k) list[k] = kNone;
+        each<V, ROLLED>([&](int j) {
+            double v = key(j);
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                const double low = min_of(list[k], v);
+                list[k] = max_of(list[k], v);
+                v = low;
+            }
+        });
+    } else {
+#pragma unroll
+        for (int j = 0; j < KP; ++j) list[j] = key(j);
+        sort_values<KP>(list);
+#pragma unroll
+        for (int j0 = KP; j0 < V; j0 += KP) {
+            double m[KP];
+#pragma unroll
+            for (int j = 0; j < KP; ++j) m[j] = key(j0 + j);
+            sort_values<KP>(m);
+            merge_into<KP>(list, m);
+        }
+    }
+    merge_lists<L, KP>(list);
+}
+
 template <class T, int L, int V, int KP>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     using E = typename T::E;
     int rank;
     int32_t row;
-    // lanes past the last token repeat it, so that all take part in the exchanges
+    // lanes past the last token have no experts, but take part in the exchanges
     const bool live = token_of<L>(a.tokens, &rank, &row);
     if (!live) {
         rank = 0;
         row = -1;
     }
     const int lane = threadIdx.x & (L - 1);
-    const int group = lane / a.group_lanes, part = lane - group * a.group_lanes;
-    const bool in_group = group < a.groups;
+    Part p;
+    p.lanes = a.group_lanes;
+    p.group = lane / a.group_lanes;
+    p.part = lane - p.group * a.group_lanes;
+    p.size = a.group_size;
+    p.base = p.group * a.group_size;
+    p.in_group = live && p.group < a.groups;
     const E* logits = static_cast<const E*>(a.logits[rank]) + (int64_t)row * a.num_experts;
-    const int base = group * a.group_size;
 
     float x[V];
 #pragma unroll
     for (int j = 0; j < V; j += 4) {
-        const int at = (j / 4 * a.group_lanes + part) * 4;  // within the group
-        if (live && in_group && a.vec && at < a.group_size) {
+        const int at = p.at(j);
+        if (p.in_group && a.vec && at < p.size) {
             if constexpr (sizeof(E) == 4) {
-                F32::unpack(*reinterpret_cast<const u32x4*>(logits + base + at), x + j);
+                F32::unpack(*reinterpret_cast<const u32x4*>(logits + p.base + at), x + j);
             } else {
-                const uint64_t v = *reinterpret_cast<const uint64_t*>(logits + base + at);
+                const uint64_t v = *reinterpret_cast<const uint64_t*>(logits + p.base + at);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[j + i] = T::load(__builtin_bit_cast(E, (uint16_t)(v >> (16 * i))));
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x[j + i] = live && in_group && at + i < a.group_size ? T::load(logits[base + at + i]) : -__builtin_inff();
+                x[j + i] = p.in_group && at + i < p.size ? T::load(logits[p.base + at + i]) : kNone32;
         }
     }
 
     // softmax: the largest logit, and whether the row has a NaN or +inf, which
     // leaves no score that is a number
-    float top = -__builtin_inff();
+    float top = kNone32;
     bool broken = false;
     if (!a.sigmoid) {
 #pragma unroll
@@ -122,128 +350,163 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         }
         top = max_lanes<L>(top);
         broken = max_lanes<L>((int)broken) != 0;
-        if (top == -__builtin_inff()) top = 0.0f;
+        if (top == kNone32) top = 0.0f;
     }
     // scores are needed where their order is not the logits'
     const bool scored = a.bias || (a.groups > 1 && a.top2);
-    double total = 0.0;
+    float total = 0.0f;
     if (!a.sigmoid && (scored || !a.renormalize)) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) total += exp((double)x[j] - (double)top);
+        for (int j = 0; j < V; ++j) total += exp32(x[j] - top);
         total = sum_lanes<L>(total);
     }
-    double c[V];
+    const float share = a.sigmoid ? 0.0f : 1.0f / total;
+    auto score32 = [&](float v) { return a.sigmoid ? sigmoid32(v) : exp32(v - top) * share; };
+    // x becomes what the choice goes by: no NaN (v_max takes the other operand),
+    // nothing above the largest float
+    const float huge = 3.4028234663852886e38f;
+    if (a.bias) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int at = (j / 4 * a.group_lanes + part) * 4 + j % 4;
-        double v = (double)x[j];
-        if (scored) {
-            v = a.sigmoid ? sigmoid64(v) : exp(v - (double)top) / total;
-            if (a.bias && in_group && at < a.group_size) v += (double)a.bias[base + at];
-        }
-        const bool choosable = x[j] > -__builtin_inff() && v > kNone && !broken;  // neither is NaN
-        c[j] = choosable ? (v < kHuge ? v : kHuge) : kNone;
-    }
-
-    if (a.groups > 1) {
-        double first = kNone, second = kNone;
+        for (int j = 0; j < V; j += 4) {
+            const int at = p.at(j);
+            float b[4] = {};
+            if (p.in_group && a.bias_vec && at < p.size) {
+                F32::unpack(*reinterpret_cast<const u32x4*>(a.bias + p.base + at), b);
+            } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            second = max64(second, min64(first, c[j]));
-            first = max64(first, c[j]);
-        }
-        for (int o = 1; o < a.group_lanes; o <<= 1) {
-            const double f = __shfl_xor(first, o), s = __shfl_xor(second, o);
-            second = max64(min64(first, f), max64(second, s));
-            first = max64(first, f);
-        }
-        const double score = a.top2 && a.group_size > 1 ? first + second : first;
-        int better = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const double other = __shfl(score, (threadIdx.x & (kWave - 1) & ~(L - 1)) + g * a.group_lanes);
-            better += other > score || (other == score && g < group);
-        }
-        if (better >= a.top_groups) {
+                for (int i = 0; i < 4; ++i)
+                    if (p.in_group && at + i < p.size) b[i] = a.bias[p.base + at + i];
+            }
 #pragma unroll
-            for (int j = 0; j < V; ++j) c[j] = kNone;
-        }
-    }
-
-    double list[KP];
-#pragma unroll
-    for (int k = 0; k < KP; ++k) list[k] = kNone;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        double v = key_of(c[j], base + (j / 4 * a.group_lanes + part) * 4 + j % 4);
-#pragma unroll
-        for (int k = 0; k < KP; ++k) {
-            const double low = min64(list[k], v);
-            list[k] = max64(list[k], v);
-            v = low;
-        }
-    }
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) {
-        double m[KP];
-#pragma unroll
-        for (int k = 0; k < KP; ++k) m[k] = __shfl_xor(list[KP - 1 - k], o);
-#pragma unroll
-        for (int k = 0; k < KP; ++k) list[k] = max64(list[k], m[k]);
-#pragma unroll
-        for (int h = KP / 2; h > 0; h >>= 1) {
-#pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                if (k & h) continue;
-                const double hi = max64(list[k], list[k + h]);
-                list[k + h] = min64(list[k], list[k + h]);
-                list[k] = hi;
+            for (int i = 0; i < 4; ++i) {
+                const float c = min_of(max_of(score32(x[j + i]) + b[i], kNone32), huge);
+                x[j + i] = x[j + i] > kNone32 ? c : kNone32;
             }
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = min_of(max_of(x[j] + 0.0f, kNone32), huge);  // one zero
+    }
+    // The error of a score, in kU.  Sigmoid: 5.  Softmax: s <= share is off by
+    // (2.25 t + 3) s for its own exponential, t = top - v and s t <= 0.4, and
+    // by (V + 25) s for the sum's: its rounding, and that of exponentials whose
+    // mean t is at most about log E.
+    const float error = a.sigmoid ? 6.0f : 2.0f + share * (float)(V + 32);
+    bool doubt = false, kept;
+    double list[KP];
+    if (a.bias || !scored) {
+        // adding the bias rounds each score by |c|, a group's sum of two by as
+        // much again: the difference of two such sums is off by this at most
+        float near = 0.0f;
+        if (scored) {
+            float most = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) most = x[j] > kNone32 && x[j] < huge ? max_of(most, __builtin_fabsf(x[j])) : most;
+            near = 4.0f * kU * (error + 2.0f * max_lanes<L>(most));
+        }
+        const auto value = [&](int j) { return x[j]; };
+        pick<float, L, V, KP, false>(a, p, broken, value, value, scored ? near : -1.0f, list, &kept, &doubt);
+        if (scored) {
+            // neighbours among the chosen, and whatever else comes close to the last of them
+            float last = 0.0f;
+            bool all = true;  // top_k could be chosen
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                if (k < a.top_k) {
+                    const float c = (float)list[k];
+                    const bool has = list[k] > kNoKey;
+                    doubt |= k > 0 && has && last - c <= near;
+                    all &= has;
+                    last = c;
+                }
+            }
+            int close = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) close += kept && x[j] > kNone32 && x[j] >= last - near;
+            doubt |= all && sum_lanes<L>(close) > a.top_k;
+        }
+    } else {
+        pick<float, L, V, KP, false>(
+            a, p, broken, [&](int j) { return x[j] > kNone32 ? score32(x[j]) : kNone32; }, [&](int j) { return x[j]; },
+            4.0f * kU * (error + 2.0f), list, &kept, &doubt);
+    }
+    doubt = max_lanes<L>((int)doubt) != 0;
+
+    if (__any(doubt)) {
+        // the same in 64 bits, the logits read again
+        auto logit = [&](int j) -> double {
+            const int at = p.at(j);
+            return p.in_group && at < p.size ? (double)T::load(logits[p.base + at]) : kNone;
+        };
+        double sum = 0.0;
+        if (!a.sigmoid) {
+#pragma unroll 1
+            for (int j = 0; j < V; ++j) sum += exp(logit(j) - (double)top);
+            sum = sum_lanes<L>(sum);
+        }
+        auto score = [&](int j) -> double {
+            const double v = logit(j);
+            double c = a.sigmoid ? sigmoid64(v) : exp(v - (double)top) / sum;
+            const int at = p.at(j);
+            if (a.bias && p.in_group && at < p.size) c += (double)a.bias[p.base + at];
+            return v > kNone && c > kNone && !broken ? (c < 1e290 ? c : 1e290) : kNone;
+        };
+        auto choice = [&](int j) -> double {
+            if (a.bias) return score(j);
+            const double v = logit(j) + 0.0;  // one zero
+            return v > kNone && !broken ? (v < 1e290 ? v : 1e290) : kNone;
+        };
+        double exact[KP];
+        bool never = false, kept64;
+        pick<double, L, V, KP, true>(a, p, broken, score, choice, -1.0, exact, &kept64, &never);
+#pragma unroll
+        for (int k = 0; k < KP; ++k) list[k] = doubt ? exact[k] : list[k];
     }
 
-    // weights: lane l takes the choices l, l + L, ...
+    // weights, in 64 bits: lane l takes the choices l, l + L, ...
     constexpr int kEach = (KP + L - 1) / L;
     int expert[kEach];
-    double score[kEach], best = kNone, sum = 0.0;
+    double chosen[kEach], best = kNone, sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         double key = kNone;
 #pragma unroll
         for (int k = 0; k < KP; ++k)
             if (k == lane + i * L && k < a.top_k) key = list[k];
-        expert[i] = key == kNone ? -1 : expert_of(key);
-        score[i] = expert[i] < 0 ? kNone : (double)T::load(logits[expert[i]]);
-        best = score[i] > best ? score[i] : best;
+        expert[i] = key > kNoKey ? expert_of(key) : -1;
+        chosen[i] = expert[i] < 0 ? kNone : (double)T::load(logits[expert[i]]);
+        best = chosen[i] > best ? chosen[i] : best;
     }
     // the chosen softmax scores relative to the largest chosen, or to all
     const bool relative = !a.sigmoid && a.renormalize;
     if (relative) best = max_lanes<L>(best);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        if (expert[i] < 0) score[i] = 0.0;
-        else if (a.sigmoid) score[i] = sigmoid64(score[i]);
-        else score[i] = exp(score[i] - (relative ? best : (double)top));
-        sum += score[i];
+        if (expert[i] < 0) chosen[i] = 0.0;
+        else if (a.sigmoid) chosen[i] = sigmoid64(chosen[i]);
+        else chosen[i] = exp(chosen[i] - (relative ? best : (double)top));
+        sum += chosen[i];
     }
     if (a.renormalize) sum = sum_lanes<L>(sum);
-    else sum = a.sigmoid ? 1.0 : total;
+    else sum = a.sigmoid ? 1.0 : (double)total;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int k = lane + i * L;
         if (!live || k >= a.top_k) continue;
         const int64_t at = (int64_t)row * a.top_k + k;
         a.experts[rank][at] = expert[i];
-        a.weights[rank][at] = expert[i] >= 0 && sum > 0.0 ? (float)((double)a.scale * (score[i] / sum)) : 0.0f;
+        a.weights[rank][at] = expert[i] >= 0 && sum > 0.0 ? (float)((double)a.scale * (chosen[i] / sum)) : 0.0f;
     }
 }
 
 // The weights' gradient.  Each token's row of E values is put together in LDS:
 // cleared (or filled with the softmax's part that every expert has), then the
-// chosen experts' parts are added by the lane that owns them, in order of k.
+// chosen experts' parts are added in order of k; one lane makes, adds to and
+// writes out each of its four experts.
 template <class T, int L>
 __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a) {
     using E = typename T::E;
-    extern __shared__ float lds[];
+    extern __shared__ __align__(16) float lds[];
     int rank;
     int32_t row;
     const bool live = token_of<L>(a.tokens, &rank, &row);
@@ -308,23 +571,28 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a) 
         else d[i] = g[i] * p[i];
         if (a.sigmoid && expert[i] >= 0) d[i] *= sigmoid64(-x[i]);
     }
-    // the row
-    for (int e = lane; e < a.num_experts; e += L) {
-        float v = 0.0f;
-        if (full && any && live) v = -(float)dot * (expf(T::load(logits[e]) - top) / total);
-        mine[e] = v;
+    // the row; lane l makes the experts 4 l .. 4 l + 3 and every 4 L on
+    float part[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) part[i] = (float)d[i];
+    for (int e = lane * 4; e < a.num_experts; e += L * 4) {
+        float v[4] = {};
+        if (full && any && live) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (e + i < a.num_experts) v[i] = -(float)dot * (expf(T::load(logits[e + i]) - top) / total);
+        }
+        *reinterpret_cast<u32x4*>(mine + e) = F32::pack(v);
     }
-    __syncthreads();
 #pragma unroll
     for (int k = 0; k < RC_MAX_TOP_K; ++k) {
         if (k < a.top_k) {
             const int from = (threadIdx.x & (kWave - 1) & ~(L - 1)) + k % L;
             const int e = __shfl(expert[k / L], from);
-            const float v = (float)__shfl(d[k / L], from);
-            if (e >= 0 && e % L == lane) mine[e] += v;
+            const float v = __shfl(part[k / L], from);
+            if (e >= 0 && e / 4 % L == lane) mine[e] += v;
         }
     }
-    __syncthreads();
     if (!live) return;
     E* out = static_cast<E*>(a.d_logits[rank]) + at;
     if (a.vec) {
@@ -340,7 +608,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a) 
             }
         }
     } else {
-        for (int e = lane; e < a.num_experts; e += L) out[e] = T::store(mine[e]);
+        for (int e0 = lane * 4; e0 < a.num_experts; e0 += L * 4)
+            for (int e = e0; e < min(e0 + 4, a.num_experts); ++e) out[e] = T::store(mine[e]);
     }
 }
 
@@ -366,12 +635,20 @@ int run_route(RouteArgs a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Lanes per token: 8, so that a wave's instructions serve eight tokens; 64
+// where there are so few tokens that latency counts (64 tokens of 256 experts:
+// FIGFEW), or too many experts.
+constexpr int64_t kFewTokens = 2048;
 template <class T>
 int pick_route(const RouteArgs& a, hipStream_t s) {
     const int few = per_lane(a, 8), many = per_lane(a, 64);
+    if (few <= 4) return run_route<T, 8, 4>(a, s);
+    if (many <= 4 && a.tokens.total() <= kFewTokens) return run_route<T, 64, 4>(a, s);
     if (few <= 8) return run_route<T, 8, 8>(a, s);
+    if (few <= 16) return run_route<T, 8, 16>(a, s);
     if (few <= 32) return run_route<T, 8, 32>(a, s);
     if (many <= 8) return run_route<T, 64, 8>(a, s);
+    if (many <= 16) return run_route<T, 64, 16>(a, s);
     return run_route<T, 64, 32>(a, s);
 }
 
@@ -392,11 +669,16 @@ int pick_route_grad(const RouteArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int launch_route(const RouteArgs& a, int dtype, void* stream) {
-    return RC_BY_TYPE(pick_route, a, static_cast<hipStream_t>(stream));
+// This file is compiled once per element type of the logits (RC_ROW_TYPE), so
+// that the instantiations compile in parallel.
+#define RC_JOIN2(a, b) a##b
+#define RC_JOIN(a, b) RC_JOIN2(a, b)
+
+int RC_JOIN(launch_route_, RC_ROW_TYPE)(const RouteArgs& a, void* stream) {
+    return pick_route<RC_ROW_TYPE>(a, static_cast<hipStream_t>(stream));
 }
-int launch_route_grad(const RouteArgs& a, int dtype, void* stream) {
-    return RC_BY_TYPE(pick_route_grad, a, static_cast<hipStream_t>(stream));
+int RC_JOIN(launch_route_grad_, RC_ROW_TYPE)(const RouteArgs& a, void* stream) {
+    return pick_route_grad<RC_ROW_TYPE>(a, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace rc
