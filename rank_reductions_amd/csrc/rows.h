@@ -45,6 +45,7 @@ struct RouteArgs {
     int32_t group_lanes;  // lanes of a token that share a group
     int32_t vec;          // every row starts on a 4-element boundary, and so does every group
     int32_t bias_vec;     // and the bias
+    int32_t staged;       // rows go through LDS
 };
 
 // ---------------------------------------------------------------- counting sort

@@ -117,6 +117,12 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
 
+// LDS written by this wave's lanes may be read by its other lanes behind it.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 #define RC_BY_TYPE(fn, ...)                                    \
     (dtype == RC_F32 ? fn<F32>(__VA_ARGS__)                    \
      : dtype == RC_F16 ? fn<F16>(__VA_ARGS__) : fn<BF16>(__VA_ARGS__))

@@ -15,10 +15,12 @@
 // The choice has to be that of the values in 64 bits.  Where the logits'
 // order is the scores' (no bias), the keys are made from the logits, exactly.
 // Otherwise the scores are computed in float32, with a bound on their error;
-// where two of them that decide something are closer than that, the wave takes
-// the same path again on scores in 64 bits (kept apart to 2^-42 of their
-// size).  A double exp and division per expert cost more than all the rest:
-// FIGROUTE.
+// where two that decide something are closer than that, the scores that could
+// matter - a handful - are computed again in 64 bits and decide (apart to
+// 2^-42 of their size).  A double exp and division for every expert cost more
+// than all the rest: FIGROUTE.
+//
+// Bound by instruction issue where there are many tokens: FIGVALU.
 #include "rows_impl.h"
 
 namespace rc {
@@ -165,6 +167,13 @@ __device__ __forceinline__ void sort_values(double* v) {
     }
 }
 
+// list (sorted) becomes the KP largest of it and v.
+template <int KP>
+__device__ __forceinline__ void insert(double* list, double v) {
+#pragma unroll
+    for (int k = 0; k < KP; ++k) order(list[k], v);
+}
+
 // list (sorted) becomes the KP largest of it and of m (sorted), sorted.
 template <int KP>
 __device__ __forceinline__ void merge_into(double* list, const double* m) {
@@ -211,96 +220,65 @@ __device__ __forceinline__ double quad_mirror(double v) {
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// f(j) for j in [0, V): unrolled, or as a loop where its code is long and rarely run.
-template <int V, bool ROLLED, class F>
-__device__ __forceinline__ void each(F f) {
-    if constexpr (ROLLED) {
-#pragma unroll 1
-        for (int j = 0; j < V; ++j) f(j);
-    } else {
+// Whether the lane's group is among the top_groups best, by the two best
+// scores of each lane's experts (joined over the lanes of a group here); sets
+// *doubt where another group's score is within margin.
+template <int L, class C>
+__device__ __forceinline__ bool group_kept(const RouteArgs& a, const Part& p, C& first, C& second, C margin, bool* doubt) {
+    for (int o = 1; o < p.lanes; o <<= 1) {
+        const C f = __shfl_xor(first, o), s = __shfl_xor(second, o);
+        second = max_of(min_of(first, f), max_of(second, s));
+        first = max_of(first, f);
+    }
+    const C of_group = a.top2 && a.group_size > 1 ? first + second : first;
+    int better = 0;
+    auto against = [&](C other, bool lower) {
+        better += other > of_group || (other == of_group && lower);
+        const C apart = other > of_group ? other - of_group : of_group - other;  // NaN: both kNone
+        *doubt |= apart <= margin;
+    };
+    const int lane = threadIdx.x & (L - 1);
+    if constexpr (L == 8) {
+        // the token's seven other lanes, of those the ones that stand for a group in this lane's place
+        const C other[8] = {of_group, across<1>(of_group), across<2>(of_group), quad_mirror(of_group),
+                            quad_mirror(across<4>(of_group)), across<2>(across<4>(of_group)),
+                            across<1>(across<4>(of_group)), across<4>(of_group)};
 #pragma unroll
-        for (int j = 0; j < V; ++j) f(j);
+        for (int k = 1; k < 8; ++k) {
+            const int from = lane ^ k;
+            if ((from & (p.lanes - 1)) == p.part && from < a.groups * p.lanes && p.in_group) against(other[k], from < lane);
+        }
+    } else {
+        for (int g = 0; g < a.groups; ++g) {
+            const C other = __shfl(of_group, (threadIdx.x & (kWave - 1) & ~(L - 1)) + g * p.lanes);
+            if (g != p.group && p.in_group) against(other, g < p.group);
+        }
+    }
+    return better < a.top_groups;
+}
+
+// Four consecutive logits.
+template <class T>
+__device__ __forceinline__ void load4(const typename T::E* p, float* x) {
+    using E = typename T::E;
+    if constexpr (sizeof(E) == 4) {
+        F32::unpack(*reinterpret_cast<const u32x4*>(p), x);
+    } else {
+        const uint64_t v = *reinterpret_cast<const uint64_t*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = T::load(__builtin_bit_cast(E, (uint16_t)(v >> (16 * i))));
     }
 }
 
-// The token's best keys.  group_score(j) and score(j): of the lane's expert j,
-// neither NaN nor +inf, kNone where it cannot be chosen; margin: group scores
-// (of type C) closer than this set *doubt.  *kept: whether the lane's group is
-// among the best, and the row not `broken`.
-template <class C, int L, int V, int KP, bool ROLLED, class G, class F>
-__device__ __forceinline__ void pick(const RouteArgs& a, const Part& p, bool broken, G group_score, F score, C margin,
-                                     double* list, bool* kept, bool* doubt) {
-    *kept = true;
-    if (a.groups > 1) {
-        C first = (C)kNone, second = (C)kNone;
-        each<V, ROLLED>([&](int j) { best_two(first, second, group_score(j)); });
-        for (int o = 1; o < p.lanes; o <<= 1) {
-            const C f = __shfl_xor(first, o), s = __shfl_xor(second, o);
-            second = max_of(min_of(first, f), max_of(second, s));
-            first = max_of(first, f);
-        }
-        const C of_group = a.top2 && a.group_size > 1 ? first + second : first;
-        int better = 0;
-        auto against = [&](C other, bool lower) {
-            better += other > of_group || (other == of_group && lower);
-            const C apart = other > of_group ? other - of_group : of_group - other;  // NaN: both kNone
-            *doubt |= apart <= margin;
-        };
-        const int lane = threadIdx.x & (L - 1);
-        if constexpr (L == 8) {
-            // the token's seven other lanes, of those the ones that stand for a group in this lane's place
-            const C other[8] = {of_group, across<1>(of_group), across<2>(of_group), quad_mirror(of_group),
-                                quad_mirror(across<4>(of_group)), across<2>(across<4>(of_group)),
-                                across<1>(across<4>(of_group)), across<4>(of_group)};
-#pragma unroll
-            for (int k = 1; k < 8; ++k) {
-                const int from = lane ^ k;
-                if ((from & (p.lanes - 1)) == p.part && from < a.groups * p.lanes && p.in_group) against(other[k], from < lane);
-            }
-        } else {
-            for (int g = 0; g < a.groups; ++g) {
-                const C other = __shfl(of_group, (threadIdx.x & (kWave - 1) & ~(L - 1)) + g * p.lanes);
-                if (g != p.group && p.in_group) against(other, g < p.group);
-            }
-        }
-        *kept = better < a.top_groups;
-    }
-    *kept &= !broken;
-    const bool open = *kept;
-    auto key = [&](int j) {
-        return key_of(open ? score(j) : (decltype(score(j)))kNone, (uint32_t)(RC_MAX_EXPERTS - 1 - (p.base + p.at(j))));
-    };
-    if constexpr (ROLLED || V < KP) {
-#pragma unroll
-        for (int k = 0; k < KP; ++k) list[k] = kNone;
-        each<V, ROLLED>([&](int j) {
-            double v = key(j);
-#pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                const double low = min_of(list[k], v);
-                list[k] = max_of(list[k], v);
-                v = low;
-            }
-        });
-    } else {
-#pragma unroll
-        for (int j = 0; j < KP; ++j) list[j] = key(j);
-        sort_values<KP>(list);
-#pragma unroll
-        for (int j0 = KP; j0 < V; j0 += KP) {
-            double m[KP];
-#pragma unroll
-            for (int j = 0; j < KP; ++j) m[j] = key(j0 + j);
-            sort_values<KP>(m);
-            merge_into<KP>(list, m);
-        }
-    }
-    merge_lists<L, KP>(list);
-}
+// Where piece q (four logits) of the wave's token t lies in the wave's LDS:
+// turned within eight pieces by the piece and the token, so that lanes that
+// read pieces eight apart, of eight tokens, meet all banks.
+__device__ __forceinline__ int staged_at(int t, int q, int pieces) { return t * pieces + (q ^ (((q >> 3) + t) & 7)); }
 
 template <class T, int L, int V, int KP>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     using E = typename T::E;
+    extern __shared__ __align__(16) unsigned char route_lds[];
     int rank;
     int32_t row;
     // lanes past the last token have no experts, but take part in the exchanges
@@ -320,21 +298,52 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     const E* logits = static_cast<const E*>(a.logits[rank]) + (int64_t)row * a.num_experts;
 
     float x[V];
+    if (L == 8 && a.staged) {
+        // A lane that holds a group of its own reads a line of its own in each
+        // load, 64 lines a wave, which the L1 cannot keep until their next
+        // quarter is read: whole rows by whole waves, then, through LDS.
+        constexpr int kTokens = kWave / L;
+        const int w = lane_id(), pieces = (a.num_experts / 4 + 7) & ~7;
+        E* stage = reinterpret_cast<E*>(route_lds) + (threadIdx.x / kWave) * kTokens * pieces * 4;
+        const uint64_t mine = live ? reinterpret_cast<uint64_t>(logits) : 0;
+        float v[kTokens][4];
 #pragma unroll
-    for (int j = 0; j < V; j += 4) {
-        const int at = p.at(j);
-        if (p.in_group && a.vec && at < p.size) {
-            if constexpr (sizeof(E) == 4) {
-                F32::unpack(*reinterpret_cast<const u32x4*>(logits + p.base + at), x + j);
+        for (int t = 0; t < kTokens; ++t) {
+            const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)mine, t * L);
+            const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(mine >> 32), t * L);
+            const E* from = reinterpret_cast<const E*>((uint64_t)hi << 32 | lo);
+            if (from && w < a.num_experts / 4) load4<T>(from + 4 * w, v[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < kTokens; ++t) {
+            if (w >= a.num_experts / 4) continue;
+            E e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = T::store(v[t][i]);  // exact: it was loaded from one
+            __builtin_memcpy(__builtin_assume_aligned(stage + 4 * staged_at(t, w, pieces), 4 * sizeof(E)), e, sizeof e);
+        }
+        wave_sync();
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const int at = p.at(j);
+            if (p.in_group && at < p.size) {
+                load4<T>(stage + 4 * staged_at(w / L, (p.base + at) / 4, pieces), x + j);
             } else {
-                const uint64_t v = *reinterpret_cast<const uint64_t*>(logits + p.base + at);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[j + i] = T::load(__builtin_bit_cast(E, (uint16_t)(v >> (16 * i))));
+                for (int i = 0; i < 4; ++i) x[j + i] = kNone32;
             }
-        } else {
+        }
+    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[j + i] = p.in_group && at + i < p.size ? T::load(logits[p.base + at + i]) : kNone32;
+        for (int j = 0; j < V; j += 4) {
+            const int at = p.at(j);
+            if (p.in_group && a.vec && at < p.size) {
+                load4<T>(logits + p.base + at, x + j);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[j + i] = p.in_group && at + i < p.size ? T::load(logits[p.base + at + i]) : kNone32;
+            }
         }
     }
 
@@ -387,80 +396,143 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) x[j] = min_of(max_of(x[j] + 0.0f, kNone32), huge);  // one zero
     }
-    // The error of a score, in kU.  Sigmoid: 5.  Softmax: s <= share is off by
-    // (2.25 t + 3) s for its own exponential, t = top - v and s t <= 0.4, and
-    // by (V + 25) s for the sum's: its rounding, and that of exponentials whose
-    // mean t is at most about log E.
-    const float error = a.sigmoid ? 6.0f : 2.0f + share * (float)(V + 32);
-    bool doubt = false, kept;
-    double list[KP];
-    if (a.bias || !scored) {
-        // adding the bias rounds each score by |c|, a group's sum of two by as
-        // much again: the difference of two such sums is off by this at most
-        float near = 0.0f;
-        if (scored) {
-            float most = 0.0f;
+    // How close two values that decide something may come.  The error of a
+    // score, in kU.  Sigmoid: 5.  Softmax: s <= share is off by (2.25 t + 3) s
+    // for its own exponential, t = top - v and s t <= 0.4, and by (V + 25) s for
+    // the sum's: its rounding, and that of exponentials whose mean t is at most
+    // about log E.  Adding the bias rounds by |c|, a group's sum of two by as
+    // much again: the difference of two such sums is off by this at most.
+    float near = 0.0f;
+    if (scored) {
+        float most = 1.0f;
+        if (a.bias) {
 #pragma unroll
             for (int j = 0; j < V; ++j) most = x[j] > kNone32 && x[j] < huge ? max_of(most, __builtin_fabsf(x[j])) : most;
-            near = 4.0f * kU * (error + 2.0f * max_lanes<L>(most));
+            most = max_lanes<L>(most);
         }
-        const auto value = [&](int j) { return x[j]; };
-        pick<float, L, V, KP, false>(a, p, broken, value, value, scored ? near : -1.0f, list, &kept, &doubt);
-        if (scored) {
-            // neighbours among the chosen, and whatever else comes close to the last of them
-            float last = 0.0f;
-            bool all = true;  // top_k could be chosen
+        near = 4.0f * kU * ((a.sigmoid ? 6.0f : 2.0f + share * (float)(V + 32)) + 2.0f * most);
+    }
+
+    // scores in 64 bits, from the logits and the bias
+    double sum64 = 0.0;
+    auto logit = [&](int j) -> double {
+        const int at = p.at(j);
+        return p.in_group && at < p.size ? (double)T::load(logits[p.base + at]) : kNone;
+    };
+    auto sum_exact = [&]() {
+        if (a.sigmoid || sum64 != 0.0) return;
+#pragma unroll 4
+        for (int j = 0; j < V; ++j) sum64 += exp(logit(j) - (double)top);
+        sum64 = sum_lanes<L>(sum64);
+    };
+    auto exact = [&](int j) -> double {
+        const double v = logit(j);
+        double c = a.sigmoid ? sigmoid64(v) : exp(v - (double)top) / sum64;
+        const int at = p.at(j);
+        if (a.bias && p.in_group && at < p.size) c += (double)a.bias[p.base + at];
+        return c < 1e290 ? c : 1e290;
+    };
+
+    bool kept = true;
+    if (a.groups > 1) {
+        float first = kNone32, second = kNone32;
+        bool doubt = false;
+        const bool by_score = scored && !a.bias;
+        if (by_score) {
 #pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                if (k < a.top_k) {
-                    const float c = (float)list[k];
-                    const bool has = list[k] > kNoKey;
-                    doubt |= k > 0 && has && last - c <= near;
-                    all &= has;
-                    last = c;
+            for (int j = 0; j < V; ++j) best_two(first, second, x[j] > kNone32 ? score32(x[j]) : kNone32);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) best_two(first, second, x[j]);
+        }
+        kept = group_kept<L>(a, p, first, second, scored ? near : -1.0f, &doubt);
+        if (__any(doubt)) {
+            // what may be among its group's two best
+            const float from = (a.top2 ? second : first) - near;
+            uint32_t close = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float c = by_score ? score32(x[j]) : x[j];
+                close = close + close + (uint32_t)(x[j] > kNone32 && c >= from);
+            }
+            sum_exact();
+            double first64 = kNone, second64 = kNone;
+            while (__any(close)) {
+                if (close) {
+                    best_two(first64, second64, exact(V - 1 - __builtin_ctz(close)));
+                    close &= close - 1;
                 }
             }
-            int close = 0;
-#pragma unroll
-            for (int j = 0; j < V; ++j) close += kept && x[j] > kNone32 && x[j] >= last - near;
-            doubt |= all && sum_lanes<L>(close) > a.top_k;
+            bool never = false;
+            kept = group_kept<L>(a, p, first64, second64, -1.0, &never);
         }
-    } else {
-        pick<float, L, V, KP, false>(
-            a, p, broken, [&](int j) { return x[j] > kNone32 ? score32(x[j]) : kNone32; }, [&](int j) { return x[j]; },
-            4.0f * kU * (error + 2.0f), list, &kept, &doubt);
     }
-    doubt = max_lanes<L>((int)doubt) != 0;
+    kept &= !broken;
 
-    if (__any(doubt)) {
-        // the same in 64 bits, the logits read again
-        auto logit = [&](int j) -> double {
-            const int at = p.at(j);
-            return p.in_group && at < p.size ? (double)T::load(logits[p.base + at]) : kNone;
-        };
-        double sum = 0.0;
-        if (!a.sigmoid) {
-#pragma unroll 1
-            for (int j = 0; j < V; ++j) sum += exp(logit(j) - (double)top);
-            sum = sum_lanes<L>(sum);
-        }
-        auto score = [&](int j) -> double {
-            const double v = logit(j);
-            double c = a.sigmoid ? sigmoid64(v) : exp(v - (double)top) / sum;
-            const int at = p.at(j);
-            if (a.bias && p.in_group && at < p.size) c += (double)a.bias[p.base + at];
-            return v > kNone && c > kNone && !broken ? (c < 1e290 ? c : 1e290) : kNone;
-        };
-        auto choice = [&](int j) -> double {
-            if (a.bias) return score(j);
-            const double v = logit(j) + 0.0;  // one zero
-            return v > kNone && !broken ? (v < 1e290 ? v : 1e290) : kNone;
-        };
-        double exact[KP];
-        bool never = false, kept64;
-        pick<double, L, V, KP, true>(a, p, broken, score, choice, -1.0, exact, &kept64, &never);
+    auto reversed = [&](int j) { return (uint32_t)(RC_MAX_EXPERTS - 1 - (p.base + p.at(j))); };
+    double list[KP];
+    if constexpr (V < KP) {
 #pragma unroll
-        for (int k = 0; k < KP; ++k) list[k] = doubt ? exact[k] : list[k];
+        for (int k = 0; k < KP; ++k) list[k] = kNone;
+#pragma unroll
+        for (int j = 0; j < V; ++j) insert<KP>(list, key_of(x[j], reversed(j)));
+    } else {
+#pragma unroll
+        for (int j = 0; j < KP; ++j) list[j] = key_of(x[j], reversed(j));
+        sort_values<KP>(list);
+#pragma unroll
+        for (int j0 = KP; j0 < V; j0 += KP) {
+            double m[KP];
+#pragma unroll
+            for (int j = 0; j < KP; ++j) m[j] = key_of(x[j0 + j], reversed(j0 + j));
+            sort_values<KP>(m);
+            merge_into<KP>(list, m);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < KP; ++k) list[k] = kept ? list[k] : kNone;
+    merge_lists<L, KP>(list);
+
+    if (a.bias) {
+        // neighbours among the chosen, and whatever else comes close to the last of them
+        float last = 0.0f;
+        bool all = true, doubt = false;  // all: top_k could be chosen
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            if (k < a.top_k) {
+                const float c = (float)list[k];
+                const bool has = list[k] > kNoKey;
+                doubt |= k > 0 && has && last - c <= near;
+                all &= has;
+                last = c;
+            }
+        }
+        const float from = all ? last - near : -huge;
+        uint32_t close = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) close = close + close + (uint32_t)(x[j] >= from);
+        if (!kept) close = 0;
+        doubt |= all && sum_lanes<L>(__builtin_popcount(close)) > a.top_k;
+        doubt = max_lanes<L>((int)doubt) != 0;
+        if (__any(doubt)) {
+            sum_exact();
+            double list64[KP];
+#pragma unroll
+            for (int k = 0; k < KP; ++k) list64[k] = kNone;
+            if (!doubt) close = 0;
+            while (__any(close)) {
+                double key = kNone;
+                if (close) {
+                    const int j = V - 1 - __builtin_ctz(close);
+                    key = key_of(exact(j), reversed(j));
+                    close &= close - 1;
+                }
+                insert<KP>(list64, key);
+            }
+            merge_lists<L, KP>(list64);
+#pragma unroll
+            for (int k = 0; k < KP; ++k) list[k] = doubt ? list64[k] : list[k];
+        }
     }
 
     // weights, in 64 bits: lane l takes the choices l, l + L, ...
@@ -631,7 +703,9 @@ int run_route(RouteArgs a, hipStream_t s) {
     constexpr int per = kRouteThreads / L;
     const dim3 grid = grid_of(((int64_t)a.tokens.total() + per - 1) / per);
     auto fn = a.top_k <= 4 ? route_kernel<T, L, V, 4> : a.top_k <= 8 ? route_kernel<T, L, V, 8> : route_kernel<T, L, V, 16>;
-    hipLaunchKernelGGL(fn, grid, dim3(kRouteThreads), 0, s, a);
+    a.staged = L == 8 && a.vec && a.group_lanes < L;
+    const int lds = a.staged ? per * ((a.num_experts / 4 + 7) & ~7) * 4 * (int)sizeof(typename T::E) : 0;
+    hipLaunchKernelGGL(fn, grid, dim3(kRouteThreads), lds, s, a);
     return hipGetLastError();
 }
 

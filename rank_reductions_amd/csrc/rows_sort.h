@@ -60,8 +60,6 @@ __device__ __forceinline__ uint64_t same_digit(int digit, int bits, bool has) {
     return has ? mask : 0;
 }
 
-__device__ __forceinline__ void wave_sync() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); __builtin_amdgcn_wave_barrier(); }
-
 // Position of this lane's entry among those of its digit that the wave has
 // met, counting from count[digit], which moves on by the strip's.
 __device__ __forceinline__ int32_t strip_rank(int digit, int bits, bool has, volatile int32_t* count) {
