@@ -371,9 +371,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     }
     const float share = a.sigmoid ? 0.0f : 1.0f / total;
     auto score32 = [&](float v) { return a.sigmoid ? sigmoid32(v) : exp32(v - top) * share; };
-    // x becomes what the choice goes by: no NaN (v_max takes the other operand),
-    // nothing above the largest float
+    // x becomes what the choice goes by: nothing above the largest float, and
+    // kNone32 for a NaN (v_max takes the other operand)
     const float huge = 3.4028234663852886e38f;
+    auto tidy = [&](float v) { return min_of(max_of(v, kNone32), huge); };
     if (a.bias) {
 #pragma unroll
         for (int j = 0; j < V; j += 4) {
@@ -388,30 +389,23 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float c = min_of(max_of(score32(x[j + i]) + b[i], kNone32), huge);
+                const float c = tidy(score32(x[j + i]) + b[i]);
                 x[j + i] = x[j + i] > kNone32 ? c : kNone32;
             }
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = min_of(max_of(x[j] + 0.0f, kNone32), huge);  // one zero
+        for (int j = 0; j < V; ++j) x[j] = tidy(x[j] + 0.0f);  // one zero
     }
-    // How close two values that decide something may come.  The error of a
-    // score, in kU.  Sigmoid: 5.  Softmax: s <= share is off by (2.25 t + 3) s
-    // for its own exponential, t = top - v and s t <= 0.4, and by (V + 25) s for
-    // the sum's: its rounding, and that of exponentials whose mean t is at most
-    // about log E.  Adding the bias rounds by |c|, a group's sum of two by as
-    // much again: the difference of two such sums is off by this at most.
-    float near = 0.0f;
-    if (scored) {
-        float most = 1.0f;
-        if (a.bias) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) most = x[j] > kNone32 && x[j] < huge ? max_of(most, __builtin_fabsf(x[j])) : most;
-            most = max_lanes<L>(most);
-        }
-        near = 4.0f * kU * ((a.sigmoid ? 6.0f : 2.0f + share * (float)(V + 32)) + 2.0f * most);
-    }
+    // How close two values that decide something may come, of size up to
+    // `size`.  The error of a score, in kU.  Sigmoid: 5.  Softmax: s <= share is
+    // off by (2.25 t + 3) s for its own exponential, t = top - v and s t <= 0.4,
+    // and by (V + 25) s for the sum's: its rounding, and that of exponentials
+    // whose mean t is at most about log E.  Adding the bias rounds by the
+    // result, a group's sum of two by as much again: the difference of two such
+    // sums is off by this at most.
+    const float error = a.sigmoid ? 6.0f : 2.0f + share * (float)(V + 32);
+    auto near_of = [&](float size) { return 4.0f * kU * (error + 2.0f * (size < huge ? max_of(size, 1.0f) : 1.0f)); };
 
     // scores in 64 bits, from the logits and the bias
     double sum64 = 0.0;
@@ -445,7 +439,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 #pragma unroll
             for (int j = 0; j < V; ++j) best_two(first, second, x[j]);
         }
-        kept = group_kept<L>(a, p, first, second, scored ? near : -1.0f, &doubt);
+        // the sizes of what is compared: a lane's two best, of all lanes
+        float near = -1.0f;
+        if (scored) {
+            const float f = __builtin_fabsf(first), g = __builtin_fabsf(second);
+            near = near_of(max_lanes<L>(max_of(f < huge ? f : 0.0f, g < huge ? g : 0.0f)));
+        }
+        kept = group_kept<L>(a, p, first, second, near, &doubt);
         if (__any(doubt)) {
             // what may be among its group's two best
             const float from = (a.top2 ? second : first) - near;
@@ -491,30 +491,40 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     }
 #pragma unroll
     for (int k = 0; k < KP; ++k) list[k] = kept ? list[k] : kNone;
+    float own[KP];  // the lane's best scores
+#pragma unroll
+    for (int k = 0; k < KP; ++k) own[k] = (float)list[k];
     merge_lists<L, KP>(list);
 
     if (a.bias) {
         // neighbours among the chosen, and whatever else comes close to the last of them
-        float last = 0.0f;
-        bool all = true, doubt = false;  // all: top_k could be chosen
+        const float best = __builtin_fabsf((float)list[0]);
+        float last = 0.0f, least = -1.0f;  // least: the smallest distance
+        bool all = true;                   // top_k could be chosen
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
             if (k < a.top_k) {
                 const float c = (float)list[k];
                 const bool has = list[k] > kNoKey;
-                doubt |= k > 0 && has && last - c <= near;
+                if (k > 0 && has) least = k == 1 ? last - c : min_of(least, last - c);
                 all &= has;
-                last = c;
+                last = has ? c : last;
             }
         }
+        const float near = near_of(max_of(best, __builtin_fabsf(last)));
+        bool doubt = least >= 0.0f && least <= near;
         const float from = all ? last - near : -huge;
-        uint32_t close = 0;
+        // a lane's KP best are enough to see whether more than top_k come as close
+        int count = 0;
 #pragma unroll
-        for (int j = 0; j < V; ++j) close = close + close + (uint32_t)(x[j] >= from);
-        if (!kept) close = 0;
-        doubt |= all && sum_lanes<L>(__builtin_popcount(close)) > a.top_k;
+        for (int k = 0; k < KP; ++k) count += own[k] >= from;
+        doubt |= all && sum_lanes<L>(count) > a.top_k;
         doubt = max_lanes<L>((int)doubt) != 0;
         if (__any(doubt)) {
+            uint32_t close = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) close = close + close + (uint32_t)(x[j] >= from);
+            if (!kept) close = 0;
             sum_exact();
             double list64[KP];
 #pragma unroll
