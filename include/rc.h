@@ -486,7 +486,7 @@ int rc_embedding(const rc_embedding_desc* desc, const void* const* tables, void*
 
 /* The table's gradient, summed over the tokens of all ranks: row v of
  * d_tables is scale times the sum of d_outs[r][t] over ids[r][t] == v, taken
- * in order of rank and t: pieces of 64 are summed from zero, runs of 64
+ * in order of rank and t: pieces of 64 are summed from zero, runs of 16
  * pieces likewise, and the runs added in order.  With accumulate the row's
  * old value is added once at the end, and rows that no id names are not
  * touched; without, they are set to zero. */

@@ -169,7 +169,7 @@ def embedding(ids, table, scale=1.0):
     return out
 
 
-PIECE = 64
+PIECE, RUN = 64, 16
 
 
 def embedding_grad(ids, d_outs, vocab, scale=1.0):
@@ -188,7 +188,7 @@ def embedding_grad(ids, d_outs, vocab, scale=1.0):
 
 def embedding_grad_ordered(ids, d_outs, vocab, scale=1.0, old=None):
     """The same in float32, in the documented order: pieces of 64 tokens summed
-    from zero, runs of 64 pieces likewise, the runs added in order; then the
+    from zero, runs of 16 pieces likewise, the runs added in order; then the
     scale, then the old value.  Rows in float32 as they are before the last
     rounding; `old` (or zeros) where no token names the row."""
     width = d_outs[0].shape[1]
@@ -204,13 +204,13 @@ def embedding_grad_ordered(ids, d_outs, vocab, scale=1.0, old=None):
             total = total + p
         return total
 
-    def by_piece(parts):
-        return [add_up(parts[i:i + PIECE]) for i in range(0, len(parts), PIECE)]
+    def in_parts(parts, size):
+        return [add_up(parts[i:i + size]) for i in range(0, len(parts), size)]
 
     out = np.zeros((vocab, width), dtype=np.float32) if old is None else old.astype(np.float32)
     for v, parts in rows.items():
         if len(parts) > PIECE:
-            total = add_up(by_piece(by_piece(parts)))
+            total = add_up(in_parts(in_parts(parts, PIECE), RUN))
         else:
             total = add_up(parts)
         total = total * np.float32(scale)

@@ -72,6 +72,7 @@ struct SortPass {
     int32_t bins;          // digits in use
     int32_t* hist;         // [blocks][bins] counts; scanned: sums of the blocks before, then bins totals
     int32_t scanned;
+    uint8_t* named;        // embedding gradient: a byte per table row, one if a key names it
 };
 
 struct PlanArgs {
@@ -127,6 +128,7 @@ struct EmbeddingGradArgs {
     RankSpans tokens;
     const int32_t* keys;   // sorted ids; vocab for those outside the table
     const int32_t* vals;   // position in the sequence of all ranks' tokens
+    const uint8_t* named;  // [vocab], one for a row that some token names
     float* partial;        // [blocks of kPiece entries][2][width]
     int64_t vocab;
     int64_t shard;
@@ -135,7 +137,9 @@ struct EmbeddingGradArgs {
     int32_t accumulate;
     int32_t window;        // sorted entries per workgroup, a power of two up to kPiece
     int32_t windows;
-    int32_t fill_groups;   // groups of 64 table rows to be cleared where no id names them
+    int32_t fill_rows;     // table rows per workgroup that clears those no id names, a power of two up to 64
+    int32_t fill_groups;
+    int32_t spacing;       // the fewer of the two kinds of workgroups are the multiples of this
     int32_t chunks;        // column pieces of a row, one workgroup each
 };
 

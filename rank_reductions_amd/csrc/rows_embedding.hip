@@ -73,7 +73,7 @@ __global__ __launch_bounds__(kRowThreads) void embedding_kernel(EmbeddingArgs a)
 // ---------------------------------------------------------------- sorting the ids
 
 // One pass's places over one block.
-template <bool FIRST>
+template <bool FIRST, bool LAST>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortPass s) {
     __shared__ int32_t count[kSortWaves * kSortBins];
     __shared__ int32_t start[kSortBins];
@@ -88,12 +88,15 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortPass s) {
 #pragma unroll
     for (int k = 0; k < kStrips; ++k)
         if (!sort_entry<FIRST>(s, rank, block, at + k * kWave, &key[k], &val[k])) key[k] = -1;
+    BlockSums sums;
+    sums.load(s);
     for (int d = threadIdx.x; d < s.bins; d += kSortThreads) {
         before[d] = start[d] = 0;
         for (int w = 0; w < kSortWaves; ++w) count[w * kSortBins + d] = 0;
     }
     __syncthreads();
-    block_sums(s, before, start);
+    sums.add(s, before, start);
+    __syncthreads();
     exclusive_sum<kSortThreads>(start, s.bins, carry);
     for (int d = threadIdx.x; d < s.bins; d += kSortThreads) start[d] += before[d];
 #pragma unroll
@@ -107,94 +110,125 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortPass s) {
         if (has) {
             s.out_keys[place] = key[k];
             s.out_vals[place] = val[k];
+            if (LAST && s.named && key[k] < s.key_limit) s.named[key[k]] = 1;  // whoever else writes it writes the same
         }
     }
 }
 
-// All passes in one workgroup, for few ids: each pass reads what the one
-// before wrote (the first the ids) and the last writes to `to`, so the
-// buffers alternate from there.
-constexpr int kSmallWaves = 8;
-constexpr int kSmallIds = 8192;
-constexpr int kSmallStrips = kSmallIds / (kSmallWaves * kWave);
+// All passes in one workgroup, for few ids: keys and positions stay in LDS.
+constexpr int kSmallThreads = 512;
+constexpr int kSmallWaves = kSmallThreads / kWave;
+constexpr int kSmallStrips = 8;
+constexpr int kSmallIds = kSmallThreads * kSmallStrips;
+constexpr int kSmallBits = 9;  // a digit per thread
 struct SmallSort {
-    SortPass first;    // spans, ids, id64, key_limit
-    int32_t* keys[2];  // pass p writes to [(passes - 1 - p) & 1]
-    int32_t* vals[2];
+    SortPass first;  // spans, ids, id64, key_limit, out_keys, out_vals
     int32_t passes;
-    int32_t bits;      // of each pass
+    int32_t bits;    // of each pass
 };
-__global__ __launch_bounds__(kSmallWaves* kWave) void sort_small_kernel(SmallSort a) {
-    __shared__ int32_t count[kSmallWaves * kSortBins];
-    __shared__ int32_t start[kSortBins];
+__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SmallSort a) {
+    __shared__ int32_t count[kSmallWaves][1 << kSmallBits];
+    __shared__ int32_t keys[kSmallIds];
+    __shared__ int32_t vals[kSmallIds];
     __shared__ int32_t carry[kSmallWaves];
-    constexpr int kThreads = kSmallWaves * kWave;
     const int lane = lane_id(), wave = threadIdx.x / kWave;
     const int32_t n = a.first.spans.total();
-    const int strips = (n + kThreads - 1) / kThreads;
+    const int strips = (n + kSmallThreads - 1) / kSmallThreads;
     const int32_t at = wave * strips * kWave + lane;
-    const int bins = 1 << a.bits;
+    const int bins = 1 << a.bits, d = threadIdx.x;
+    int32_t key[kSmallStrips], val[kSmallStrips];
+#pragma unroll
+    for (int k = 0; k < kSmallStrips; ++k) {
+        const int32_t j = at + k * kWave;
+        key[k] = -1;
+        val[k] = j;
+        if (k < strips && j < n) {
+            int32_t i;
+            const int rank = rank_of(a.first.spans, j, &i);
+            key[k] = first_key(a.first, rank, i);
+        }
+    }
+    if (a.first.named) clear_named(a.first, 0, 1, kSmallThreads);
     for (int p = 0; p < a.passes; ++p) {
         const int shift = p * a.bits;
-        for (int d = threadIdx.x; d < bins; d += kThreads)
-            for (int w = 0; w < kSmallWaves; ++w) count[w * kSortBins + d] = 0;
-        __syncthreads();
-        const int from = (a.passes - p) & 1, to = from ^ 1;
-        int32_t key[kSmallStrips], val[kSmallStrips];
+        if (d < bins)
 #pragma unroll
-        for (int k = 0; k < kSmallStrips; ++k) {
-            const int32_t j = at + k * kWave;
-            key[k] = -1;
-            val[k] = j;
-            if (k < strips && j < n) {
-                if (p == 0) {
-                    int32_t i;
-                    const int rank = rank_of(a.first.spans, j, &i);
-                    key[k] = first_key(a.first, rank, i);
-                } else {
-                    key[k] = a.keys[from][j];
-                    val[k] = a.vals[from][j];
-                }
-                atomicAdd(&count[wave * kSortBins + ((key[k] >> shift) & (bins - 1))], 1);
+            for (int w = 0; w < kSmallWaves; ++w) count[w][d] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kSmallStrips; ++k)
+            if (key[k] >= 0) atomicAdd(&count[wave][(key[k] >> shift) & (bins - 1)], 1);
+        __syncthreads();
+        // where each wave's entries of digit d begin
+        int32_t c[kSmallWaves], sum = 0;
+#pragma unroll
+        for (int w = 0; w < kSmallWaves; ++w) {
+            c[w] = d < bins ? count[w][d] : 0;
+            sum += c[w];
+        }
+        int32_t incl = sum;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+            const int32_t up = __shfl_up(incl, o);
+            incl += lane >= o ? up : 0;
+        }
+        if (lane == kWave - 1) carry[wave] = incl;
+        __syncthreads();
+        int32_t run = incl - sum;
+        for (int w = 0; w < wave; ++w) run += carry[w];
+        if (d < bins)
+#pragma unroll
+            for (int w = 0; w < kSmallWaves; ++w) {
+                count[w][d] = run;
+                run += c[w];
             }
-        }
         __syncthreads();
-        for (int d = threadIdx.x; d < bins; d += kThreads) {
-            int32_t sum = 0;
-            for (int w = 0; w < kSmallWaves; ++w) sum += count[w * kSortBins + d];
-            start[d] = sum;
-        }
-        __syncthreads();
-        exclusive_sum<kThreads>(start, bins, carry);
-        wave_starts<kSmallWaves>(count, start, bins);
+        const bool last = p + 1 == a.passes;
 #pragma unroll
         for (int k = 0; k < kSmallStrips; ++k) {
             if (k < strips) {  // alike in all lanes
                 const bool has = key[k] >= 0;
-                const int32_t place = strip_rank((key[k] >> shift) & (bins - 1), a.bits, has, &count[wave * kSortBins]);
+                const int32_t place = strip_rank((key[k] >> shift) & (bins - 1), a.bits, has, count[wave]);
                 if (has) {
-                    a.keys[to][place] = key[k];
-                    a.vals[to][place] = val[k];
+                    (last ? a.first.out_keys : keys)[place] = key[k];
+                    (last ? a.first.out_vals : vals)[place] = val[k];
+                    if (last && a.first.named && key[k] < a.first.key_limit) a.first.named[key[k]] = 1;
                 }
             }
         }
-        __threadfence_block();
+        if (last) break;
         __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kSmallStrips; ++k) {
+            const int32_t j = at + k * kWave;
+            if (k < strips && j < n) {
+                key[k] = keys[j];
+                val[k] = vals[j];
+            }
+        }
     }
 }
 
 // ---------------------------------------------------------------- summing
 
 constexpr int kSumThreads = 256;
-constexpr int kAhead = 4;  // rows of dy in flight per lane
-constexpr int64_t kSumGroups = 2048;  // summing workgroups that keep the GPU busy
+// Workgroups that keep the GPU busy: 65536 tokens of 4096 columns took 304 us
+// with windows of 64 (2048 workgroups), 292 with 32 (4096), 307 with 16.
+constexpr int64_t kSumGroups = 4096;
+constexpr int64_t kFillGroups = 1000;  // their stores need no waiting for
 
-// First of the sorted keys in [lo, hi) that is not below `key`.
-__device__ __forceinline__ int32_t lower_bound(const int32_t* keys, int32_t lo, int32_t hi, int64_t key) {
+// First of the sorted keys in [lo, hi) that is not below `key`, for arguments
+// that all lanes share: 64 probes at a time, so that
+// 65536 keys take three dependent loads rather than 16 (the keys come from
+// another launch, mostly from beyond this XCD's L2).
+__device__ __forceinline__ int32_t wave_lower_bound(const int32_t* keys, int32_t lo, int32_t hi, int64_t key) {
     while (lo < hi) {
-        const int32_t mid = lo + (hi - lo) / 2;
-        if (keys[mid] < key) lo = mid + 1;
-        else hi = mid;
+        const int32_t step = (hi - lo + (kWave - 1)) / kWave;
+        const int64_t p = lo + (int64_t)lane_id() * step;
+        const int less = __popcll(__ballot(p < hi && keys[p < hi ? p : lo] < key));
+        if (less == 0) break;
+        hi = (int32_t)min((int64_t)hi, lo + (int64_t)less * step);
+        lo += (less - 1) * step + 1;
     }
     return lo;
 }
@@ -206,24 +240,69 @@ __device__ __forceinline__ typename G::E* table_row(const EmbeddingGradArgs& a, 
     return static_cast<typename G::E*>(a.table[shard]) + (v - shard * a.shard) * a.width;
 }
 
+// A lane's columns: as many as one of its stores takes, in kParts pieces a
+// wave's width apart, so that every store of a wave is of consecutive bytes
+// (two 16-byte stores to the two halves of each lane's 32 bytes wrote half
+// lines: FIGHALF).
+template <class T, class G>
+struct Cols {
+    static constexpr int kPart = T::n < G::n ? T::n : G::n;
+    static constexpr int kParts = T::n / kPart;
+    static constexpr int kWords = kPart * (int)sizeof(typename T::E) / 4;
+};
+typedef uint32_t u32x2m __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// `rem` elements of a part, the others zero.
+template <class T, int PART, int WORDS>
+__device__ __forceinline__ void load_part(const typename T::E* src, int rem, uint32_t* w) {
+    if (rem == PART) {
+        if constexpr (WORDS == 4) {
+            const u32x4 v = load16<T>(src);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = v[i];
+        } else {
+            const u32x2 v = *reinterpret_cast<const u32x2m*>(src);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) w[i] = v[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < PART; ++i) {
+            if (i >= rem) continue;
+            if constexpr (sizeof(typename T::E) == 4) w[i] = __builtin_bit_cast(uint32_t, src[i]);
+            else w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, src[i]) << (16 * (i % 2));
+        }
+    }
+}
+template <class T>
+__device__ __forceinline__ float element_of(const uint32_t* w, int i) {
+    if constexpr (sizeof(typename T::E) == 4) {
+        const uint32_t u = w[i];
+        return __builtin_bit_cast(float, u);
+    } else {
+        const uint16_t u = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+        return T::load(__builtin_bit_cast(typename T::E, u));
+    }
+}
+
+// Writes N elements (G::n of them) of a table row, or `rem`.
 template <class G, int N>
-__device__ __forceinline__ void finish_row(const EmbeddingGradArgs& a, int64_t v, int64_t col, int rem, const float* sum) {
-    typename G::E* row = table_row<G>(a, v) + col;
-    float f[N];
+__device__ __forceinline__ void finish_row(const EmbeddingGradArgs& a, typename G::E* row, int rem, const float* sum) {
+    static_assert(N == G::n);
     if (rem == N) {
+        float f[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) f[i] = sum[i] * a.scale;
         if (a.accumulate) {
+            float old[N];
+            G::unpack(load16<G>(row), old);
 #pragma unroll
-            for (int i = 0; i < N; i += G::n) {
-                float old[G::n];
-                G::unpack(load16<G>(row + i), old);
-#pragma unroll
-                for (int j = 0; j < G::n; ++j) f[i + j] += old[j];
-            }
+            for (int i = 0; i < N; ++i) f[i] += old[i];
         }
-#pragma unroll
-        for (int i = 0; i < N; i += G::n) store16<G>(row + i, G::pack(f + i));
+        store16_past<G>(row, G::pack(f));
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -231,29 +310,36 @@ __device__ __forceinline__ void finish_row(const EmbeddingGradArgs& a, int64_t v
     }
 }
 
-// T: type of dy; G: type of the table's gradient.
-template <class T, class G>
+// T: type of dy; G: type of the table's gradient; AHEAD: rows of dy in flight
+// per lane.
+template <class T, class G, int AHEAD>
 __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGradArgs a) {
     using E = typename T::E;
     __shared__ int32_t keys[2 * kPiece + 2];  // of the positions p0 - 1 .. p0 + window + kPiece
     __shared__ const E* rows[2 * kPiece];
     const int lane = lane_id();
     const int32_t n = a.tokens.total();
-    const int64_t group = group_index();
+    int64_t group = group_index();
     if (group >= (int64_t)a.windows + a.fill_groups) return;
-    if (group >= a.windows) {
-        // clear the rows of 64 ids that no token names
-        const int64_t first = (group - a.windows) * kWave;
-        const int32_t at = first + lane < a.vocab ? lower_bound(a.keys, 0, n, first + lane) : n;
-        const bool hit = at < n && a.keys[at] == first + lane;
-        uint64_t clear = __ballot(first + lane < a.vocab && !hit);
+    // summing and clearing workgroups take turns, so that both are under way
+    // at any time
+    const int32_t fewer = min(a.windows, a.fill_groups), turn = (int32_t)group / a.spacing;
+    const bool of_fewer = (int32_t)group % a.spacing == 0 && turn < fewer;
+    const bool clears = of_fewer == (a.fill_groups < a.windows);
+    group = of_fewer ? turn : group - min(fewer, turn + 1);
+    if (clears) {
+        // clear the rows of these ids that no token names
+        const int64_t first = group * a.fill_rows;
+        const int64_t v = first + lane;
+        const bool mine = lane < a.fill_rows && v < a.vocab;
+        uint64_t clear = __ballot(mine && !(n && a.named[v]));
         const int64_t lo = (int64_t)blockIdx.z * (kSumThreads * T::n), hi = min(lo + kSumThreads * T::n, a.width);
         while (clear) {
             const int j = __builtin_ctzll(clear);
             clear &= clear - 1;
             typename G::E* row = table_row<G>(a, first + j);
             for (int64_t c = lo + threadIdx.x * G::n; c < hi; c += kSumThreads * G::n) {
-                if (c + G::n <= hi) store16<G>(row + c, u32x4{0, 0, 0, 0});
+                if (c + G::n <= hi) store16_past<G>(row + c, u32x4{0, 0, 0, 0});
                 else
                     for (int64_t i = c; i < hi; ++i) row[i] = G::store(0.0f);
             }
@@ -291,7 +377,7 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
     int begin = begins ? (int)__builtin_ctzll(begins) : 2 * kPiece;
     int carried = 0;  // positions below it belong to a piece of an id that began earlier
     if (key[0] >= 0 && key[0] < none && key[0] == key[-1]) {
-        const int32_t s = lower_bound(a.keys, 0, p0, key[0]);
+        const int32_t s = wave_lower_bound(a.keys, 0, p0, key[0]);
         if (s + (int64_t)kPiece < n && a.keys[s + kPiece] == key[0]) {
             const int ps = (int)(((int64_t)p0 - s + kPiece - 1) / kPiece * kPiece + s - p0);
             const int end = begins ? begin : last_end;  // of the id, or past the piece
@@ -311,104 +397,141 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
     float* const carried_out = a.partial + 2 * (int64_t)((p0 + begin) / kPiece) * a.width;
     float* const hot_out = a.partial + (2 * (int64_t)((p0 + hot) / kPiece) + 1) * a.width;
 
-    const int64_t col = ((int64_t)blockIdx.z * kSumThreads + threadIdx.x) * T::n;
-    const int rem = (int)max((int64_t)0, min((int64_t)T::n, a.width - col));
-    if (rem == 0) return;
-    auto fetch = [&](int j, float* f) {
-        const E* src = rows[j] + col;
-        if (rem == T::n) T::unpack(load16<T>(src), f);
-        else {
+    using C = Cols<T, G>;
+    int64_t col[C::kParts];
+    int rem[C::kParts];
 #pragma unroll
-            for (int i = 0; i < T::n; ++i) f[i] = i < rem ? T::load(src[i]) : 0.0f;
+    for (int h = 0; h < C::kParts; ++h) {
+        col[h] = ((int64_t)blockIdx.z * kSumThreads + threadIdx.x / kWave * kWave) * T::n + (h * kWave + lane) * C::kPart;
+        rem[h] = (int)max((int64_t)0, min((int64_t)C::kPart, a.width - col[h]));
+    }
+    float acc[C::kParts][C::kPart] = {};
+    for (int j0 = begin; j0 < end; j0 += AHEAD) {
+        uint32_t w[AHEAD][C::kParts][C::kWords];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (j0 + u < end) {
+#pragma unroll
+                for (int h = 0; h < C::kParts; ++h) load_part<T, C::kPart, C::kWords>(rows[j0 + u] + col[h], rem[h], w[u][h]);
+            }
         }
-    };
-    float acc[T::n] = {};
-    for (int j0 = begin; j0 < end; j0 += kAhead) {
-        float f[kAhead][T::n];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (j0 + u < end) fetch(j0 + u, f[u]);
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < AHEAD; ++u) {
             const int j = j0 + u;
-            if (j >= end) break;
+            if (j < end) {
 #pragma unroll
-            for (int i = 0; i < T::n; ++i) acc[i] += f[u][i];
-            // an id's last entry, or a piece's
-            if (j + 1 == end || j + 1 == carried || key[j + 1] != key[j]) {
-                if (j < carried || j >= hot) {
-                    float* out = (j < carried ? carried_out : hot_out) + col;
+                for (int h = 0; h < C::kParts; ++h)
 #pragma unroll
-                    for (int i = 0; i < T::n; ++i)
-                        if (i < rem) out[i] = acc[i];
-                } else {
-                    finish_row<G, T::n>(a, key[j], col, rem, acc);
+                    for (int i = 0; i < C::kPart; ++i) acc[h][i] += element_of<T>(w[u][h], i);
+                // an id's last entry, or a piece's
+                if (j + 1 == end || j + 1 == carried || key[j + 1] != key[j]) {
+                    const bool piece = j < carried || j >= hot;
+                    float* out = j < carried ? carried_out : hot_out;
+                    typename G::E* row = piece ? nullptr : table_row<G>(a, key[j]);
+#pragma unroll
+                    for (int h = 0; h < C::kParts; ++h) {
+                        if (!piece) {
+                            finish_row<G, C::kPart>(a, row + col[h], rem[h], acc[h]);
+                        } else if (rem[h] == C::kPart) {
+#pragma unroll
+                            for (int i = 0; i < C::kPart; i += 4) store16<F32>(out + col[h] + i, F32::pack(acc[h] + i));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < C::kPart; ++i)
+                                if (i < rem[h]) out[col[h] + i] = acc[h][i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < C::kPart; ++i) acc[h][i] = 0.0f;
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < T::n; ++i) acc[i] = 0.0f;
             }
         }
     }
 }
 
-// Joins the pieces of the long id that begins in the block of kPiece entries,
-// if there is one: runs of kPiece pieces, added in order.  Piece i is there if
-// the entry kPiece i past the id's first is still the id's; it lies i blocks on.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinCols = kJoinThreads * 4;
-constexpr int kJoinAhead = 16;
+// Joins the pieces of the long ids that begin in some blocks of kPiece entries,
+// at most one in each: runs of kRun pieces, each summed by a wave of its own with
+// all its loads in flight, added in order.  Piece i is there if the entry
+// kPiece i past the id's first is still the id's; it lies i blocks on.
+constexpr int kRun = 16;
+constexpr int kJoinRuns = 4;                  // at a time
+constexpr int kJoinCols = kWave * 4;          // of a wave
+constexpr int kJoinSides = 1;                 // waves side by side
+constexpr int kJoinThreads = kJoinRuns * kJoinSides * kWave;
+constexpr int kJoinBlocks = 8;                // blocks of entries per workgroup
 template <class G>
 __global__ __launch_bounds__(kJoinThreads) void embedding_join_kernel(EmbeddingGradArgs a) {
-    const int lane = lane_id();
+    __shared__ float sums[kJoinRuns][kJoinSides * kJoinCols];
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
     const int32_t n = a.tokens.total();
-    const int64_t block = group_index(), p = block * kPiece + lane;
-    const int32_t key = p < n ? a.keys[p] : -1;
-    const int32_t before = p > 0 && p < n ? a.keys[p - 1] : -1;
-    const int32_t past = p + kPiece < n ? a.keys[p + kPiece] : -1;
-    const uint64_t longs = __ballot(key >= 0 && key < a.vocab && before != key && past == key);
-    if (!longs) return;
-    const int at = (int)__builtin_ctzll(longs);
-    const int32_t id = __shfl(key, at);
-    const int64_t s = block * kPiece + at;
-    const int64_t col = (int64_t)blockIdx.z * kJoinCols + threadIdx.x * 4;
+    const int run = wave / kJoinSides, here = (wave % kJoinSides) * kJoinCols + lane * 4;
+    const int64_t col = (int64_t)blockIdx.z * (kJoinSides * kJoinCols) + here;
     const int rem = (int)max((int64_t)0, min((int64_t)4, a.width - col));
-    float total[4] = {};
-    for (int64_t base = 0;; base += kPiece) {
-        const int64_t q = s + (base + lane) * kPiece;
-        const int pieces = __popcll(__ballot(q < n && a.keys[q] == id));  // of this run
-        // the first piece of all is the second kind of its block
-        const float* src = a.partial + 2 * (block + base) * a.width + col;
-        float sum[4] = {};
-        for (int i0 = 0; i0 < pieces; i0 += kJoinAhead) {
-            float f[kJoinAhead][4];
+    // the long ids that begin in these blocks (alike in all waves), which lie
+    // apart, since common ids lie together
+    const int64_t groups = (((int64_t)n + kPiece - 1) / kPiece + kJoinBlocks - 1) / kJoinBlocks;
+    if (group_index() >= groups) return;
+    int32_t key[kJoinBlocks];
+    uint64_t longs[kJoinBlocks];
 #pragma unroll
-            for (int u = 0; u < kJoinAhead; ++u) {
-                if (i0 + u < pieces) {
-                    const float* row = src + (2 * (int64_t)(i0 + u) + (base + i0 + u == 0)) * a.width;
+    for (int b = 0; b < kJoinBlocks; ++b) {
+        const int64_t p = (group_index() + b * groups) * kPiece + lane;
+        key[b] = p < n ? a.keys[p] : -1;
+        const int32_t before = p > 0 && p < n ? a.keys[p - 1] : -1;
+        const int32_t past = p + kPiece < n ? a.keys[p + kPiece] : -1;
+        longs[b] = __ballot(key[b] >= 0 && key[b] < a.vocab && before != key[b] && past == key[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < kJoinBlocks; ++b) {
+        if (!longs[b]) continue;
+        const int64_t block = group_index() + b * groups;
+        const int at = (int)__builtin_ctzll(longs[b]);
+        const int32_t id = __shfl(key[b], at);
+        const int64_t s = block * kPiece + at;
+        float total[4] = {};
+        for (int64_t base = 0;; base += kJoinRuns * kRun) {
+            const int64_t q = s + (base + lane) * kPiece;
+            const int pieces = __popcll(__ballot(q < n && a.keys[q] == id));  // of these runs
+            const int mine = max(0, min(kRun, pieces - run * kRun));
+            // the first piece of all is the second kind of its block
+            const float* src = a.partial + 2 * (block + base + run * kRun) * a.width + col;
+            float f[kRun][4];
+#pragma unroll
+            for (int u = 0; u < kRun; ++u) {
+                if (u < mine) {
+                    const float* row = src + (2 * (int64_t)u + (base + run * kRun + u == 0)) * a.width;
                     if (rem == 4) F32::unpack(load16<F32>(row), f[u]);
                     else
 #pragma unroll
                         for (int c = 0; c < 4; ++c) f[u][c] = c < rem ? row[c] : 0.0f;
                 }
             }
+            float sum[4] = {};
 #pragma unroll
-            for (int u = 0; u < kJoinAhead; ++u) {
-                if (i0 + u < pieces) {
+            for (int u = 0; u < kRun; ++u) {
+                if (u < mine) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) sum[c] += f[u][c];
                 }
             }
+            *reinterpret_cast<u32x4*>(&sums[run][here]) = F32::pack(sum);
+            __syncthreads();
+            for (int w = 0; w < kJoinRuns && w * kRun < pieces; ++w) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) total[c] += sums[w][here + c];
+            }
+            __syncthreads();
+            if (pieces < kJoinRuns * kRun) break;
         }
+        if (run == 0) {
+            typename G::E* row = table_row<G>(a, id) + col;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) total[c] += sum[c];
-        if (pieces < kPiece) break;
+            for (int c = 0; c < 4; ++c)
+                if (c < rem) row[c] = G::store((a.accumulate ? G::load(row[c]) : 0.0f) + total[c] * a.scale);
+        }
     }
-    if (rem == 0) return;
-    typename G::E* row = table_row<G>(a, id) + col;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        if (c < rem) row[c] = G::store((a.accumulate ? G::load(row[c]) : 0.0f) + total[c] * a.scale);
 }
+static_assert(kJoinRuns * kRun == kWave, "one lane looks for each piece");
 
 int bits_of(int64_t values) {
     int b = 0;
@@ -416,10 +539,10 @@ int bits_of(int64_t values) {
     return b;
 }
 
-// The sort's passes over keys in [0, vocab]: as few as kSortBins allows, of
-// equal width.
-void passes_of(int64_t vocab, int* passes, int* bits) {
-    const int all = bits_of(vocab + 1), most = bits_of(kSortBins);
+// The sort's passes over keys in [0, vocab]: as few as the digits' width
+// allows, of equal width.
+void passes_of(int64_t vocab, int64_t n, int* passes, int* bits) {
+    const int all = bits_of(vocab + 1), most = n <= kSmallIds ? kSmallBits : bits_of(kSortBins);
     *passes = (all + most - 1) / most;
     *bits = (all + *passes - 1) / *passes;
 }
@@ -428,7 +551,7 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Where the gradient's workspace keeps what.
 struct Layout {
-    int64_t keys[2], vals[2], hist, partial, bytes;
+    int64_t keys[2], vals[2], hist, named, partial, bytes;
 };
 Layout layout_of(const RankSpans& tokens, int64_t vocab, int64_t width) {
     Layout l{};
@@ -440,10 +563,11 @@ Layout layout_of(const RankSpans& tokens, int64_t vocab, int64_t width) {
     l.vals[1] = 3 * list;
     l.hist = 4 * list;
     int passes, bits;
-    passes_of(vocab, &passes, &bits);
+    passes_of(vocab, n, &passes, &bits);
     // the first pass cuts each rank's ids into blocks of their own
     const int64_t hist = n <= kSmallIds ? 0 : ((int64_t)sort_blocks(tokens).total() + 1) * (int64_t(1) << bits) * 4;
-    l.partial = l.hist + align256(hist);
+    l.named = l.hist + align256(hist);
+    l.partial = l.named + align256(vocab);
     l.bytes = l.partial + (n + kPiece - 1) / kPiece * 2 * width * 4;
     return l;
 }
@@ -460,16 +584,26 @@ int run_embedding(EmbeddingArgs a, hipStream_t s) {
 template <class T, class G>
 int run_sum(EmbeddingGradArgs a, hipStream_t s) {
     const int64_t cols = kSumThreads * T::n, chunks = (a.width + cols - 1) / cols, n = a.tokens.total();
-    // shorter windows where whole pieces would leave the GPU idle
+    // shorter windows, and fewer rows to clear at once, where the largest would
+    // leave the GPU idle
     a.window = kPiece;
     while (a.window > 4 && n / a.window * chunks < kSumGroups) a.window /= 2;
     a.windows = (int32_t)((n + a.window - 1) / a.window);
+    a.fill_rows = kWave;
+    while (a.fill_rows > 4 && a.vocab / a.fill_rows * chunks < kFillGroups) a.fill_rows /= 2;
+    a.fill_groups = a.accumulate ? 0 : (int32_t)((a.vocab + a.fill_rows - 1) / a.fill_rows);
+    const int32_t fewer = a.windows < a.fill_groups ? a.windows : a.fill_groups;
+    a.spacing = fewer ? (a.windows + a.fill_groups) / fewer : 1;
     const int64_t groups = (int64_t)a.windows + a.fill_groups;
+    // more rows in flight where few workgroups run and an id's rows one after
+    // another are what takes the time: 1450 tokens FIGAHEAD; 65536 tokens 292
+    // with four, 316 with eight
     if (groups)
-        hipLaunchKernelGGL((embedding_grad_kernel<T, G>), grid_of(groups, chunks), dim3(kSumThreads), 0, s, a);
-    if (a.tokens.total() > kPiece)
+        hipLaunchKernelGGL((a.window <= 16 ? embedding_grad_kernel<T, G, 16> : embedding_grad_kernel<T, G, 4>),
+                           grid_of(groups, chunks), dim3(kSumThreads), 0, s, a);
+    if (n > kPiece)
         hipLaunchKernelGGL(embedding_join_kernel<G>,
-                           grid_of(((int64_t)a.tokens.total() + kPiece - 1) / kPiece, (a.width + kJoinCols - 1) / kJoinCols),
+                           grid_of(((n + kPiece - 1) / kPiece + kJoinBlocks - 1) / kJoinBlocks, (a.width + kJoinSides * kJoinCols - 1) / (kJoinSides * kJoinCols)),
                            dim3(kJoinThreads), 0, s, a);
     return hipGetLastError();
 }
@@ -495,18 +629,18 @@ int launch_embedding_grad(EmbeddingGradArgs a, SortPass sort, int dtype, int gra
         vals[i] = reinterpret_cast<int32_t*>(ws + l.vals[i]);
     }
     int passes, bits;
-    passes_of(a.vocab, &passes, &bits);
+    passes_of(a.vocab, n, &passes, &bits);
     sort.drop = 0;
+    sort.named = a.accumulate || !n ? nullptr : reinterpret_cast<uint8_t*>(ws + l.named);
+    a.named = sort.named;
     if (n > 0 && n <= kSmallIds) {
         SmallSort m{};
         m.first = sort;
-        for (int i = 0; i < 2; ++i) {
-            m.keys[i] = keys[i];
-            m.vals[i] = vals[i];
-        }
+        m.first.out_keys = keys[0];
+        m.first.out_vals = vals[0];
         m.passes = passes;
         m.bits = bits;
-        hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(kSmallWaves * kWave), 0, s, m);
+        hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(kSmallThreads), 0, s, m);
     } else if (n > 0) {
         sort.bits = bits;
         sort.bins = 1 << bits;
@@ -528,14 +662,15 @@ int launch_embedding_grad(EmbeddingGradArgs a, SortPass sort, int dtype, int gra
             const int32_t blocks = sort.blocks.total();
             if (p == 0) launch_counts<true>(sort, s);
             else launch_counts<false>(sort, s);
-            if (p == 0) hipLaunchKernelGGL(sort_place_kernel<true>, dim3(blocks), dim3(kSortThreads), 0, s, sort);
-            else hipLaunchKernelGGL(sort_place_kernel<false>, dim3(blocks), dim3(kSortThreads), 0, s, sort);
+            const bool last = p + 1 == passes;
+            auto place = p == 0 ? (last ? sort_place_kernel<true, true> : sort_place_kernel<true, false>)
+                                : (last ? sort_place_kernel<false, true> : sort_place_kernel<false, false>);
+            hipLaunchKernelGGL(place, dim3(blocks), dim3(kSortThreads), 0, s, sort);
         }
     }
     a.keys = keys[0];
     a.vals = vals[0];
     a.partial = reinterpret_cast<float*>(ws + l.partial);
-    a.fill_groups = a.accumulate ? 0 : (int32_t)((a.vocab + kWave - 1) / kWave);
     if (dtype == RC_F32) return run_sum<F32, F32>(a, s);
     if (dtype == RC_F16) return grad_dtype == RC_F32 ? run_sum<F16, F32>(a, s) : run_sum<F16, F16>(a, s);
     return grad_dtype == RC_F32 ? run_sum<BF16, F32>(a, s) : run_sum<BF16, BF16>(a, s);

@@ -44,12 +44,15 @@ __global__ __launch_bounds__(kSortThreads) void plan_place_kernel(PlanArgs a) {
         int32_t val;
         if (!sort_entry<true>(s, rank, block, at + k * kWave, &key[k], &val)) key[k] = -1;
     }
+    BlockSums sums;
+    sums.load(s);
     for (int d = threadIdx.x; d < s.bins; d += kSortThreads) {
         base[d] = total[d] = 0;
         for (int w = 0; w < kSortWaves; ++w) count[w * kSortBins + d] = 0;
     }
     __syncthreads();
-    block_sums(s, base, total);
+    sums.add(s, base, total);
+    __syncthreads();
     for (int d = threadIdx.x; d < s.bins; d += kSortThreads) start[d] = total[d];
     __syncthreads();
     exclusive_sum<kSortThreads>(start, s.bins, carry);

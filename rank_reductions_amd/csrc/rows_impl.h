@@ -91,6 +91,12 @@ __device__ __forceinline__ void store16(typename T::E* p, u32x4 v) {
     *reinterpret_cast<u32x4m*>(p) = v;
 }
 
+// A store that goes past the caches, for what is not read again soon.
+template <class T>
+__device__ __forceinline__ void store16_past(typename T::E* p, u32x4 v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4m*>(p));
+}
+
 // The rank whose span holds item i (spans may be empty), and the item's index within it.
 __device__ __forceinline__ int rank_of(const RankSpans& s, int32_t i, int32_t* local) {
     int r = 0;

@@ -72,6 +72,12 @@ __device__ __forceinline__ int32_t strip_rank(int digit, int bits, bool has, vol
     return base + below;
 }
 
+// This workgroup's share of clearing s.named (16-byte aligned, and padded to 16).
+__device__ __forceinline__ void clear_named(const SortPass& s, int64_t group, int64_t groups, int threads) {
+    u32x4* at = reinterpret_cast<u32x4*>(s.named);
+    for (int64_t i = group * threads + threadIdx.x; i < (s.key_limit + 15) / 16; i += groups * threads) at[i] = u32x4{0, 0, 0, 0};
+}
+
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortPass s) {
     __shared__ int32_t count[kSortBins];
@@ -84,6 +90,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortPass s) {
         if (!sort_entry<FIRST>(s, rank, block, k * kSortThreads + threadIdx.x, &key[k], &val)) key[k] = -1;
     }
     for (int d = threadIdx.x; d < s.bins; d += kSortThreads) count[d] = 0;
+    if (FIRST && s.named) clear_named(s, blockIdx.x, gridDim.x, kSortThreads);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kStrips; ++k)
@@ -93,9 +100,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortPass s) {
 }
 
 // Up to this many counts, each block adds them up itself: at 16384 a lane
-// reads 64 of them, eight at a time, about 3 us; the launch between took 4.7.
+// reads 64 of them, 32 at a time; the launch between took 4.7 us.
 constexpr int64_t kFusedCounts = 16384;
-constexpr int kBatch = 8;
+constexpr int kBatch = 32;
 
 // Exclusive sums over the blocks, for 64 digits per workgroup; the totals
 // follow the last block's row.
@@ -129,49 +136,58 @@ __global__ __launch_bounds__(kScanWaves* kWave) void sort_scan_kernel(int32_t* h
     if (wave == kScanWaves - 1) hist[(int64_t)blocks * bins + d] = run;
 }
 
-// before[d]: entries of digit d in the blocks before this one; total[d]: in
-// all.  Both are cleared LDS; ends with a barrier.
-__device__ __forceinline__ void block_sums(const SortPass& s, int32_t* before, int32_t* total) {
-    const int32_t blocks = s.blocks.first[kMaxRanks];
-    const int32_t me = blockIdx.x;
-    if (s.scanned) {
-        for (int d = threadIdx.x; d < s.bins; d += kSortThreads) {
-            before[d] = s.hist[(int64_t)me * s.bins + d];
-            total[d] = s.hist[(int64_t)blocks * s.bins + d];
-        }
-        __syncthreads();
-        return;
-    }
-    // lanes past the digits take further blocks: thread t the digit t mod
-    // width, every `parts`-th block
-    int width = 1;
-    while (width < s.bins && width < kSortThreads) width *= 2;
-    const int parts = kSortThreads / width, part = threadIdx.x / width;
-    for (int d = threadIdx.x & (width - 1); d < s.bins; d += width) {
-        int32_t lower = 0, all = 0;
-        for (int b0 = part; b0 < blocks; b0 += parts * kBatch) {
-            int32_t c[kBatch];
+// Entries of a digit in the blocks before this one, and in all, for the digits
+// that a thread looks after: held in registers until add() puts them into LDS,
+// so that their loads are under way together with the block's keys (a barrier
+// waits for every load before it).
+struct BlockSums {
+    static constexpr int kDigits = kSortBins / kSortThreads;
+    int32_t lower[kDigits], all[kDigits];
+    int width;  // threads per set of digits; the sets share out the blocks
+
+    __device__ __forceinline__ void load(const SortPass& s) {
+        const int32_t blocks = s.blocks.first[kMaxRanks], me = blockIdx.x;
+        width = 1;
+        while (width < s.bins && width < kSortThreads) width *= 2;
+        const int parts = kSortThreads / width, part = threadIdx.x / width;
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int b = b0 + u * parts;
-                c[u] = b < blocks ? s.hist[(int64_t)b * s.bins + d] : 0;
+        for (int i = 0; i < kDigits; ++i) {
+            lower[i] = all[i] = 0;
+            const int d = (threadIdx.x & (width - 1)) + i * width;
+            if (d >= s.bins) continue;
+            if (s.scanned) {
+                if (part == 0) {
+                    lower[i] = s.hist[(int64_t)me * s.bins + d];
+                    all[i] = s.hist[(int64_t)blocks * s.bins + d];
+                }
+                continue;
             }
+            for (int b0 = part; b0 < blocks; b0 += parts * kBatch) {
+                int32_t c[kBatch];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                all += c[u];
-                lower += b0 + u * parts < me ? c[u] : 0;
+                for (int u = 0; u < kBatch; ++u) {
+                    const int b = b0 + u * parts;
+                    c[u] = b < blocks ? s.hist[(int64_t)b * s.bins + d] : 0;
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    all[i] += c[u];
+                    lower[i] += b0 + u * parts < me ? c[u] : 0;
+                }
             }
-        }
-        if (parts == 1) {
-            before[d] = lower;
-            total[d] = all;
-        } else {
-            atomicAdd(&before[d], lower);
-            atomicAdd(&total[d], all);
         }
     }
-    __syncthreads();
-}
+    // before[d] and total[d], cleared; a barrier is due on both sides.
+    __device__ __forceinline__ void add(const SortPass& s, int32_t* before, int32_t* total) const {
+#pragma unroll
+        for (int i = 0; i < kDigits; ++i) {
+            const int d = (threadIdx.x & (width - 1)) + i * width;
+            if (d >= s.bins) continue;
+            atomicAdd(&before[d], lower[i]);
+            atomicAdd(&total[d], all[i]);
+        }
+    }
+};
 
 // In-place exclusive sum of v[0..bins) by a workgroup of THREADS; `carry`
 // holds one word per wave.

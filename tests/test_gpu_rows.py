@@ -448,7 +448,7 @@ def test_embedding_and_gradient(case, dtype, off):
             near(f64(got)[r], want[r], (0 if scale == 1.0 else 1.01 * U + h) * np.abs(want[r]) + (scale != 1.0) * TINY[dtype],
                  f"looked up, rank {r}")
         exact, size, count = orc.embedding_grad(ints(ids), f64(d_outs), V, float(np.float32(scale)))
-        depth = np.minimum(count, 64) + np.minimum(-(-count // 64), 64) + -(-count // 4096) + 2
+        depth = np.minimum(count, 64) + np.minimum(-(-count // 64), 16) + -(-count // 1024) + 2
         for out_type in {"f32", dtype}:
             for accumulate in (False, True):
                 held = [normal(g, hi - lo, D, dtype=out_type) for lo, hi in bounds]
