@@ -411,7 +411,7 @@ int rc_route_grad(const rc_route_desc* desc, const int64_t* tokens, const void* 
  *   num_experts  E in [1, RC_MAX_EXPERTS], divisible by R; rank d has the
  *                experts [d*E/R, (d+1)*E/R)
  *   top_k        K in [1, RC_MAX_TOP_K]
- *   width        elements of a row, >= 1
+ *   width        elements of a row, in [1, 2^22]
  *   tokens       [R]
  *   capacity     [R] >= 0: rows that rank d's row buffer holds
  *   experts      [R]: [tokens[r], K]
@@ -463,7 +463,7 @@ int rc_combine_grad(const rc_exchange_desc* desc, const void* const* d_outs, con
  *   grad_dtype  of the table's gradient: RC_F32 or dtype
  *   accumulate  gradient: nonzero adds to what d_tables hold
  *   vocab       in [1, 2^31 - 2]
- *   width       elements of a row, >= 1
+ *   width       elements of a row, in [1, 2^22]
  *   scale       factor of the looked-up rows
  *   tokens      [R]
  *   ids         [R]: [tokens[r]]; an id outside [0, vocab) names no row */

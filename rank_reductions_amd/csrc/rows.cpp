@@ -14,7 +14,7 @@ namespace rc {
 namespace {
 
 constexpr int64_t kMaxItems = 0x7fffffff;              // counts fit 32 bits
-constexpr int64_t kMaxWidth = int64_t(1) << 24;        // elements of a row
+constexpr int64_t kMaxWidth = int64_t(1) << 22;        // elements of a row
 constexpr int64_t kMaxCapacity = 0x7fffffff;
 
 std::string fmt(const char* f, long long a = 0, long long b = 0, long long c = 0) {
@@ -150,7 +150,7 @@ Error check_exchange(const char* what, int R, const rc_exchange_desc* d, bool pl
     x->es = row_element_size(d->dtype);
     if (!plan) {
         if (!x->es) return bad(what, fmt("unknown dtype %lld", d->dtype));
-        if (d->width < 1 || d->width > kMaxWidth) return bad(what, fmt("width %lld outside [1, 2^24]", d->width));
+        if (d->width < 1 || d->width > kMaxWidth) return bad(what, fmt("width %lld outside [1, 2^22]", d->width));
     }
     if (d->num_experts < 1 || d->num_experts > RC_MAX_EXPERTS || d->num_experts % R)
         return bad(what, fmt("num_experts %lld outside [1, 1024] or not divisible by the %lld ranks", d->num_experts, R));
@@ -205,7 +205,7 @@ Error check_embedding(const char* what, int R, const rc_embedding_desc* d, bool 
         x->ges = row_element_size(d->grad_dtype);
     }
     if (d->vocab < 1 || d->vocab > kMaxItems - 1) return bad(what, "vocab outside [1, 2^31 - 2]");
-    if (d->width < 1 || d->width > kMaxWidth) return bad(what, fmt("width %lld outside [1, 2^24]", d->width));
+    if (d->width < 1 || d->width > kMaxWidth) return bad(what, fmt("width %lld outside [1, 2^22]", d->width));
     if (!std::isfinite(d->scale)) return bad(what, "scale is not finite");
     RC_TRY(spans_of(what, R, d->tokens, 1, &x->tokens));
     if (with_ids) RC_TRY(need(what, d->ids, "ids"));

@@ -139,7 +139,7 @@ struct EmbeddingGradArgs {
     int32_t windows;
     int32_t fill_rows;     // table rows per workgroup that clears those no id names, a power of two up to 64
     int32_t fill_groups;
-    int32_t spacing;       // the fewer of the two kinds of workgroups are the multiples of this
+    int32_t spacing;       // the first workgroups at multiples of this clear rows; 0: those behind the windows do
     int32_t chunks;        // column pieces of a row, one workgroup each
 };
 

@@ -212,10 +212,10 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SmallSort a) 
 // ---------------------------------------------------------------- summing
 
 constexpr int kSumThreads = 256;
-// Workgroups that keep the GPU busy: 65536 tokens of 4096 columns took 304 us
-// with windows of 64 (2048 workgroups), 292 with 32 (4096), 307 with 16.
-constexpr int64_t kSumGroups = 4096;
-constexpr int64_t kFillGroups = 1000;  // their stores need no waiting for
+constexpr int kAhead = 2;  // rows of dy in flight per lane
+// Workgroups that keep the GPU busy.
+constexpr int64_t kSumGroups = 8192;
+constexpr int64_t kFillGroups = 4000;
 
 // First of the sorted keys in [lo, hi) that is not below `key`, for arguments
 // that all lanes share: 64 probes at a time, so that
@@ -310,9 +310,8 @@ __device__ __forceinline__ void finish_row(const EmbeddingGradArgs& a, typename 
     }
 }
 
-// T: type of dy; G: type of the table's gradient; AHEAD: rows of dy in flight
-// per lane.
-template <class T, class G, int AHEAD>
+// T: type of dy; G: type of the table's gradient.
+template <class T, class G>
 __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGradArgs a) {
     using E = typename T::E;
     __shared__ int32_t keys[2 * kPiece + 2];  // of the positions p0 - 1 .. p0 + window + kPiece
@@ -320,13 +319,16 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
     const int lane = lane_id();
     const int32_t n = a.tokens.total();
     int64_t group = group_index();
-    if (group >= (int64_t)a.windows + a.fill_groups) return;
-    // summing and clearing workgroups take turns, so that both are under way
-    // at any time
-    const int32_t fewer = min(a.windows, a.fill_groups), turn = (int32_t)group / a.spacing;
-    const bool of_fewer = (int32_t)group % a.spacing == 0 && turn < fewer;
-    const bool clears = of_fewer == (a.fill_groups < a.windows);
-    group = of_fewer ? turn : group - min(fewer, turn + 1);
+    bool clears;
+    if (a.spacing) {
+        const int32_t turn = (int32_t)group / a.spacing;
+        clears = (int32_t)group % a.spacing == 0 && turn < a.fill_groups;
+        group = clears ? turn : group - min(a.fill_groups, turn + 1);
+    } else {
+        clears = group >= a.windows;
+        if (clears) group -= a.windows;
+    }
+    if (group >= (clears ? a.fill_groups : a.windows)) return;
     if (clears) {
         // clear the rows of these ids that no token names
         const int64_t first = group * a.fill_rows;
@@ -406,17 +408,17 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
         rem[h] = (int)max((int64_t)0, min((int64_t)C::kPart, a.width - col[h]));
     }
     float acc[C::kParts][C::kPart] = {};
-    for (int j0 = begin; j0 < end; j0 += AHEAD) {
-        uint32_t w[AHEAD][C::kParts][C::kWords];
+    for (int j0 = begin; j0 < end; j0 += kAhead) {
+        uint32_t w[kAhead][C::kParts][C::kWords];
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
+        for (int u = 0; u < kAhead; ++u) {
             if (j0 + u < end) {
 #pragma unroll
                 for (int h = 0; h < C::kParts; ++h) load_part<T, C::kPart, C::kWords>(rows[j0 + u] + col[h], rem[h], w[u][h]);
             }
         }
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
+        for (int u = 0; u < kAhead; ++u) {
             const int j = j0 + u;
             if (j < end) {
 #pragma unroll
@@ -449,87 +451,71 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
     }
 }
 
-// Joins the pieces of the long ids that begin in some blocks of kPiece entries,
-// at most one in each: runs of kRun pieces, each summed by a wave of its own with
+// Joins the pieces of the long id that begins in the block of kPiece entries,
+// if there is one: runs of kRun pieces, each summed by a wave of its own with
 // all its loads in flight, added in order.  Piece i is there if the entry
-// kPiece i past the id's first is still the id's; it lies i blocks on.
+// kPiece i past the id's first is still the id's; it lies i blocks on.  65536
+// tokens, a hundred long ids: 14.6 us; with eight blocks to a workgroup 18, with
+// 1024 columns to a workgroup 21.
 constexpr int kRun = 16;
-constexpr int kJoinRuns = 4;                  // at a time
-constexpr int kJoinCols = kWave * 4;          // of a wave
-constexpr int kJoinSides = 1;                 // waves side by side
-constexpr int kJoinThreads = kJoinRuns * kJoinSides * kWave;
-constexpr int kJoinBlocks = 8;                // blocks of entries per workgroup
+constexpr int kJoinRuns = 4;          // at a time
+constexpr int kJoinCols = kWave * 4;
 template <class G>
-__global__ __launch_bounds__(kJoinThreads) void embedding_join_kernel(EmbeddingGradArgs a) {
-    __shared__ float sums[kJoinRuns][kJoinSides * kJoinCols];
-    const int lane = lane_id(), wave = threadIdx.x / kWave;
+__global__ __launch_bounds__(kJoinRuns* kWave) void embedding_join_kernel(EmbeddingGradArgs a) {
+    __shared__ __align__(16) float sums[kJoinRuns][kJoinCols];
+    const int lane = lane_id(), run = threadIdx.x / kWave, here = lane * 4;
     const int32_t n = a.tokens.total();
-    const int run = wave / kJoinSides, here = (wave % kJoinSides) * kJoinCols + lane * 4;
-    const int64_t col = (int64_t)blockIdx.z * (kJoinSides * kJoinCols) + here;
+    const int64_t block = group_index(), p = block * kPiece + lane;
+    const int32_t key = p < n ? a.keys[p] : -1;
+    const int32_t before = p > 0 && p < n ? a.keys[p - 1] : -1;
+    const int32_t past = p + kPiece < n ? a.keys[p + kPiece] : -1;
+    const uint64_t longs = __ballot(key >= 0 && key < a.vocab && before != key && past == key);
+    if (!longs) return;  // alike in all waves
+    const int at = (int)__builtin_ctzll(longs);
+    const int32_t id = __shfl(key, at);
+    const int64_t s = block * kPiece + at;
+    const int64_t col = (int64_t)blockIdx.z * kJoinCols + here;
     const int rem = (int)max((int64_t)0, min((int64_t)4, a.width - col));
-    // the long ids that begin in these blocks (alike in all waves), which lie
-    // apart, since common ids lie together
-    const int64_t groups = (((int64_t)n + kPiece - 1) / kPiece + kJoinBlocks - 1) / kJoinBlocks;
-    if (group_index() >= groups) return;
-    int32_t key[kJoinBlocks];
-    uint64_t longs[kJoinBlocks];
+    float total[4] = {};
+    for (int64_t base = 0;; base += kJoinRuns * kRun) {
+        const int64_t q = s + (base + lane) * kPiece;
+        const int pieces = __popcll(__ballot(q < n && a.keys[q < n ? q : s] == id));  // of these runs
+        const int mine = max(0, min(kRun, pieces - run * kRun));
+        // the first piece of all is the second kind of its block
+        const float* src = a.partial + 2 * (block + base + run * kRun) * a.width + col;
+        float f[kRun][4];
 #pragma unroll
-    for (int b = 0; b < kJoinBlocks; ++b) {
-        const int64_t p = (group_index() + b * groups) * kPiece + lane;
-        key[b] = p < n ? a.keys[p] : -1;
-        const int32_t before = p > 0 && p < n ? a.keys[p - 1] : -1;
-        const int32_t past = p + kPiece < n ? a.keys[p + kPiece] : -1;
-        longs[b] = __ballot(key[b] >= 0 && key[b] < a.vocab && before != key[b] && past == key[b]);
-    }
+        for (int u = 0; u < kRun; ++u) {
+            if (u < mine) {
+                const float* row = src + (2 * (int64_t)u + (base + run * kRun + u == 0)) * a.width;
+                if (rem == 4) F32::unpack(load16<F32>(row), f[u]);
+                else
 #pragma unroll
-    for (int b = 0; b < kJoinBlocks; ++b) {
-        if (!longs[b]) continue;
-        const int64_t block = group_index() + b * groups;
-        const int at = (int)__builtin_ctzll(longs[b]);
-        const int32_t id = __shfl(key[b], at);
-        const int64_t s = block * kPiece + at;
-        float total[4] = {};
-        for (int64_t base = 0;; base += kJoinRuns * kRun) {
-            const int64_t q = s + (base + lane) * kPiece;
-            const int pieces = __popcll(__ballot(q < n && a.keys[q] == id));  // of these runs
-            const int mine = max(0, min(kRun, pieces - run * kRun));
-            // the first piece of all is the second kind of its block
-            const float* src = a.partial + 2 * (block + base + run * kRun) * a.width + col;
-            float f[kRun][4];
-#pragma unroll
-            for (int u = 0; u < kRun; ++u) {
-                if (u < mine) {
-                    const float* row = src + (2 * (int64_t)u + (base + run * kRun + u == 0)) * a.width;
-                    if (rem == 4) F32::unpack(load16<F32>(row), f[u]);
-                    else
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) f[u][c] = c < rem ? row[c] : 0.0f;
-                }
+                    for (int c = 0; c < 4; ++c) f[u][c] = c < rem ? row[c] : 0.0f;
             }
-            float sum[4] = {};
-#pragma unroll
-            for (int u = 0; u < kRun; ++u) {
-                if (u < mine) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) sum[c] += f[u][c];
-                }
-            }
-            *reinterpret_cast<u32x4*>(&sums[run][here]) = F32::pack(sum);
-            __syncthreads();
-            for (int w = 0; w < kJoinRuns && w * kRun < pieces; ++w) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) total[c] += sums[w][here + c];
-            }
-            __syncthreads();
-            if (pieces < kJoinRuns * kRun) break;
         }
-        if (run == 0) {
-            typename G::E* row = table_row<G>(a, id) + col;
+        float sum[4] = {};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c < rem) row[c] = G::store((a.accumulate ? G::load(row[c]) : 0.0f) + total[c] * a.scale);
+        for (int u = 0; u < kRun; ++u) {
+            if (u < mine) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sum[c] += f[u][c];
+            }
         }
+        *reinterpret_cast<u32x4*>(&sums[run][here]) = F32::pack(sum);
+        __syncthreads();
+        for (int w = 0; w < kJoinRuns && w * kRun < pieces; ++w) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) total[c] += sums[w][here + c];
+        }
+        __syncthreads();
+        if (pieces < kJoinRuns * kRun) break;
     }
+    if (run != 0) return;
+    typename G::E* row = table_row<G>(a, id) + col;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (c < rem) row[c] = G::store((a.accumulate ? G::load(row[c]) : 0.0f) + total[c] * a.scale);
 }
 static_assert(kJoinRuns * kRun == kWave, "one lane looks for each piece");
 
@@ -584,27 +570,27 @@ int run_embedding(EmbeddingArgs a, hipStream_t s) {
 template <class T, class G>
 int run_sum(EmbeddingGradArgs a, hipStream_t s) {
     const int64_t cols = kSumThreads * T::n, chunks = (a.width + cols - 1) / cols, n = a.tokens.total();
-    // shorter windows, and fewer rows to clear at once, where the largest would
-    // leave the GPU idle
+    // Shorter windows, and fewer rows to clear at once, where the longest would
+    // leave the GPU idle.  Where there are twice as many summing workgroups, the
+    // clearing ones come between them, so that reads and writes are under way
+    // together; at odd distances, since at every second or fourth place each
+    // kind would get half of the shader engines.  65536 tokens of 4096 columns
+    // and 32000 rows, us a call: 281 at a distance of three, 372 at two, 294
+    // with the clearing last.
     a.window = kPiece;
     while (a.window > 4 && n / a.window * chunks < kSumGroups) a.window /= 2;
     a.windows = (int32_t)((n + a.window - 1) / a.window);
     a.fill_rows = kWave;
     while (a.fill_rows > 4 && a.vocab / a.fill_rows * chunks < kFillGroups) a.fill_rows /= 2;
     a.fill_groups = a.accumulate ? 0 : (int32_t)((a.vocab + a.fill_rows - 1) / a.fill_rows);
-    const int32_t fewer = a.windows < a.fill_groups ? a.windows : a.fill_groups;
-    a.spacing = fewer ? (a.windows + a.fill_groups) / fewer : 1;
     const int64_t groups = (int64_t)a.windows + a.fill_groups;
-    // more rows in flight where few workgroups run and an id's rows one after
-    // another are what takes the time: 1450 tokens FIGAHEAD; 65536 tokens 292
-    // with four, 316 with eight
+    a.spacing = a.fill_groups && a.windows >= 2 * (int64_t)a.fill_groups ? (int32_t)((groups / a.fill_groups - 1) | 1) : 0;
     if (groups)
-        hipLaunchKernelGGL((a.window <= 16 ? embedding_grad_kernel<T, G, 16> : embedding_grad_kernel<T, G, 4>),
-                           grid_of(groups, chunks), dim3(kSumThreads), 0, s, a);
+        hipLaunchKernelGGL((embedding_grad_kernel<T, G>), grid_of(groups, chunks), dim3(kSumThreads), 0, s, a);
     if (n > kPiece)
         hipLaunchKernelGGL(embedding_join_kernel<G>,
-                           grid_of(((n + kPiece - 1) / kPiece + kJoinBlocks - 1) / kJoinBlocks, (a.width + kJoinSides * kJoinCols - 1) / (kJoinSides * kJoinCols)),
-                           dim3(kJoinThreads), 0, s, a);
+                           grid_of((n + kPiece - 1) / kPiece, (a.width + kJoinCols - 1) / kJoinCols),
+                           dim3(kJoinRuns * kWave), 0, s, a);
     return hipGetLastError();
 }
 

@@ -199,7 +199,7 @@ def test_exchange_refusals(lib, bad):
     assert set(exchange_calls(lib, **bad).values()) == {INVAL}
 
 
-@pytest.mark.parametrize("bad", [dict(dtype=rr.RC_I32), dict(dtype=rows.RC_I64), dict(width=0), dict(width=2**24 + 1)])
+@pytest.mark.parametrize("bad", [dict(dtype=rr.RC_I32), dict(dtype=rows.RC_I64), dict(width=0), dict(width=2**22 + 1)])
 def test_exchange_refuses_rows(lib, bad):
     got = exchange_calls(lib, **bad)
     assert got.pop("plan") == OK and got.pop("plan_workspace") == OK
@@ -274,7 +274,7 @@ def test_embedding_accepts(lib):
 
 
 @pytest.mark.parametrize("bad", [dict(size=1), dict(dtype=rr.RC_I32), dict(id=rr.RC_F32), dict(vocab=0),
-                                 dict(vocab=2**31 - 1), dict(width=0), dict(width=2**25), dict(scale=float("nan")),
+                                 dict(vocab=2**31 - 1), dict(width=0), dict(width=2**22 + 1), dict(scale=float("nan")),
                                  dict(tokens=[-1, 0, 0, 0]), dict(tokens=[2**31, 0, 0, 0])])
 def test_embedding_refusals(lib, bad):
     assert set(embedding_calls(lib, **bad).values()) == {INVAL}
