@@ -16,11 +16,14 @@
 // order is the scores' (no bias), the keys are made from the logits, exactly.
 // Otherwise the scores are computed in float32, with a bound on their error;
 // where two that decide something are closer than that, the scores that could
-// matter - a handful - are computed again in 64 bits and decide (apart to
-// 2^-42 of their size).  A double exp and division for every expert cost more
-// than all the rest: FIGROUTE.
+// matter - a handful - are computed again in 64 bits and decide, to their last
+// bit.  A double exp and division for every expert cost more than all the rest:
+// 131072 tokens of 256 experts in 8 groups with a bias, eight chosen, took 151 us
+// that way and take 69 (without bias or groups 43).
 //
-// Bound by instruction issue where there are many tokens: FIGVALU.
+// Bound by instruction issue where there are many tokens: that case issues
+// 1770 vector instructions a wave of eight tokens, 49 us of the 69 if none ever
+// waited; its 142 MB are 27 us at the rate of a large copy.
 #include "rows_impl.h"
 
 namespace rc {
@@ -196,6 +199,38 @@ __device__ __forceinline__ void merge_lists(double* list) {
         for (int k = 0; k < KP; ++k) m[k] = across<O>(list[k]);
         merge_into<KP>(list, m);
         merge_lists<L, KP, O * 2>(list);
+    }
+}
+
+// Scores in full, each with its expert, for the few that are computed in 64 bits.
+__device__ __forceinline__ void order(double& hi, int& hi_expert, double& lo, int& lo_expert) {
+    const bool swap = lo > hi || (lo == hi && lo_expert < hi_expert);
+    const double s = swap ? lo : hi, t = swap ? hi : lo;
+    const int e = swap ? lo_expert : hi_expert, f = swap ? hi_expert : lo_expert;
+    hi = s;
+    lo = t;
+    hi_expert = e;
+    lo_expert = f;
+}
+template <int L, int KP, int O = 1>
+__device__ __forceinline__ void merge_scored(double* score, int* expert) {
+    if constexpr (O < L) {
+        double m[KP];
+        int e[KP];
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            m[k] = across<O>(score[k]);
+            e[k] = across<O>(expert[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < KP; ++k) order(score[k], expert[k], m[KP - 1 - k], e[KP - 1 - k]);
+#pragma unroll
+        for (int h = KP / 2; h > 0; h >>= 1) {
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
+                if (!(k & h)) order(score[k], expert[k], score[k + h], expert[k + h]);
+        }
+        merge_scored<L, KP, O * 2>(score, expert);
     }
 }
 
@@ -526,22 +561,73 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             for (int j = 0; j < V; ++j) close = close + close + (uint32_t)(x[j] >= from);
             if (!kept) close = 0;
             sum_exact();
+            if (!doubt) close = 0;
             double list64[KP];
 #pragma unroll
             for (int k = 0; k < KP; ++k) list64[k] = kNone;
-            if (!doubt) close = 0;
-            while (__any(close)) {
+            for (uint32_t left = close; __any(left);) {
                 double key = kNone;
-                if (close) {
-                    const int j = V - 1 - __builtin_ctz(close);
+                if (left) {
+                    const int j = V - 1 - __builtin_ctz(left);
                     key = key_of(exact(j), reversed(j));
-                    close &= close - 1;
+                    left &= left - 1;
                 }
                 insert<KP>(list64, key);
             }
+            uint32_t held[KP];  // of the lane's best keys, what is the score's
+#pragma unroll
+            for (int k = 0; k < KP; ++k) held[k] = (uint32_t)(__builtin_bit_cast(uint64_t, list64[k]) >> 10);
             merge_lists<L, KP>(list64);
+            // Keys whose scores agree to 2^-42: the bits cut off decide.  They are
+            // few enough to be chosen anew, scores and experts apart; with no keys
+            // before, 256 experts with a bias and no groups take 67 us for 63; a
+            // bias of zeros on bf16 logits, with equal scores in every row, 73 for 114.
+            bool same = false;
+            uint64_t before = 0;
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                if (k < a.top_k && list64[k] > kNoKey) {
+                    const uint64_t u = __builtin_bit_cast(uint64_t, list64[k]) >> 10;
+                    same |= u == before;
+                    before = u;
+                }
+            }
+            int as_last = 0;
+#pragma unroll
+            for (int k = 0; k < KP; ++k) as_last += held[k] == (uint32_t)before;
+            same |= sum_lanes<L>(as_last) > 1;
+            same &= doubt;
 #pragma unroll
             for (int k = 0; k < KP; ++k) list[k] = doubt ? list64[k] : list[k];
+            if (__any(same)) {
+                if (!same) close = 0;
+                double score[KP];
+                int of[KP];
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    score[k] = kNone;
+                    of[k] = RC_MAX_EXPERTS;
+                }
+                while (__any(close)) {
+                    double v = kNone;
+                    int e = RC_MAX_EXPERTS;
+                    if (close) {
+                        const int j = V - 1 - __builtin_ctz(close);
+                        v = exact(j);
+                        e = p.base + p.at(j);
+                        close &= close - 1;
+                    }
+#pragma unroll
+                    for (int k = 0; k < KP; ++k) order(score[k], of[k], v, e);
+                }
+                merge_scored<L, KP>(score, of);
+                // from here on only a key's index counts
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    const double key = score[k] > kNone ? __builtin_bit_cast(double, (uint64_t)(RC_MAX_EXPERTS - 1 - of[k])) : kNone;
+                    list[k] = same ? key : list[k];
+                }
+            }
         }
     }
 
@@ -721,7 +807,7 @@ int run_route(RouteArgs a, hipStream_t s) {
 
 // Lanes per token: 8, so that a wave's instructions serve eight tokens; 64
 // where there are so few tokens that latency counts (64 tokens of 256 experts:
-// FIGFEW), or too many experts.
+// 7.3 us against 18.5), or too many experts.
 constexpr int64_t kFewTokens = 2048;
 template <class T>
 int pick_route(const RouteArgs& a, hipStream_t s) {

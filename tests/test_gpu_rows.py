@@ -195,6 +195,12 @@ def test_route_tells_close_scores_apart():
     check_route([step], 7, "f32", score="sigmoid", bias=torch.full((E,), 0.25))
     check_route([step], 7, "f32", score="softmax", bias=torch.full((E,), 0.25))
     check_route([step], 7, "f32", score="softmax", groups=4, top_groups=2, group_by="top2")
+    # near 18 a step of the logits moves the sigmoid by 3e-14: hundreds of steps of
+    # a double, a fraction of one of its upper 42 bits
+    fine = torch.full((1, E), 18.0) + 2.0 ** -19 * torch.randperm(E, generator=gen(3)).float()
+    for b in (0.0, 0.25, -0.5):
+        check_route([fine], 5, "f32", score="sigmoid", bias=torch.full((E,), b))
+        check_route([fine], 5, "f32", score="sigmoid", bias=torch.full((E,), b), groups=4, top_groups=3)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
