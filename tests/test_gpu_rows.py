@@ -14,6 +14,7 @@ Copies, choices, slots and sums in the documented order are compared bit for bit
 """
 
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -686,3 +687,91 @@ def test_tensors_elsewhere_are_refused():
             rr.route([torch.zeros(2, 4, device=DEV), torch.zeros(2, 4)], 1)
         with pytest.raises(rr.CollectiveError):
             rr.route([torch.zeros(2, 4, device=DEV)] * 3, 1)
+
+
+# ---------------------------------------------------------------- large buffers, calls at once
+
+# Rows beyond 2^31 elements (2^32 bytes in bf16) of one buffer: results there are
+# those of the same rows in small buffers, bit for bit.
+FAR = 2 ** 31 // 4096 + 9  # rows of 4096
+
+
+def test_far_route_rows():
+    with session(2):
+        few = normal(gen(1), 3, 1024, dtype="bf16").to(DEV)
+        many = torch.zeros(2 ** 21 + 5, 1024, dtype=torch.bfloat16, device=DEV)
+        many[-3:] = few
+        dw = torch.zeros(many.shape[0], 4, device=DEV)
+        dw[-3:] = normal(gen(2), 3, 4).to(DEV)
+        none = [few[:0], dw[:0]]
+        w, e = rr.route([none[0], many], 4)
+        ws, es = rr.route([none[0], few], 4)
+        assert torch.equal(w[1][-3:], ws[1]) and torch.equal(e[1][-3:], es[1])
+        d = rr.route_grad([none[0], many], e, [none[1], dw])
+        ds = rr.route_grad([none[0], few], es, [none[1], dw[-3:].clone()])
+        assert torch.equal(d[1][-3:], ds[1])
+        assert not d[1][:-3].any()
+
+
+def test_far_exchanged_rows():
+    """One expert on rank 1 takes every token of rank 0."""
+    with session(2):
+        x = torch.zeros(FAR, 4096, dtype=torch.bfloat16, device=DEV)
+        x[-8:] = normal(gen(3), 8, 4096, dtype="bf16").to(DEV)
+        none = x[:0]
+        e = torch.ones(FAR, 1, dtype=torch.int32, device=DEV)
+        plan = rr.dispatch_plan([e, e[:0]], 2, capacity=[0, FAR])
+        assert torch.equal(plan.slots[0][:, 0], torch.arange(FAR, dtype=torch.int32, device=DEV))
+        rows = rr.dispatch([x, none], plan)
+        assert torch.equal(rows[1], x)
+        half = torch.full((FAR, 1), 0.5, device=DEV)
+        y = rr.combine(rows, plan, [half, half[:0]])[0]
+        assert torch.equal(y[-8:], x[-8:] * 0.5) and not y[:-8].any()
+        del y
+        dx, dw = rr.combine_grad([x, none], rows, plan, [half, half[:0]])
+        assert torch.equal(dx[1][-8:], x[-8:] * 0.5) and not dx[1][:-8].any()
+        want = (f64([x[-8:]])[0] ** 2).sum(1)
+        near(dw[0][-8:, 0].cpu().numpy(), want, 1.01 * 4096 * U * want, "d_weights")
+
+
+def test_far_table_rows_and_tokens():
+    with session(2):
+        vocab = 2 * FAR
+        tables = [torch.zeros(FAR, 4096, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        tables[1][-8:] = normal(gen(4), 8, 4096, dtype="bf16").to(DEV)
+        ids = torch.full((FAR,), -1, dtype=torch.int64, device=DEV)
+        ids[-12:-4] = torch.arange(vocab - 8, vocab)
+        ids[-4:] = vocab - 1
+        none = ids[:0]
+        y = rr.embedding([ids, none], tables)[0]
+        assert torch.equal(y[-12:-4], tables[1][-8:]) and torch.equal(y[-4:], tables[1][-1:].expand(4, -1))
+        assert not y[:-12].any()
+        d = rr.embedding_grad([ids, none], [y, y[:0]], vocab)
+        got, near_rows = d[1][-8:], rr.embedding_grad([ids[-12:], none], [y[-12:].clone(), y[:0]], vocab)[1][-8:]
+        assert torch.equal(got, near_rows)
+        assert torch.equal(got[:-1], tables[1][-8:-1])
+        assert not d[0].any() and not d[1][:-8].any()
+
+
+def test_calls_from_two_threads_at_once():
+    """Two threads, a stream each, the whole chain several times."""
+    with session(3):
+        states = [moe_state(5), moe_state(6)]
+        want = [[t.clone() for t in moe_chain(st)] for st in states]
+        torch.cuda.synchronize()
+        wrong = []
+
+        def work(n):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for rep in range(5):
+                    got = moe_chain(states[n])
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[n])):
+                        wrong.append((n, rep))
+
+        threads = [threading.Thread(target=work, args=(n,)) for n in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not wrong
