@@ -212,7 +212,9 @@ __global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SmallSort a) 
 // ---------------------------------------------------------------- summing
 
 constexpr int kSumThreads = 256;
-constexpr int kAhead = 2;  // rows of dy in flight per lane
+// Rows of dy in flight per lane.  2000 ids, 1000 columns, 64 of them one id's, us
+// a call: 39 with two, 31 with four, 29 with eight or sixteen.
+constexpr int kAhead = 8;
 // Workgroups that keep the GPU busy.
 constexpr int64_t kSumGroups = 8192;
 constexpr int64_t kFillGroups = 4000;
@@ -253,35 +255,37 @@ struct Cols {
 typedef uint32_t u32x2m __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// `rem` elements of a part, the others zero.
-template <class T, int PART, int WORDS>
+// A part's elements; with FULL false only the first `rem`, the others zero.
+// (One register per element there: packing them would wait for each load.)
+template <class T, int PART, int WORDS, bool FULL>
 __device__ __forceinline__ void load_part(const typename T::E* src, int rem, uint32_t* w) {
-    if (rem == PART) {
-        if constexpr (WORDS == 4) {
-            const u32x4 v = load16<T>(src);
+    if constexpr (!FULL) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = v[i];
-        } else {
-            const u32x2 v = *reinterpret_cast<const u32x2m*>(src);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) w[i] = v[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+        for (int i = 0; i < PART; ++i) w[i] = 0;
 #pragma unroll
         for (int i = 0; i < PART; ++i) {
             if (i >= rem) continue;
             if constexpr (sizeof(typename T::E) == 4) w[i] = __builtin_bit_cast(uint32_t, src[i]);
-            else w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, src[i]) << (16 * (i % 2));
+            else w[i] = __builtin_bit_cast(uint16_t, src[i]);
         }
+    } else if constexpr (WORDS == 4) {
+        const u32x4 v = load16<T>(src);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = v[i];
+    } else {
+        const u32x2 v = *reinterpret_cast<const u32x2m*>(src);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i] = v[i];
     }
 }
-template <class T>
+template <class T, bool FULL>
 __device__ __forceinline__ float element_of(const uint32_t* w, int i) {
     if constexpr (sizeof(typename T::E) == 4) {
         const uint32_t u = w[i];
         return __builtin_bit_cast(float, u);
+    } else if constexpr (!FULL) {
+        const uint16_t u = (uint16_t)w[i];
+        return T::load(__builtin_bit_cast(typename T::E, u));
     } else {
         const uint16_t u = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
         return T::load(__builtin_bit_cast(typename T::E, u));
@@ -307,6 +311,72 @@ __device__ __forceinline__ void finish_row(const EmbeddingGradArgs& a, typename 
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (i < rem) row[i] = G::store((a.accumulate ? G::load(row[i]) : 0.0f) + sum[i] * a.scale);
+    }
+}
+
+// What a workgroup sums: the positions [begin, end) of its window's list.
+struct SumRange {
+    int begin, end;
+    int carried;              // positions below it belong to a piece of an id that began earlier
+    int hot;                  // positions from it on, to an id of several pieces
+    uint64_t stops[2];        // positions that end an id or a piece
+    float *carried_out, *hot_out;
+};
+
+// The sums of a lane's columns: col and rem are its parts' first columns and
+// elements, with FULL all of them.  AHEAD rows are in flight; the addresses and
+// the ends are alike in all lanes, so the loop has no branch before a load (with
+// one, and with the zeros of a row's ragged end written between the loads, each
+// row waited for the one before: 41 us for the 29 above, and 281 for the 268 of
+// 65536 tokens of 4096 columns).
+template <class T, class G, int AHEAD, bool FULL>
+__device__ __forceinline__ void sum_rows(const EmbeddingGradArgs& a, const SumRange& r, const typename T::E* const* rows,
+                                         const int32_t* key, const int64_t* col, const int* rem) {
+    using C = Cols<T, G>;
+    using E = typename T::E;
+    constexpr int kWords = FULL ? C::kWords : C::kPart;
+    float acc[C::kParts][C::kPart] = {};
+    for (int j0 = r.begin; j0 < r.end; j0 += AHEAD) {
+        uint32_t w[AHEAD][C::kParts][kWords];
+        const E* src[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const uint64_t p = reinterpret_cast<uint64_t>(rows[min(j0 + u, r.end - 1)]);
+            const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+            src[u] = reinterpret_cast<const E*>((uint64_t)hi << 32 | lo);
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+            for (int h = 0; h < C::kParts; ++h) load_part<T, C::kPart, C::kWords, FULL>(src[u] + col[h], rem[h], w[u][h]);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int j = j0 + u;
+            if (j >= r.end) break;
+#pragma unroll
+            for (int h = 0; h < C::kParts; ++h)
+#pragma unroll
+                for (int i = 0; i < C::kPart; ++i) acc[h][i] += element_of<T, FULL>(w[u][h], i);
+            if (!((j < kWave ? r.stops[0] >> j : r.stops[1] >> (j - kWave)) & 1)) continue;
+            const bool piece = j < r.carried || j >= r.hot;
+            float* out = j < r.carried ? r.carried_out : r.hot_out;
+            typename G::E* row = piece ? nullptr : table_row<G>(a, key[j]);
+#pragma unroll
+            for (int h = 0; h < C::kParts; ++h) {
+                if (!piece) {
+                    finish_row<G, C::kPart>(a, row + col[h], FULL ? C::kPart : rem[h], acc[h]);
+                } else if (FULL) {
+#pragma unroll
+                    for (int i = 0; i < C::kPart; i += 4) store16<F32>(out + col[h] + i, F32::pack(acc[h] + i));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C::kPart; ++i)
+                        if (i < rem[h]) out[col[h] + i] = acc[h][i];
+                }
+#pragma unroll
+                for (int i = 0; i < C::kPart; ++i) acc[h][i] = 0.0f;
+            }
+        }
     }
 }
 
@@ -395,60 +465,32 @@ __global__ __launch_bounds__(kSumThreads) void embedding_grad_kernel(EmbeddingGr
     else if (begins) end = last_end;
     else end = carried;
     if (begin >= end) return;
+    SumRange r;
+    r.begin = __builtin_amdgcn_readfirstlane(begin);
+    r.end = __builtin_amdgcn_readfirstlane(end);
+    r.carried = __builtin_amdgcn_readfirstlane(carried);
+    r.hot = hot;
+    for (int i = 0; i < 2; ++i) {
+        const int j = i * kWave + lane;
+        r.stops[i] = __ballot(j < r.end && (j + 1 == r.end || j + 1 == r.carried || key[j + 1] != key[j]));
+    }
     // where the sums of the carried piece and of the long id's first go
-    float* const carried_out = a.partial + 2 * (int64_t)((p0 + begin) / kPiece) * a.width;
-    float* const hot_out = a.partial + (2 * (int64_t)((p0 + hot) / kPiece) + 1) * a.width;
+    r.carried_out = a.partial + 2 * (int64_t)((p0 + r.begin) / kPiece) * a.width;
+    r.hot_out = a.partial + (2 * (int64_t)((p0 + hot) / kPiece) + 1) * a.width;
 
     using C = Cols<T, G>;
     int64_t col[C::kParts];
     int rem[C::kParts];
+    bool full = true, some = false;
 #pragma unroll
     for (int h = 0; h < C::kParts; ++h) {
         col[h] = ((int64_t)blockIdx.z * kSumThreads + threadIdx.x / kWave * kWave) * T::n + (h * kWave + lane) * C::kPart;
         rem[h] = (int)max((int64_t)0, min((int64_t)C::kPart, a.width - col[h]));
+        full &= rem[h] == C::kPart;
+        some |= rem[h] > 0;
     }
-    float acc[C::kParts][C::kPart] = {};
-    for (int j0 = begin; j0 < end; j0 += kAhead) {
-        uint32_t w[kAhead][C::kParts][C::kWords];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (j0 + u < end) {
-#pragma unroll
-                for (int h = 0; h < C::kParts; ++h) load_part<T, C::kPart, C::kWords>(rows[j0 + u] + col[h], rem[h], w[u][h]);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int j = j0 + u;
-            if (j < end) {
-#pragma unroll
-                for (int h = 0; h < C::kParts; ++h)
-#pragma unroll
-                    for (int i = 0; i < C::kPart; ++i) acc[h][i] += element_of<T>(w[u][h], i);
-                // an id's last entry, or a piece's
-                if (j + 1 == end || j + 1 == carried || key[j + 1] != key[j]) {
-                    const bool piece = j < carried || j >= hot;
-                    float* out = j < carried ? carried_out : hot_out;
-                    typename G::E* row = piece ? nullptr : table_row<G>(a, key[j]);
-#pragma unroll
-                    for (int h = 0; h < C::kParts; ++h) {
-                        if (!piece) {
-                            finish_row<G, C::kPart>(a, row + col[h], rem[h], acc[h]);
-                        } else if (rem[h] == C::kPart) {
-#pragma unroll
-                            for (int i = 0; i < C::kPart; i += 4) store16<F32>(out + col[h] + i, F32::pack(acc[h] + i));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < C::kPart; ++i)
-                                if (i < rem[h]) out[col[h] + i] = acc[h][i];
-                        }
-#pragma unroll
-                        for (int i = 0; i < C::kPart; ++i) acc[h][i] = 0.0f;
-                    }
-                }
-            }
-        }
-    }
+    if (full) sum_rows<T, G, kAhead, true>(a, r, rows, key, col, rem);
+    else if (some) sum_rows<T, G, 2, false>(a, r, rows, key, col, rem);
 }
 
 // Joins the pieces of the long id that begins in the block of kPiece entries,
@@ -576,7 +618,7 @@ int run_sum(EmbeddingGradArgs a, hipStream_t s) {
     // together; at odd distances, since at every second or fourth place each
     // kind would get half of the shader engines.  65536 tokens of 4096 columns
     // and 32000 rows, us a call: 281 at a distance of three, 372 at two, 294
-    // with the clearing last.
+    // with the clearing last (268 at three since rows are loaded eight ahead).
     a.window = kPiece;
     while (a.window > 4 && n / a.window * chunks < kSumGroups) a.window /= 2;
     a.windows = (int32_t)((n + a.window - 1) / a.window);
