@@ -333,7 +333,6 @@ int rc_dispatch_plan(const rc_exchange_desc* desc, int32_t* const* offsets, int3
         a.sort.key_limit = desc->num_experts;
         a.num_experts = desc->num_experts;
         a.per_rank = x.a.per_rank;
-        a.nranks = R;
         if (validate_only) return {};
         return device_run([&] { return launch_plan(a, workspace, stream); });
     });

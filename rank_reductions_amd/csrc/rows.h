@@ -83,7 +83,6 @@ struct PlanArgs {
     int64_t capacity[kMaxRanks];
     int32_t num_experts;
     int32_t per_rank;  // experts of each rank
-    int32_t nranks;
 };
 
 // ---------------------------------------------------------------- row moves
@@ -109,7 +108,7 @@ struct ExchangeArgs {
 struct EmbeddingArgs {
     const void* ids[kMaxRanks];
     const void* table[kMaxRanks];
-    void* out[kMaxRanks];  // lookup: each rank's rows; gradient: each rank's shard
+    void* out[kMaxRanks];
     RankSpans tokens;
     int64_t vocab;
     int64_t shard;   // rows of a full shard, ceil(vocab / ranks)
@@ -140,7 +139,6 @@ struct EmbeddingGradArgs {
     int32_t fill_rows;     // table rows per workgroup that clears those no id names, a power of two up to 64
     int32_t fill_groups;
     int32_t spacing;       // the first workgroups at multiples of this clear rows; 0: those behind the windows do
-    int32_t chunks;        // column pieces of a row, one workgroup each
 };
 
 // ---------------------------------------------------------------- launches (rows_*.hip)
