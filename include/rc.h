@@ -390,7 +390,9 @@ typedef struct rc_route_desc {
 
 /* Chooses K experts for every token.  logits[r]: [tokens[r], E]; weights[r]
  * and experts[r]: [tokens[r], K], by falling s + bias, equal ones by rising
- * index.  The comparison is that of the values in 64 bits, however close.
+ * index.  What is compared are the values computed in 64 bits, however close
+ * (two sums of other scores and biases that agree in exact arithmetic, as
+ * groups' may, can differ in the last of those).
  * weights = scale * s, or scale * s / (sum of the K s).  An expert whose
  * logit is -inf, or whose s + bias is -inf or NaN, is never chosen; a token
  * with fewer than K others has expert -1 and weight 0 in the rest, and a sum

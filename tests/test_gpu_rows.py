@@ -775,3 +775,19 @@ def test_calls_from_two_threads_at_once():
         for t in threads:
             t.join()
         assert not wrong
+
+
+def test_small_outputs_share_an_allocation_and_large_ones_do_not():
+    with session(3):
+        e = [torch.zeros(4, 1, dtype=torch.int32, device=DEV)] * 3
+        for width, together in ((40, True), (2 ** 20 + 8, False)):
+            xs = [normal(gen(7), 4, width, dtype="bf16").to(DEV) for _ in range(3)]
+            plan = rr.dispatch_plan(e, 3, capacity=[12, 1, 5])
+            rows = rr.dispatch(xs, plan)
+            assert [tuple(x.shape) for x in rows] == [(12, width), (1, width), (5, width)]
+            assert torch.equal(rows[0], torch.cat(xs)) and not rows[1].any() and not rows[2].any()
+            assert all(x.data_ptr() % 256 == 0 for x in rows)
+            stores = {x.untyped_storage().data_ptr() for x in rows}
+            assert len(stores) == (1 if together else 3)
+            rows[1].fill_(3)  # each is a tensor of its own
+            assert torch.equal(rows[0], torch.cat(xs)) and not rows[2].any()

@@ -437,3 +437,13 @@ def test_binding_embedding(two):
     assert code_of(lambda: rr.embedding_grad(ids, [f(2, 8), f(0, 8)], 5)) == SHAPE
     assert code_of(lambda: rr.embedding_grad(ids, d, 5, dtype=torch.float16, out=[f(3, 8), f(2, 8)])) == DTYPE
     assert rows.shard_rows(5, 4) == [2, 2, 1, 0]
+
+
+def test_binding_sizes(two):
+    """Outputs too large for any buffer are refused before they are allocated."""
+    x = [f(3, 8), f(1, 8)]
+    for capacity in ((2**31, 5), (2**62, 2**62), (2**63 - 1, 0)):
+        assert code_of(lambda: rr.dispatch(x, plan_of(capacity))) == INVAL
+    assert code_of(lambda: rr.combine([f(0, 2**40)] * 2, plan_of((0, 0)))) == INVAL
+    for vocab in (0, -1, 2**31, 2**62, 2**63 - 1):
+        assert code_of(lambda: rr.embedding_grad([i(3), i(0)], [f(3, 8), f(0, 8)], vocab)) == INVAL
