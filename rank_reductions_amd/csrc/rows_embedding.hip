@@ -17,6 +17,8 @@
 // and the table written once.
 #include "rows_sort.h"
 
+#include <algorithm>
+
 namespace rc {
 namespace {
 
@@ -115,105 +117,91 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortPass s) {
     }
 }
 
-// All passes in one workgroup, for few ids: keys and positions stay in LDS.
-constexpr int kSmallThreads = 512;
-constexpr int kSmallWaves = kSmallThreads / kWave;
-constexpr int kSmallStrips = 8;
-constexpr int kSmallIds = kSmallThreads * kSmallStrips;
-constexpr int kSmallBits = 9;  // a digit per thread
-struct SmallSort {
-    SortPass first;  // spans, ids, id64, key_limit, out_keys, out_vals
-    int32_t passes;
-    int32_t bits;    // of each pass
-};
-__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SmallSort a) {
-    __shared__ int32_t count[kSmallWaves][1 << kSmallBits];
-    __shared__ int32_t keys[kSmallIds];
-    __shared__ int32_t vals[kSmallIds];
-    __shared__ int32_t carry[kSmallWaves];
+// Few ids, in one launch: an id's place is the number of ids below it, and of
+// equal ones before it, counted by comparing it with all (kept in LDS).  A
+// workgroup places 64 ids, one per lane; its waves share out what they are
+// compared with.  Each workgroup also makes its part of the table's named bytes.
+// 1700 ids take 7.7 us; two counting passes in one workgroup took 10.8, and the
+// launches for more ids take 27 and up.
+constexpr int kRankThreads = 1024;
+constexpr int kRankWaves = kRankThreads / kWave;
+constexpr int kRankIds = 8192;
+constexpr int kRankEach = kRankIds / kRankThreads;
+constexpr int kNamedChunk = 4096;  // table rows at a time
+constexpr int64_t kRankGroups = 256;
+__global__ __launch_bounds__(kRankThreads) void sort_rank_kernel(SortPass s) {
+    __shared__ __align__(16) int32_t keys[kRankIds];
+    __shared__ int32_t part[kRankWaves][kWave];
+    __shared__ __align__(16) uint8_t named[kNamedChunk];
     const int lane = lane_id(), wave = threadIdx.x / kWave;
-    const int32_t n = a.first.spans.total();
-    const int strips = (n + kSmallThreads - 1) / kSmallThreads;
-    const int32_t at = wave * strips * kWave + lane;
-    const int bins = 1 << a.bits, d = threadIdx.x;
-    int32_t key[kSmallStrips], val[kSmallStrips];
+    const int32_t n = s.spans.total(), blocks = (n + kWave - 1) / kWave;
+    int32_t own[kRankEach];
 #pragma unroll
-    for (int k = 0; k < kSmallStrips; ++k) {
-        const int32_t j = at + k * kWave;
-        key[k] = -1;
-        val[k] = j;
-        if (k < strips && j < n) {
+    for (int k = 0; k < kRankEach; ++k) {
+        const int32_t j = k * kRankThreads + threadIdx.x;
+        own[k] = 0x7fffffff;  // behind all ids
+        if (j < n) {
             int32_t i;
-            const int rank = rank_of(a.first.spans, j, &i);
-            key[k] = first_key(a.first, rank, i);
+            const int rank = rank_of(s.spans, j, &i);
+            own[k] = first_key(s, rank, i);
         }
     }
-    if (a.first.named) clear_named(a.first, 0, 1, kSmallThreads);
-    for (int p = 0; p < a.passes; ++p) {
-        const int shift = p * a.bits;
-        if (d < bins)
 #pragma unroll
-            for (int w = 0; w < kSmallWaves; ++w) count[w][d] = 0;
-        __syncthreads();
+    for (int k = 0; k < kRankEach; ++k)
+        if (k * kRankThreads < n) keys[k * kRankThreads + threadIdx.x] = own[k];
+    __syncthreads();
+    const int32_t mine = blockIdx.x;
+    if (mine < blocks) {
+        const int32_t i = mine * kWave + lane, key = keys[i];
+        const int32_t from = (int32_t)((int64_t)wave * blocks / kRankWaves), to = (int32_t)((int64_t)(wave + 1) * blocks / kRankWaves);
+        int32_t below = 0;
+        // f(j): what an id j places into the block has to lie below
+        auto compare = [&](int32_t b, auto f) {
 #pragma unroll
-        for (int k = 0; k < kSmallStrips; ++k)
-            if (key[k] >= 0) atomicAdd(&count[wave][(key[k] >> shift) & (bins - 1)], 1);
-        __syncthreads();
-        // where each wave's entries of digit d begin
-        int32_t c[kSmallWaves], sum = 0;
+            for (int j = 0; j < kWave; j += 4) {
+                const u32x4 v = *reinterpret_cast<const u32x4*>(keys + b * kWave + j);
 #pragma unroll
-        for (int w = 0; w < kSmallWaves; ++w) {
-            c[w] = d < bins ? count[w][d] : 0;
-            sum += c[w];
-        }
-        int32_t incl = sum;
-#pragma unroll
-        for (int o = 1; o < kWave; o <<= 1) {
-            const int32_t up = __shfl_up(incl, o);
-            incl += lane >= o ? up : 0;
-        }
-        if (lane == kWave - 1) carry[wave] = incl;
-        __syncthreads();
-        int32_t run = incl - sum;
-        for (int w = 0; w < wave; ++w) run += carry[w];
-        if (d < bins)
-#pragma unroll
-            for (int w = 0; w < kSmallWaves; ++w) {
-                count[w][d] = run;
-                run += c[w];
+                for (int c = 0; c < 4; ++c) below += v[c] < f(j + c);
             }
-        __syncthreads();
-        const bool last = p + 1 == a.passes;
-#pragma unroll
-        for (int k = 0; k < kSmallStrips; ++k) {
-            if (k < strips) {  // alike in all lanes
-                const bool has = key[k] >= 0;
-                const int32_t place = strip_rank((key[k] >> shift) & (bins - 1), a.bits, has, count[wave]);
-                if (has) {
-                    (last ? a.first.out_keys : keys)[place] = key[k];
-                    (last ? a.first.out_vals : vals)[place] = val[k];
-                    if (last && a.first.named && key[k] < a.first.key_limit) a.first.named[key[k]] = 1;
-                }
-            }
+        };
+        for (int32_t b = from; b < to; ++b) {
+            const uint32_t limit = (uint32_t)key + (b < mine);
+            if (b != mine) compare(b, [&](int) { return limit; });
+            else compare(b, [&](int j) { return (uint32_t)key + (j < lane); });
         }
-        if (last) break;
+        part[wave][lane] = below;
+        __syncthreads();
+        if (wave == 0 && i < n) {
+            int32_t place = 0;
+#pragma unroll
+            for (int w = 0; w < kRankWaves; ++w) place += part[w][lane];
+            s.out_keys[place] = key;
+            s.out_vals[place] = i;
+        }
+    }
+    if (!s.named) return;
+    for (int64_t base = (int64_t)blockIdx.x * kNamedChunk; base < s.key_limit; base += (int64_t)gridDim.x * kNamedChunk) {
+        __syncthreads();
+        reinterpret_cast<uint32_t*>(named)[threadIdx.x] = 0;
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kSmallStrips; ++k) {
-            const int32_t j = at + k * kWave;
-            if (k < strips && j < n) {
-                key[k] = keys[j];
-                val[k] = vals[j];
-            }
+        for (int k = 0; k < kRankEach; ++k) {
+            const int64_t at = own[k] - base;
+            if (at >= 0 && at < kNamedChunk) named[at] = 1;
         }
+        __syncthreads();
+        const int at = threadIdx.x * 16;
+        if (at < kNamedChunk && base + at < s.key_limit)  // the bytes are padded to 16
+            *reinterpret_cast<u32x4*>(s.named + base + at) = *reinterpret_cast<const u32x4*>(named + at);
     }
 }
+static_assert(kNamedChunk == 4 * kRankThreads, "a word each to clear");
 
 // ---------------------------------------------------------------- summing
 
 constexpr int kSumThreads = 256;
-// Rows of dy in flight per lane.  2000 ids, 1000 columns, 64 of them one id's, us
-// a call: 39 with two, 31 with four, 29 with eight or sixteen.
+// Rows of dy in flight per lane.  1700 ids, 1000 columns, 64 and more of them one
+// id's, us a call: 39 with two, 31 with four, 29 with eight or sixteen.
 constexpr int kAhead = 8;
 // Workgroups that keep the GPU busy.
 constexpr int64_t kSumGroups = 8192;
@@ -569,8 +557,8 @@ int bits_of(int64_t values) {
 
 // The sort's passes over keys in [0, vocab]: as few as the digits' width
 // allows, of equal width.
-void passes_of(int64_t vocab, int64_t n, int* passes, int* bits) {
-    const int all = bits_of(vocab + 1), most = n <= kSmallIds ? kSmallBits : bits_of(kSortBins);
+void passes_of(int64_t vocab, int* passes, int* bits) {
+    const int all = bits_of(vocab + 1), most = bits_of(kSortBins);
     *passes = (all + most - 1) / most;
     *bits = (all + *passes - 1) / *passes;
 }
@@ -591,9 +579,9 @@ Layout layout_of(const RankSpans& tokens, int64_t vocab, int64_t width) {
     l.vals[1] = 3 * list;
     l.hist = 4 * list;
     int passes, bits;
-    passes_of(vocab, n, &passes, &bits);
+    passes_of(vocab, &passes, &bits);
     // the first pass cuts each rank's ids into blocks of their own
-    const int64_t hist = n <= kSmallIds ? 0 : ((int64_t)sort_blocks(tokens).total() + 1) * (int64_t(1) << bits) * 4;
+    const int64_t hist = n <= kRankIds ? 0 : ((int64_t)sort_blocks(tokens).total() + 1) * (int64_t(1) << bits) * 4;
     l.named = l.hist + align256(hist);
     l.partial = l.named + align256(vocab);
     l.bytes = l.partial + (n + kPiece - 1) / kPiece * 2 * width * 4;
@@ -657,18 +645,16 @@ int launch_embedding_grad(EmbeddingGradArgs a, SortPass sort, int dtype, int gra
         vals[i] = reinterpret_cast<int32_t*>(ws + l.vals[i]);
     }
     int passes, bits;
-    passes_of(a.vocab, n, &passes, &bits);
+    passes_of(a.vocab, &passes, &bits);
     sort.drop = 0;
     sort.named = a.accumulate || !n ? nullptr : reinterpret_cast<uint8_t*>(ws + l.named);
     a.named = sort.named;
-    if (n > 0 && n <= kSmallIds) {
-        SmallSort m{};
-        m.first = sort;
-        m.first.out_keys = keys[0];
-        m.first.out_vals = vals[0];
-        m.passes = passes;
-        m.bits = bits;
-        hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(kSmallThreads), 0, s, m);
+    if (n > 0 && n <= kRankIds) {
+        sort.out_keys = keys[0];
+        sort.out_vals = vals[0];
+        const int64_t chunks = sort.named ? (a.vocab + kNamedChunk - 1) / kNamedChunk : 0;
+        const int64_t groups = std::max<int64_t>((n + kWave - 1) / kWave, std::min<int64_t>(chunks, kRankGroups));
+        hipLaunchKernelGGL(sort_rank_kernel, dim3((unsigned)groups), dim3(kRankThreads), 0, s, sort);
     } else if (n > 0) {
         sort.bits = bits;
         sort.bins = 1 << bits;

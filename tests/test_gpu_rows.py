@@ -495,6 +495,21 @@ def test_embedding_grad_long_sums(counts, ranks):
     assert np.array_equal(np.concatenate(f64(out)), want.astype(np.float64))
 
 
+@pytest.mark.parametrize("vocab", [5, 4096, 4097, 300001])
+@pytest.mark.parametrize("n", [64, 65, 1025, 4097, 8191, 8192, 8193])
+def test_embedding_grad_sorts(n, vocab):
+    """Around what one launch sorts, and the table rows it marks at a time."""
+    g = gen(n + vocab)
+    ids = token_ids(g, [n // 3, n - n // 3], vocab, torch.int64)
+    ids[1][-1] = vocab - 1
+    d_outs = [normal(g, i.numel(), 3) for i in ids]
+    with session(2):
+        out = rr.embedding_grad(dev(ids), dev(d_outs), vocab)
+        torch.cuda.synchronize()
+    want = orc.embedding_grad_ordered(ints(ids), f64(d_outs), vocab, 1.0)
+    assert np.array_equal(np.concatenate(f64(out)), want.astype(np.float64))
+
+
 def test_embedding_passes_special_values_through():
     with session(1):
         bits = torch.tensor([0x7FC1, 0x7F80, 0xFF80, 0x8000, 0x0001, 0x7F7F, 0x3F80, 0x8001], dtype=torch.int32)
