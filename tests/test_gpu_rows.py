@@ -118,6 +118,12 @@ def check_route_grad(logits, experts, dtype, score, renormalize, scale, seed):
                 parts = q * (np.abs(gg) + np.abs((gg * q).sum()))
             else:
                 parts = np.abs(gg * p)
+                if score == "softmax":
+                    # p is the exponential in 64 bits over the float32 sum of all E, which is
+                    # off by (V + 17) u as in the weights (above): no more than E / 8 + 4 sums
+                    # a lane and three to six over the lanes, of exponentials off by
+                    # (t + 2) u; the bound below counts 2 u for each unit
+                    parts = parts * (1 + (min(x[r].shape[1] / 8 + 4, 32) + 17) / 2)
             for k, v in zip(ok, parts):
                 part[t, ex[r][t, k]] += v
             if score == "softmax" and not renormalize:
