@@ -19,7 +19,7 @@
 // matter - a handful - are computed again in 64 bits and decide, to their last
 // bit.  A double exp and division for every expert cost more than all the rest:
 // 131072 tokens of 256 experts in 8 groups with a bias, eight chosen, took 151 us
-// that way and take 69 (without bias or groups 43).
+// that way and take 66 (without bias or groups 40).
 //
 // Bound by instruction issue where there are many tokens: that case issues
 // 1770 vector instructions a wave of eight tokens, 49 us of the 69 if none ever
@@ -71,7 +71,7 @@ __device__ __forceinline__ double key_of(float score, uint32_t reversed) {
     // a float's double has 29 zeros at its end
     const uint64_t u = __builtin_bit_cast(uint64_t, max_of((double)score, __builtin_bit_cast(double, 0xffe0000000000000ull)));
     const uint32_t hi = (uint32_t)(u >> 32);
-    const uint32_t lo = (uint32_t)u | (reversed ^ ((uint32_t)((int32_t)hi >> 31) & (RC_MAX_EXPERTS - 1)));
+    const uint32_t lo = ((reversed ^ (uint32_t)((int32_t)hi >> 31)) & (RC_MAX_EXPERTS - 1)) | (uint32_t)u;
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 __device__ __forceinline__ int expert_of(double key) {
@@ -368,17 +368,19 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
                 for (int i = 0; i < 4; ++i) x[j + i] = kNone32;
             }
         }
-    } else {
+    } else if (a.vec) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = kNone32;
 #pragma unroll
         for (int j = 0; j < V; j += 4) {
             const int at = p.at(j);
-            if (p.in_group && a.vec && at < p.size) {
-                load4<T>(logits + p.base + at, x + j);
-            } else {
+            if (p.in_group && at < p.size) load4<T>(logits + p.base + at, x + j);
+        }
+    } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[j + i] = p.in_group && at + i < p.size ? T::load(logits[p.base + at + i]) : kNone32;
-            }
+        for (int j = 0; j < V; ++j) {
+            const int at = p.at(j);
+            x[j] = p.in_group && at < p.size ? T::load(logits[p.base + at]) : kNone32;
         }
     }
 
@@ -387,13 +389,19 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     float top = kNone32;
     bool broken = false;
     if (!a.sigmoid) {
+        // the bits of +inf and of NaNs are the largest, as signed numbers where the
+        // sign is clear and as unsigned ones where it is set
+        int32_t high = 0;
+        uint32_t negative = 0;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            top = x[j] > top ? x[j] : top;
-            broken |= !(x[j] < __builtin_inff());
+        for (int j = 0; j < V; j += 2) {
+            const int32_t u = __builtin_bit_cast(int32_t, x[j]), v = __builtin_bit_cast(int32_t, x[j + 1]);
+            asm("v_max3_f32 %0, %0, %1, %2" : "+v"(top) : "v"(x[j]), "v"(x[j + 1]));
+            high = max(high, max(u, v));
+            negative = max(negative, max((uint32_t)u, (uint32_t)v));
         }
         top = max_lanes<L>(top);
-        broken = max_lanes<L>((int)broken) != 0;
+        broken = max_lanes<L>((int)(high >= 0x7f800000 || negative > 0xff800000u)) != 0;
         if (top == kNone32) top = 0.0f;
     }
     // scores are needed where their order is not the logits'
@@ -406,31 +414,48 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     }
     const float share = a.sigmoid ? 0.0f : 1.0f / total;
     auto score32 = [&](float v) { return a.sigmoid ? sigmoid32(v) : exp32(v - top) * share; };
+    // the scores of all, kNone32 for logits that are that or NaN (the kind is
+    // asked once, not for each)
+    auto score_all = [&](float* to) {
+        if (a.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) to[j] = x[j] > kNone32 ? sigmoid32(x[j]) : kNone32;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) to[j] = x[j] > kNone32 ? exp32(x[j] - top) * share : kNone32;
+        }
+    };
     // x becomes what the choice goes by: nothing above the largest float, and
     // kNone32 for a NaN (v_max takes the other operand)
     const float huge = 3.4028234663852886e38f;
     auto tidy = [&](float v) { return min_of(max_of(v, kNone32), huge); };
     if (a.bias) {
+        float b[V];
 #pragma unroll
-        for (int j = 0; j < V; j += 4) {
-            const int at = p.at(j);
-            float b[4] = {};
-            if (p.in_group && a.bias_vec && at < p.size) {
-                F32::unpack(*reinterpret_cast<const u32x4*>(a.bias + p.base + at), b);
-            } else {
+        for (int j = 0; j < V; ++j) b[j] = 0.0f;
+        if (a.bias_vec) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (p.in_group && at + i < p.size) b[i] = a.bias[p.base + at + i];
+            for (int j = 0; j < V; j += 4) {
+                const int at = p.at(j);
+                if (p.in_group && at < p.size) F32::unpack(*reinterpret_cast<const u32x4*>(a.bias + p.base + at), b + j);
             }
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float c = tidy(score32(x[j + i]) + b[i]);
-                x[j + i] = x[j + i] > kNone32 ? c : kNone32;
+            for (int j = 0; j < V; ++j) {
+                const int at = p.at(j);
+                if (p.in_group && at < p.size) b[j] = a.bias[p.base + at];
             }
         }
-    } else {
+        score_all(x);
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = tidy(x[j] + b[j]);
+    } else if (a.sigmoid) {
 #pragma unroll
         for (int j = 0; j < V; ++j) x[j] = tidy(x[j] + 0.0f);  // one zero
+    } else {
+        // a NaN or +inf leaves nothing to choose from
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] += 0.0f;
     }
     // How close two values that decide something may come, of size up to
     // `size`.  The error of a score, in kU.  Sigmoid: 5.  Softmax: s <= share is
@@ -468,8 +493,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         bool doubt = false;
         const bool by_score = scored && !a.bias;
         if (by_score) {
+            float c[V];
+            score_all(c);
 #pragma unroll
-            for (int j = 0; j < V; ++j) best_two(first, second, x[j] > kNone32 ? score32(x[j]) : kNone32);
+            for (int j = 0; j < V; ++j) best_two(first, second, c[j]);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) best_two(first, second, x[j]);
