@@ -170,11 +170,12 @@ __device__ __forceinline__ void sort_values(double* v) {
     }
 }
 
-// list (sorted) becomes the KP largest of it and v.
+// list (sorted) becomes the KP largest of it and v; returns the one left out.
 template <int KP>
-__device__ __forceinline__ void insert(double* list, double v) {
+__device__ __forceinline__ double insert(double* list, double v) {
 #pragma unroll
     for (int k = 0; k < KP; ++k) order(list[k], v);
+    return v;
 }
 
 // list (sorted) becomes the KP largest of it and of m (sorted), sorted.
@@ -576,10 +577,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         const float near = near_of(max_of(best, __builtin_fabsf(last)));
         bool doubt = least >= 0.0f && least <= near;
         const float from = all ? last - near : -huge;
-        // a lane's KP best are enough to see whether more than top_k come as close
+        // A lane's KP best show whether more than top_k come as close, but for the
+        // lane whose KP best are all among those.
         int count = 0;
 #pragma unroll
         for (int k = 0; k < KP; ++k) count += own[k] >= from;
+        if (V > KP && __any(own[KP - 1] >= from)) {
+            count = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) count += kept && x[j] >= from;
+        }
         doubt |= all && sum_lanes<L>(count) > a.top_k;
         doubt = max_lanes<L>((int)doubt) != 0;
         if (__any(doubt)) {
@@ -592,6 +599,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             double list64[KP];
 #pragma unroll
             for (int k = 0; k < KP; ++k) list64[k] = kNone;
+            double past = kNone;  // the best that the lane's list has no place for
             for (uint32_t left = close; __any(left);) {
                 double key = kNone;
                 if (left) {
@@ -599,7 +607,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
                     key = key_of(exact(j), reversed(j));
                     left &= left - 1;
                 }
-                insert<KP>(list64, key);
+                past = max_of(past, insert<KP>(list64, key));
             }
             uint32_t held[KP];  // of the lane's best keys, what is the score's
 #pragma unroll
@@ -619,7 +627,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
                     before = u;
                 }
             }
-            int as_last = 0;
+            int as_last = (uint32_t)(__builtin_bit_cast(uint64_t, past) >> 10) == (uint32_t)before;
 #pragma unroll
             for (int k = 0; k < KP; ++k) as_last += held[k] == (uint32_t)before;
             same |= sum_lanes<L>(as_last) > 1;

@@ -210,6 +210,30 @@ def test_route_tells_close_scores_apart():
         check_route([fine], 5, "f32", score="sigmoid", bias=torch.full((E,), b), groups=4, top_groups=3)
 
 
+@pytest.mark.parametrize("K", [2, 4, 8, 16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_close_scores_in_one_group(K, score):
+    """All chosen experts, and the next one close behind, in one group of those
+    that are far apart: the last place goes by what float32 does not tell."""
+    g = gen(13)
+    E, size = 100, 20
+    for _ in range(2):
+        l = torch.full((6, E), -4.0)
+        l[:, 60:80] = torch.linspace(2.0, 0.0, size)[torch.argsort(torch.rand(6, size, generator=g), 1)]
+        for t in range(6):
+            rank = torch.argsort(l[t, 60:80], descending=True) + 60
+            l[t, rank[K]] = l[t, rank[K - 1]]  # the bias decides
+        # few tokens, and enough for a lane to have a group of its own
+        check_route([l, l.repeat(350, 1)], K, "f32", score=score, bias=torch.rand(E, generator=g) * 2.0 ** -28, groups=5,
+                    top_groups=1)
+    # and by what the upper 42 bits of the scores do not
+    fine = torch.full((6, E), 15.0)
+    for t in range(6):
+        fine[t, 60:80] = 18.0 + 2.0 ** -19 * torch.randperm(size, generator=g).float()
+    for b in (0.0, 0.25):
+        check_route([fine, fine.repeat(350, 1)], K, "f32", score="sigmoid", bias=torch.full((E,), b), groups=5, top_groups=1)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups", [1, 4])
 def test_route_extreme_logits(score, groups):
