@@ -1,9 +1,13 @@
 // Dispatch and combine: the plan (a counting sort of all ranks' choices by
 // expert) and the row moves between tokens and experts' ranks.
 //
-// All are bound by memory.  A row move gives one wave a piece of one token's
-// row: a dispatched row is read once and written to its K places, a combined
-// one is the sum of K places, held in float32 and rounded once.
+// A row move gives one wave a piece of one token's row: a dispatched row is read
+// once and written to its K places, a combined one is the sum of K places, held
+// in float32 and rounded once.  All are bound by memory: 16384 tokens of 4096
+// bf16, eight places each, take 221 us to dispatch (1.2 GB at 5.5 TB/s), 259 to
+// combine (4.7 TB/s) and 432 for the combination's gradient (2.3 GB at 5.3).
+// The plan is bound by latency: 131072 entries 15.8 us in two launches, 512 in
+// one, 5.3 us.
 #include "rows_sort.h"
 
 namespace rc {
@@ -297,6 +301,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(ExchangeArgs a) {
 
 // One workgroup per token: its waves take the row's pieces in turn, each lane
 // summing its own products, then all lanes' sums are joined in a fixed tree.
+// Rows and their products are read once for both gradients.
 constexpr int kGradThreads = 256;
 template <class T, int KP>
 __global__ __launch_bounds__(kGradThreads) void combine_grad_kernel(ExchangeArgs a) {

@@ -22,7 +22,7 @@
 // that way and take 66 (without bias or groups 40).
 //
 // Bound by instruction issue where there are many tokens: that case issues
-// 1770 vector instructions a wave of eight tokens, 49 us of the 69 if none ever
+// 1750 vector instructions a wave of eight tokens, 48 us of the 66 if none ever
 // waited; its 142 MB are 27 us at the rate of a large copy.
 #include "rows_impl.h"
 
@@ -615,8 +615,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             merge_lists<L, KP>(list64);
             // Keys whose scores agree to 2^-42: the bits cut off decide.  They are
             // few enough to be chosen anew, scores and experts apart; with no keys
-            // before, 256 experts with a bias and no groups take 67 us for 63; a
-            // bias of zeros on bf16 logits, with equal scores in every row, 73 for 114.
+            // before, 256 experts with a bias and no groups took 67 us for 63; a
+            // bias of zeros on bf16 logits, with equal scores in every row, 73 for 114
+            // (110 since).
             bool same = false;
             uint64_t before = 0;
 #pragma unroll
