@@ -12,9 +12,11 @@
 // Sorting takes 9 instructions per expert for KP = 8; running each expert
 // through a sorted list takes 16.
 //
-// The choice has to be that of the values in 64 bits.  Where the logits'
-// order is the scores' (no bias), the keys are made from the logits, exactly.
-// Otherwise the scores are computed in float32, with a bound on their error;
+// The choice has to be that of the values in 64 bits.  Without a bias the
+// logits' order is the scores', and the keys are made from the logits, exactly.
+// But logits that share a score in 64 bits (kind_of below) are told apart by
+// their index: once some are seen among the chosen, the scores are compared.
+// With a bias the scores are computed in float32, with a bound on their error;
 // where two that decide something are closer than that, the scores that could
 // matter - a handful - are computed again in 64 bits and decide, to their last
 // bit.  A double exp and division for every expert cost more than all the rest:
@@ -311,8 +313,12 @@ __device__ __forceinline__ void load4(const typename T::E* p, float* x) {
 // read pieces eight apart, of eight tokens, meet all banks.
 __device__ __forceinline__ int staged_at(int t, int q, int pieces) { return t * pieces + (q ^ (((q >> 3) + t) & 7)); }
 
+// With more than eight choices, 168 registers, a few of them spilled, for three
+// waves per SIMD: without the bound most variants take 172 to 175, for two
+// (131072 tokens, ten chosen of 512 experts: 301 us with it, 386 without; of 32:
+// 29 and 37).
 template <class T, int L, int V, int KP>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(kRouteThreads, KP == 16 ? 3 : 1) void route_kernel(RouteArgs a) {
     using E = typename T::E;
     extern __shared__ __align__(16) unsigned char route_lds[];
     int rank;
@@ -488,6 +494,19 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         return c < 1e290 ? c : 1e290;
     };
 
+    // Distinct logits u > v may share a score in 64 bits only if both are of one
+    // kind.  Sigmoid: 1, from 20 on (the score's steps of 2^-53 outgrow the
+    // logit's from 23 on); 2, up to 2^-16 in size; 3, from -700 down (below -709
+    // scores are 0).  Softmax: 3, from 690 below the largest (scores are below
+    // the normal range, or 0); 2, up to 2^-16 in size.  For others u - v is
+    // 2^-40 or more (a step of a float32 beyond 2^-16), while the rounding of
+    // v - top, 2^-44 below 690, and of the exponential and the quotient move
+    // what is compared by less than 2^-42.
+    const float high = a.sigmoid ? 20.0f : __builtin_inff(), low = a.sigmoid ? -700.0f : top - 690.0f, tiny = 0x1p-16f;
+    auto kind_of = [&](float v) { return v <= low ? 3 : v >= high ? 1 : __builtin_fabsf(v) <= tiny ? 2 : 0; };
+    // the least logit that may share v's score
+    auto least_of = [&](float v) { return v <= low ? -huge : v >= high ? high : __builtin_fabsf(v) <= tiny ? -tiny : v; };
+
     bool kept = true;
     if (a.groups > 1) {
         float first = kNone32, second = kNone32;
@@ -509,9 +528,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             near = near_of(max_lanes<L>(max_of(f < huge ? f : 0.0f, g < huge ? g : 0.0f)));
         }
         kept = group_kept<L>(a, p, first, second, near, &doubt);
+        if (!scored) {
+            // whether the best of two groups are of one kind and differ
+            const int kind = first > kNone32 ? kind_of(first) : 0;
+            if (__builtin_expect(__any(kind), 0)) {
+#pragma unroll 1
+                for (int q = 1; q <= 3; ++q) {
+                    const float most = max_lanes<L>(kind == q ? first : kNone32);
+                    const float least = -max_lanes<L>(kind == q ? -first : kNone32);
+                    doubt |= kind == q && most > least;
+                }
+            }
+        }
         if (__any(doubt)) {
             // what may be among its group's two best
-            const float from = (a.top2 ? second : first) - near;
+            const float from = scored ? (a.top2 ? second : first) - near : least_of(first);
             uint32_t close = 0;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -533,22 +564,25 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     kept &= !broken;
 
     auto reversed = [&](int j) { return (uint32_t)(RC_MAX_EXPERTS - 1 - (p.base + p.at(j))); };
-    double list[KP];
+    double list[KP], lowest;
     if constexpr (V < KP) {
 #pragma unroll
         for (int k = 0; k < KP; ++k) list[k] = kNone;
 #pragma unroll
         for (int j = 0; j < V; ++j) insert<KP>(list, key_of(x[j], reversed(j)));
+        lowest = list[V - 1];
     } else {
 #pragma unroll
         for (int j = 0; j < KP; ++j) list[j] = key_of(x[j], reversed(j));
         sort_values<KP>(list);
+        lowest = list[KP - 1];
 #pragma unroll
         for (int j0 = KP; j0 < V; j0 += KP) {
             double m[KP];
 #pragma unroll
             for (int j = 0; j < KP; ++j) m[j] = key_of(x[j0 + j], reversed(j0 + j));
             sort_values<KP>(m);
+            lowest = min_of(lowest, m[KP - 1]);
             merge_into<KP>(list, m);
         }
     }
@@ -671,6 +705,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     constexpr int kEach = (KP + L - 1) / L;
     int expert[kEach];
     double chosen[kEach], best = kNone, sum = 0.0;
+    bool odd = false;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         double key = kNone;
@@ -679,8 +714,68 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             if (k == lane + i * L && k < a.top_k) key = list[k];
         expert[i] = key > kNoKey ? expert_of(key) : -1;
         chosen[i] = expert[i] < 0 ? kNone : (double)T::load(logits[expert[i]]);
-        best = chosen[i] > best ? chosen[i] : best;
+        odd |= expert[i] >= 0 && kind_of((float)key);
     }
+    if (!a.bias && __builtin_expect(__any(odd), 0)) {
+        // neighbours among the chosen that may share a score, and whatever lies
+        // below the last of them and may share its
+        float last = 0.0f;
+        bool all = true, same = false;  // all: top_k could be chosen
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+            if (k >= a.top_k) continue;
+            const float c = (float)list[k];
+            const bool has = list[k] > kNoKey;
+            same |= has && k > 0 && c < last && c >= least_of(last);
+            all &= has;
+            last = c;
+        }
+        const float from = all ? least_of(last) : -huge;
+        bool below = all && kept && from < last && (float)lowest < last;
+        if (__any(same || max_lanes<L>((int)below))) {
+            // what may be chosen; from memory, since with x held for it the kernel
+            // would take a tenth more registers
+            uint32_t close = 0;
+            below = false;
+#pragma unroll 4
+            for (int j = 0; j < V; ++j) {
+                const int at = p.at(j);
+                const float v = kept && p.in_group && at < p.size ? tidy(T::load(logits[p.base + at]) + 0.0f) : kNone32;
+                below |= v >= from && v < last;
+                close = close + close + (uint32_t)(v >= from);
+            }
+            same |= all && max_lanes<L>((int)below);
+            if (!same) close = 0;
+            sum_exact();
+            // the next best each time, by score and then by index
+            double score = __builtin_inf();
+            int of = -1;
+#pragma unroll 1
+            for (int k = 0; k < a.top_k; ++k) {
+                double next = kNone;
+                int e = RC_MAX_EXPERTS;
+                for (uint32_t left = close; left; left &= left - 1) {
+                    const int j = V - 1 - __builtin_ctz(left), at = p.base + p.at(j);
+                    const double s = exact(j);
+                    const bool after = s < score || (s == score && at > of);
+                    if (after && (s > next || (s == next && at < e))) {
+                        next = s;
+                        e = at;
+                    }
+                }
+                score = max_lanes<L>(next);
+                of = RC_MAX_EXPERTS - max_lanes<L>(next == score ? RC_MAX_EXPERTS - e : 0);
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    if (!same || k != lane + i * L) continue;
+                    expert[i] = of < RC_MAX_EXPERTS ? of : -1;
+                    chosen[i] = expert[i] < 0 ? kNone : (double)T::load(logits[expert[i]]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) best = chosen[i] > best ? chosen[i] : best;
     // the chosen softmax scores relative to the largest chosen, or to all
     const bool relative = !a.sigmoid && a.renormalize;
     if (relative) best = max_lanes<L>(best);

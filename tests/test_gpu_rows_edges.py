@@ -1,0 +1,93 @@
+"""Row exchanges on the GPU where scores saturate, one expert outweighs all
+others, rows are masked out and sums leave float32's range.
+
+u = 2^-24 is float32's half step.  References are computed in 64 bits.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import rank_reductions_amd as rr
+from gpu_util import session
+from oracle import rows as orc
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+# ---------------------------------------------------------------- the order where scores saturate
+
+def saturated_rows(score, E, g):
+    """Rows of logits whose scores in 64 bits are exactly alike, however exp
+    rounds: sigmoids of one and of zero, softmax scores of zero, and logits too
+    small to move either; smaller logits at lower indices among them."""
+    def shuffled(v):
+        return v[torch.randperm(E, generator=g)]
+
+    up, plain = torch.arange(E).float(), torch.randn(E, generator=g)
+    far = 2.0 ** -70 * (up + 1)
+    few = plain.clone()
+    few[[1, 4, E - 2]] = torch.tensor([41.0, 47.0, 44.0])
+    masked = plain.clone()
+    masked[E // 3:] = shuffled(-1e4 - 16 * up)[E // 3:]
+    most = torch.full((E,), -1e4)
+    most[[2, E - 1]] = torch.tensor([1.0, -9e3])
+    most[1::2] -= 512
+    rows = [shuffled(-900.0 - up), masked, most, shuffled(far), shuffled(-far), shuffled(far - 2.0 ** -70 * E / 2),
+            torch.where(shuffled(up) < E / 2, shuffled(far), -3.0), torch.zeros(E), few]
+    if score == "sigmoid":
+        rows += [40.0 + up, shuffled(40.0 + up), torch.where(up % 3 == 0, 60 - up / E, -800.0 - up)]
+    else:
+        rows += [torch.where(shuffled(up) < 3, 5.0, shuffled(far)), torch.where(shuffled(up) < 1, 900.0, plain),
+                 torch.where(shuffled(up) < 2, 900.0, shuffled(far))]
+    return torch.stack(rows)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K,groups,top_groups,group_by", [
+    (12, 4, 1, 1, "max"), (60, 16, 1, 1, "max"), (256, 8, 1, 1, "max"), (320, 8, 1, 1, "max"),
+    (32, 4, 4, 2, "max"), (256, 8, 8, 3, "max"), (256, 8, 8, 3, "top2"), (60, 5, 12, 4, "max"), (40, 3, 40, 6, "top2"),
+])
+def test_saturated_scores_go_to_the_lower_index(dtype, score, E, K, groups, top_groups, group_by):
+    """With no bias and with one of zeros, few tokens and many."""
+    l = saturated_rows(score, E, gen(E + K)).to(TYPES[dtype])
+    kw = dict(score=score, groups=groups, top_groups=top_groups, group_by=group_by)
+    _, want = orc.route([l.double().numpy()], K, **kw)
+    times = 200
+    with session(1):
+        for bias in (None, torch.zeros(E, device=DEV)):
+            for reps in (1, times):
+                _, e = rr.route([l.repeat(reps, 1).to(DEV)], K, bias=bias, **kw)
+                e = e[0].cpu().numpy().reshape(reps, *want[0].shape)
+                for t in range(want[0].shape[0]):
+                    assert (e[:, t] == want[0][t]).all(), \
+                        f"bias {bias is not None}, {reps} times, row {t}: {e[0, t]} not {want[0][t]}"
+
+
+def test_neighbouring_logits_with_one_sigmoid():
+    """Steps of a float32 logit that a double's sigmoid does not follow: from
+    about 24 on.  The sums 1 + exp(-x) lie on a grid of 2^-52, and exp(-x) is
+    known to 2^-87: the reference's rounding is the kernel's."""
+    E = 24
+    g = gen(5)
+    for base in (23.0, 24.0, 25.0, 30.0, 36.5):
+        l = torch.full((5, E), base)
+        for t in range(5):
+            l[t] += 2.0 ** -19 * torch.randperm(E, generator=g).float()
+        _, want = orc.route([l.double().numpy()], 7, score="sigmoid")
+        with session(1):
+            for bias in (None, torch.zeros(E, device=DEV)):
+                _, e = rr.route([l.to(DEV)], 7, score="sigmoid", bias=bias)
+                assert np.array_equal(e[0].cpu().numpy(), want[0]), f"at {base}, bias {bias is not None}"
