@@ -36,6 +36,7 @@ constexpr double kNone = -__builtin_inf();
 constexpr float kNone32 = -__builtin_inff();
 constexpr double kNoKey = -1e300;  // keys of what cannot be chosen lie below
 constexpr float kU = 0x1p-24f;
+constexpr float kHuge = 3.4028234663852886e38f;
 
 // v_max / v_min as they are: no operand is ever NaN, so the quieting that fmax
 // and fmin would add has nothing to do.
@@ -268,7 +269,13 @@ __device__ __forceinline__ bool group_kept(const RouteArgs& a, const Part& p, C&
         second = max_of(min_of(first, f), max_of(second, s));
         first = max_of(first, f);
     }
-    const C of_group = a.top2 && a.group_size > 1 ? first + second : first;
+    C of_group = first;
+    if (a.top2 && a.group_size > 1) {
+        of_group = first + second;
+        // float32's largest where the sum lies beyond it: not an infinity, which is
+        // apart from no other and, below, is a group with nothing to add
+        if constexpr (sizeof(C) == 4) of_group = second > kNone32 ? __builtin_amdgcn_fmed3f(of_group, -kHuge, kHuge) : kNone32;
+    }
     int better = 0;
     auto against = [&](C other, bool lower) {
         better += other > of_group || (other == of_group && lower);
@@ -434,8 +441,7 @@ __global__ __launch_bounds__(kRouteThreads, KP == 16 ? 3 : 1) void route_kernel(
     };
     // x becomes what the choice goes by: nothing above the largest float, and
     // kNone32 for a NaN (v_max takes the other operand)
-    const float huge = 3.4028234663852886e38f;
-    auto tidy = [&](float v) { return min_of(max_of(v, kNone32), huge); };
+    auto tidy = [&](float v) { return min_of(max_of(v, kNone32), kHuge); };
     if (a.bias) {
         float b[V];
 #pragma unroll
@@ -472,7 +478,7 @@ __global__ __launch_bounds__(kRouteThreads, KP == 16 ? 3 : 1) void route_kernel(
     // result, a group's sum of two by as much again: the difference of two such
     // sums is off by this at most.
     const float error = a.sigmoid ? 6.0f : 2.0f + share * (float)(V + 32);
-    auto near_of = [&](float size) { return 4.0f * kU * (error + 2.0f * (size < huge ? max_of(size, 1.0f) : 1.0f)); };
+    auto near_of = [&](float size) { return 4.0f * kU * (error + 2.0f * (size < kHuge ? max_of(size, 1.0f) : 1.0f)); };
 
     // scores in 64 bits, from the logits and the bias
     double sum64 = 0.0;
@@ -505,7 +511,7 @@ __global__ __launch_bounds__(kRouteThreads, KP == 16 ? 3 : 1) void route_kernel(
     const float high = a.sigmoid ? 20.0f : __builtin_inff(), low = a.sigmoid ? -700.0f : top - 690.0f, tiny = 0x1p-16f;
     auto kind_of = [&](float v) { return v <= low ? 3 : v >= high ? 1 : __builtin_fabsf(v) <= tiny ? 2 : 0; };
     // the least logit that may share v's score
-    auto least_of = [&](float v) { return v <= low ? -huge : v >= high ? high : __builtin_fabsf(v) <= tiny ? -tiny : v; };
+    auto least_of = [&](float v) { return v <= low ? -kHuge : v >= high ? high : __builtin_fabsf(v) <= tiny ? -tiny : v; };
 
     bool kept = true;
     if (a.groups > 1) {
@@ -525,7 +531,7 @@ __global__ __launch_bounds__(kRouteThreads, KP == 16 ? 3 : 1) void route_kernel(
         float near = -1.0f;
         if (scored) {
             const float f = __builtin_fabsf(first), g = __builtin_fabsf(second);
-            near = near_of(max_lanes<L>(max_of(f < huge ? f : 0.0f, g < huge ? g : 0.0f)));
+            near = near_of(max_lanes<L>(max_of(f < kHuge ? f : 0.0f, g < kHuge ? g : 0.0f)));
         }
         kept = group_kept<L>(a, p, first, second, near, &doubt);
         if (!scored) {
@@ -610,7 +616,7 @@ __global__ __launch_bounds__(kRouteThreads, KP == 16 ? 3 : 1) void route_kernel(
         }
         const float near = near_of(max_of(best, __builtin_fabsf(last)));
         bool doubt = least >= 0.0f && least <= near;
-        const float from = all ? last - near : -huge;
+        const float from = all ? last - near : -kHuge;
         // A lane's KP best show whether more than top_k come as close, but for the
         // lane whose KP best are all among those.
         int count = 0;
@@ -730,7 +736,7 @@ __global__ __launch_bounds__(kRouteThreads, KP == 16 ? 3 : 1) void route_kernel(
             all &= has;
             last = c;
         }
-        const float from = all ? least_of(last) : -huge;
+        const float from = all ? least_of(last) : -kHuge;
         bool below = all && kept && from < last && (float)lowest < last;
         if (__any(same || max_lanes<L>((int)below))) {
             // what may be chosen; from memory, since with x held for it the kernel

@@ -91,3 +91,31 @@ def test_neighbouring_logits_with_one_sigmoid():
             for bias in (None, torch.zeros(E, device=DEV)):
                 _, e = rr.route([l.to(DEV)], 7, score="sigmoid", bias=bias)
                 assert np.array_equal(e[0].cpu().numpy(), want[0]), f"at {base}, bias {bias is not None}"
+
+
+# ---------------------------------------------------------------- groups masked by the lowest value
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("big", [3.4028234663852886e38, 2.5e38])
+def test_group_sums_past_float32(score, big):
+    """A bias of the type's lowest value (or near its largest): two of them add
+    up beyond float32, not beyond the 64 bits that decide."""
+    E, G = 32, 4
+    g = gen(3)
+    l = torch.randn(20, E, generator=g)
+    l[::2, :8] = -math.inf  # group 0 has nothing to choose
+    low = torch.zeros(E)
+    low[:24] = -big
+    high = torch.zeros(E)
+    high[8:16] = big * 0.9
+    high[16:24] = big
+    for bias in (low, high, -high):
+        for top_groups in (1, 2, 3):
+            K = 8 if top_groups == 1 else 12  # more than one group has
+            kw = dict(score=score, groups=G, top_groups=top_groups, group_by="top2")
+            _, want = orc.route([l.double().numpy()], K, bias=bias.double().numpy(), **kw)
+            with session(1):
+                for reps in (1, 120):
+                    _, e = rr.route([l.repeat(reps, 1).to(DEV)], K, bias=bias.to(DEV), **kw)
+                    got = e[0].cpu().numpy().reshape(reps, 20, K)
+                    assert (got == want[0]).all(), f"bias {bias[0]}, {bias[8]}: {got[0]} not {want[0]}"
