@@ -616,7 +616,7 @@ __global__ __launch_bounds__(kRouteThreads, KP == 16 ? 3 : 1) void route_kernel(
         }
         const float near = near_of(max_of(best, __builtin_fabsf(last)));
         bool doubt = least >= 0.0f && least <= near;
-        const float from = all ? last - near : -kHuge;
+        const float from = all ? max_of(last - near, -kHuge) : -kHuge;  // -inf is never chosen
         // A lane's KP best show whether more than top_k come as close, but for the
         // lane whose KP best are all among those.
         int count = 0;

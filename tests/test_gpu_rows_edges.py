@@ -119,3 +119,20 @@ def test_group_sums_past_float32(score, big):
                     _, e = rr.route([l.repeat(reps, 1).to(DEV)], K, bias=bias.to(DEV), **kw)
                     got = e[0].cpu().numpy().reshape(reps, 20, K)
                     assert (got == want[0]).all(), f"bias {bias[0]}, {bias[8]}: {got[0]} not {want[0]}"
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("big", [3.4028234663852886e38, 2.5e38, -2.5e38])
+def test_masked_experts_under_a_large_bias(score, big):
+    """A margin beyond float32's range takes in no expert that is masked out."""
+    E, K = 32, 6
+    g = gen(4)
+    l = torch.randn(20, E, generator=g)
+    l[:, ::3] = -math.inf
+    for bias in (torch.full((E,), big), torch.where(torch.arange(E) % 2 == 0, big, 0.0)):
+        _, want = orc.route([l.double().numpy()], K, score=score, bias=bias.double().numpy())
+        with session(1):
+            for reps in (1, 120):
+                _, e = rr.route([l.repeat(reps, 1).to(DEV)], K, score=score, bias=bias.to(DEV))
+                got = e[0].cpu().numpy().reshape(reps, 20, K)
+                assert (got == want[0]).all(), f"bias {bias[0]}, {bias[1]}: {got[0]} not {want[0]}"
