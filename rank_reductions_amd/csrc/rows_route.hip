@@ -85,6 +85,25 @@ __device__ __forceinline__ int expert_of(double key) {
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
+// exp(t) for t <= 0 within 2^-36 of itself, 0 where a double's would be near
+// its end: 2^n times the series of r = t - n ln 2, |r| < 0.347, up to r^9 (the
+// next term is 2^-37, the roundings 2^-50).
+__device__ __forceinline__ double exp_of(double t) {
+    t = max_of(t, -1000.0);
+    const double n = __builtin_rint(t * 1.4426950408889634), r = __builtin_fma(n, -0.69314718055994531, t);
+    double s = 1.0 / 362880;
+    s = __builtin_fma(s, r, 1.0 / 40320);
+    s = __builtin_fma(s, r, 1.0 / 5040);
+    s = __builtin_fma(s, r, 1.0 / 720);
+    s = __builtin_fma(s, r, 1.0 / 120);
+    s = __builtin_fma(s, r, 1.0 / 24);
+    s = __builtin_fma(s, r, 1.0 / 6);
+    s = __builtin_fma(s, r, 0.5);
+    s = __builtin_fma(s, r, 1.0);
+    s = __builtin_fma(s, r, 1.0);
+    return __builtin_amdgcn_ldexp(s, (int)n);
+}
+
 // exp(x) for x <= 0 within (1.25 |x| + 2) kU of itself, and the sigmoid within
 // 5 kU: the exponent's rounding and the constant's, one step of v_exp and of
 // v_rcp, and one sum.
@@ -806,7 +825,7 @@ __global__ __launch_bounds__(kRouteThreads, KP == 16 ? 3 : 1) void route_kernel(
 
 // The weights' gradient.  Each token's row of E values is put together in LDS:
 // cleared (or filled with the softmax's part that every expert has), then each
-// lane adds its choices' parts; where a token names an expert twice, its parts
+// lane writes its choices' parts; where a token names an expert twice, its parts
 // are added in order of k.  Bound by the writes and the 64-bit scores of the
 // chosen: 131072 tokens of 256 experts, eight chosen by sigmoid, 37.5 us (27 at
 // the rate of a copy); two exponentials and divisions a score instead of one,
@@ -842,48 +861,6 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a) 
         g[i] = has ? (double)a.scale * (double)a.d_weights[rank][j] : 0.0;
         best = x[i] > best ? x[i] : best;
     }
-    const bool any = max_lanes<L>((int)(expert[0] >= 0 || expert[kEach - 1] >= 0)) != 0;
-    const bool full = !a.sigmoid && !a.renormalize;  // the softmax over all experts
-    float top = -__builtin_inff(), total = 0.0f;
-    if (full && any && live) {
-        for (int e = lane; e < a.num_experts; e += L) {
-            const float v = T::load(logits[e]);
-            top = v > top ? v : top;
-        }
-    }
-    if (full) {
-        top = max_lanes<L>(top);
-        if (any && live)
-            for (int e = lane; e < a.num_experts; e += L) total += expf(T::load(logits[e]) - top);
-        total = sum_lanes<L>(total);
-    }
-    if (!a.sigmoid && a.renormalize) best = max_lanes<L>(best);
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        p[i] = 0.0;
-        if (expert[i] < 0) continue;
-        if (a.sigmoid) {
-            // s and 1 - s, from one exponential and one division
-            const double e = exp(-__builtin_fabs(x[i])), one = 1.0 / (1.0 + e);
-            p[i] = x[i] < 0.0 ? e * one : one;
-            rest[i] = x[i] < 0.0 ? one : e * one;
-        } else p[i] = full ? exp(x[i] - (double)top) / (double)total : exp(x[i] - best);
-        sum += p[i];
-    }
-    if (a.renormalize) {
-        sum = sum_lanes<L>(sum);
-        if (!(sum > 0.0)) sum = __builtin_inf();
-    }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) dot += g[i] * (a.renormalize ? p[i] / sum : p[i]);
-    dot = sum_lanes<L>(dot);
-    float part[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        double d = a.renormalize ? p[i] / sum * (g[i] - dot) : g[i] * p[i];
-        if (a.sigmoid && expert[i] >= 0) d *= rest[i];
-        part[i] = (float)d;
-    }
     // whether a token names an expert twice: each choice writes its number at its
     // expert's place, and one of two finds the other's
     bool alone = true;
@@ -895,26 +872,134 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a) 
     for (int i = 0; i < kEach; ++i)
         if (expert[i] >= 0) alone &= mine[expert[i]] == (float)(lane + i * L);
     wave_sync();
+    const bool doubled = __any(!alone);
+    const int first_lane = threadIdx.x & (kWave - 1) & ~(L - 1);
+
+    const bool full = !a.sigmoid && !a.renormalize;  // the softmax over all experts
+    const bool any = max_lanes<L>((int)(expert[0] >= 0 || expert[kEach - 1] >= 0)) != 0;
+    float part[kEach], top = kNone32, all = 0.0f;  // all: what every expert has of the softmax's part, but for its exponential
+    // f(expert, logit) for the lane's experts, and -inf behind the last
+    auto each = [&](auto f) {
+        if (!any || !live) return;
+        for (int e = lane * 4; e < a.num_experts; e += L * 4) {
+            float v[4];
+            if (a.vec) load4<T>(logits + e, v);
+            else
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = e + i < a.num_experts ? T::load(logits[e + i]) : kNone32;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f(e + i, v[i]);
+        }
+    };
+    if (full) {
+        // the largest logit's expert, the lowest of several
+        int m = a.num_experts;
+        each([&](int e, float v) {
+            m = v > top ? e : m;
+            top = v > top ? v : top;
+        });
+        const float own = top;
+        top = max_lanes<L>(top);
+        m = a.num_experts - max_lanes<L>(own == top ? a.num_experts - m : 0);
+        double others = 0.0;  // exponentials but the largest's, which is one
+        each([&](int e, float v) { others += e == m ? 0.0 : exp_of((double)v - (double)top); });
+        others = sum_lanes<L>(others);
+        const double share = 1.0 / (1.0 + others);
+        // With D_e the sum of the g of e's choices, d_e = s_e (D_e - sum_j s_j D_j).
+        // What stands in brackets is (D_e - D_m) - sum_j s_j (D_j - D_m): near one
+        // expert that outweighs the others, the sum's terms are as small as the
+        // result, and nothing cancels.
+        double of_m = 0.0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            p[i] = any && expert[i] >= 0 ? exp(x[i] - (double)top) * share : 0.0;
+            if (expert[i] == m) of_m += g[i];
+            else dot += g[i] * p[i];
+        }
+        of_m = sum_lanes<L>(of_m);
+        dot = sum_lanes<L>(dot);
+        const double apart = dot - of_m * (others * share);
+        all = any ? (float)(-(dot + of_m * share) * share) : 0.0f;
+        double d[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) d[i] = g[i];
+        if (doubled) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) d[i] = 0.0;
+#pragma unroll 1
+            for (int k = 0; k < a.top_k; ++k) {
+                const int from = first_lane + k % L;
+                const int e = __shfl(k < L ? expert[0] : expert[kEach - 1], from);
+                const double v = __shfl(k < L ? g[0] : g[kEach - 1], from);
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) d[i] += e == expert[i] ? v : 0.0;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) part[i] = (float)(p[i] * ((expert[i] == m ? 0.0 : d[i] - of_m) - apart));
+    } else {
+        int m = 0;
+        if (a.renormalize) {
+            // the largest logit's choice, the first of several
+            best = max_lanes<L>(best);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) m = max(m, x[i] == best ? KP - (lane + i * L) : 0);
+            m = KP - max_lanes<L>(m);
+        }
+        double of_m = 0.0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (lane + i * L == m) of_m = g[i];
+            p[i] = 0.0;
+            if (expert[i] < 0) continue;
+            if (a.sigmoid) {
+                // s and 1 - s, from one exponential and one division
+                const double e = exp(-__builtin_fabs(x[i])), one = 1.0 / (1.0 + e);
+                p[i] = x[i] < 0.0 ? e * one : one;
+                rest[i] = x[i] < 0.0 ? one : e * one;
+            } else p[i] = exp(x[i] - best);
+            sum += p[i];
+        }
+        if (a.renormalize) {
+            sum = sum_lanes<L>(sum);
+            if (!(sum > 0.0)) sum = __builtin_inf();
+            of_m = sum_lanes<L>(of_m);
+            // g - sum_j q_j g_j as (g - g_m) - sum_j q_j (g_j - g_m): as above
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                p[i] /= sum;
+                g[i] -= of_m;
+                dot += g[i] * p[i];
+            }
+            dot = sum_lanes<L>(dot);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            double d = p[i] * (g[i] - dot);
+            if (a.sigmoid && expert[i] >= 0) d *= rest[i];
+            part[i] = (float)d;
+        }
+    }
     // the row; lane l makes the experts 4 l .. 4 l + 3 and every 4 L on
     for (int e = lane * 4; e < a.num_experts; e += L * 4) {
         float v[4] = {};
         if (full && any && live) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (e + i < a.num_experts) v[i] = -(float)dot * (expf(T::load(logits[e + i]) - top) / total);
+                if (e + i < a.num_experts) v[i] = all * expf(T::load(logits[e + i]) - top);
         }
         *reinterpret_cast<u32x4*>(mine + e) = F32::pack(v);
     }
     wave_sync();
-    if (!__any(!alone)) {
+    if (full || !doubled) {  // of the full softmax, the chosen experts' parts are whole
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
-            if (expert[i] >= 0) mine[expert[i]] += part[i];
+            if (expert[i] >= 0) mine[expert[i]] = part[i];
     } else {
         // in order of k, each expert's by the lane that holds it
 #pragma unroll 1
         for (int k = 0; k < a.top_k; ++k) {
-            const int from = (threadIdx.x & (kWave - 1) & ~(L - 1)) + k % L;
+            const int from = first_lane + k % L;
             const int e = __shfl(k < L ? expert[0] : expert[kEach - 1], from);
             const float v = __shfl(k < L ? part[0] : part[kEach - 1], from);
             if (e >= 0 && e / 4 % L == lane) mine[e] += v;

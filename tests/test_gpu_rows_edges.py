@@ -136,3 +136,62 @@ def test_masked_experts_under_a_large_bias(score, big):
                 _, e = rr.route([l.repeat(reps, 1).to(DEV)], K, score=score, bias=bias.to(DEV))
                 got = e[0].cpu().numpy().reshape(reps, 20, K)
                 assert (got == want[0]).all(), f"bias {bias[0]}, {bias[1]}: {got[0]} not {want[0]}"
+
+
+# ---------------------------------------------------------------- a softmax over all experts
+
+def exact_grad(x, experts, dw, renormalize):
+    """d_logits of one token without cancellation: with D_e the sum of the
+    d_weights of e's choices, d_e = s_e sum_j s_j (D_e - D_j); with renormalize
+    the same over the choices, of weights q_k, added up for each expert.  With
+    the sums of the added parts' sizes."""
+    x = np.asarray(x, np.float64)
+    if not renormalize:
+        D = np.array([sum(d for e, d in zip(experts, dw) if e == j) for j in range(x.size)])
+        s = np.exp(x - x.max())
+        s /= math.fsum(s)
+        out = np.array([s[e] * math.fsum(s * (D[e] - D)) for e in range(x.size)])
+        return out, np.abs(out)
+    dw = np.array(dw)
+    q = np.exp(x[experts] - x[experts].max())
+    q /= math.fsum(q)
+    out, size = np.zeros_like(x), np.zeros_like(x)
+    for e, p, d in zip(experts, q, dw):
+        part = p * math.fsum(q * (d - dw))
+        out[e] += part
+        size[e] += abs(part)
+    return out, size
+
+
+@pytest.mark.parametrize("E", [8, 300])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_gradient_where_one_expert_outweighs_the_others(E, renormalize):
+    """1 - p of a confident choice, against the exact gradient and relative to it:
+    64-bit terms off by 2^-36 at most, added without cancellation, rounded to
+    float32 once for a chosen expert; of the others six roundings, and their
+    exponentials' arguments.  d_weights are whole numbers, so that their
+    differences are exact."""
+    gaps = [3, 9, 12, 15, 17, 20, 25, 40, 60]
+    choose = [[5], [5, 2], [2, 5, 0], [2, 0], [5, 2, 5], [0, 2, 0]]
+    for experts in choose:
+        K = len(experts)
+        l = torch.linspace(0.0, 1.0, E).repeat(len(gaps), 1)
+        for t, gap in enumerate(gaps):
+            l[t, 5] = float(gap) + 1
+        dw = torch.tensor([[3.0, 3.0, -2.0][:K]] * len(gaps))
+        ex = torch.tensor([experts] * len(gaps), dtype=torch.int32)
+        with session(1):
+            d = rr.route_grad([l.to(DEV)], [ex.to(DEV)], [dw.to(DEV)], renormalize=renormalize)[0].cpu().double().numpy()
+        for t, gap in enumerate(gaps):
+            x = l[t].double().numpy()
+            want, size = exact_grad(x, experts, dw[t].tolist(), renormalize)
+            bound = size * U * 1.001
+            for e in set(experts):
+                if renormalize and experts.count(e) > 1:  # each part is rounded, then their sum
+                    bound[e] += np.abs(want[e]) * U * 1.001
+            if not renormalize:
+                for e in range(E):
+                    if e not in experts:
+                        bound[e] = np.abs(want[e]) * U * (8 + x.max() - x[e])
+            over = np.abs(d[t] - want) - bound - 2.0 ** -149
+            assert over.max() <= 0, f"{experts}, gap {gap}, expert {over.argmax()}: {d[t][over.argmax()]!r} not {want[over.argmax()]!r}"
