@@ -876,7 +876,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a) 
     const int first_lane = threadIdx.x & (kWave - 1) & ~(L - 1);
 
     const bool full = !a.sigmoid && !a.renormalize;  // the softmax over all experts
-    const bool any = max_lanes<L>((int)(expert[0] >= 0 || expert[kEach - 1] >= 0)) != 0;
+    bool any = max_lanes<L>((int)(expert[0] >= 0 || expert[kEach - 1] >= 0)) != 0;
     float part[kEach], top = kNone32, all = 0.0f;  // all: what every expert has of the softmax's part, but for its exponential
     // f(expert, logit) for the lane's experts, and -inf behind the last
     auto each = [&](auto f) {
@@ -894,13 +894,17 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a) 
     if (full) {
         // the largest logit's expert, the lowest of several
         int m = a.num_experts;
+        bool broken = false;
         each([&](int e, float v) {
+            broken |= v != v;
             m = v > top ? e : m;
             top = v > top ? v : top;
         });
         const float own = top;
         top = max_lanes<L>(top);
         m = a.num_experts - max_lanes<L>(own == top ? a.num_experts - m : 0);
+        // no score is a number, and none has a part
+        any &= !max_lanes<L>((int)broken) && __builtin_fabsf(top) < __builtin_inff();
         double others = 0.0;  // exponentials but the largest's, which is one
         each([&](int e, float v) { others += e == m ? 0.0 : exp_of((double)v - (double)top); });
         others = sum_lanes<L>(others);
@@ -945,6 +949,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a) 
 #pragma unroll
             for (int i = 0; i < kEach; ++i) m = max(m, x[i] == best ? KP - (lane + i * L) : 0);
             m = KP - max_lanes<L>(m);
+            if (best == kNone) best = 0.0;
         }
         double of_m = 0.0;
 #pragma unroll

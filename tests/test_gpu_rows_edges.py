@@ -195,3 +195,25 @@ def test_gradient_where_one_expert_outweighs_the_others(E, renormalize):
                         bound[e] = np.abs(want[e]) * U * (8 + x.max() - x[e])
             over = np.abs(d[t] - want) - bound - 2.0 ** -149
             assert over.max() <= 0, f"{experts}, gap {gap}, expert {over.argmax()}: {d[t][over.argmax()]!r} not {want[over.argmax()]!r}"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("E", [8, 300])
+def test_gradient_of_masked_rows_is_zero(dtype, renormalize, E):
+    """Rows masked out altogether whose experts are named all the same, and
+    rows whose named experts alone are masked out."""
+    l = torch.randn(6, E, generator=gen(1))
+    l[0] = -math.inf
+    l[1, [1, 3]] = -math.inf
+    l[2] = -math.inf
+    l[2, 5] = 1.0
+    l[5] = -math.inf
+    ex = torch.tensor([[1, 3]] * 5 + [[-1, 3]], dtype=torch.int32)
+    dw = torch.tensor([[1.0, 2.0]] * 6)
+    with session(1):
+        d = rr.route_grad([l.to(TYPES[dtype]).to(DEV)], [ex.to(DEV)], [dw.to(DEV)], renormalize=renormalize)[0].cpu()
+    assert torch.isfinite(d).all()
+    for t in (0, 1, 2, 5):
+        assert not d[t].any(), f"row {t}: {d[t]}"
+    assert d[3].any() and d[4].any()
