@@ -140,6 +140,30 @@ def test_masked_experts_under_a_large_bias(score, big):
 
 # ---------------------------------------------------------------- a softmax over all experts
 
+@pytest.mark.parametrize("E,K,bias", [(8, 2, False), (8, 6, False), (64, 4, False), (256, 8, False), (256, 8, True),
+                                      (600, 12, False), (1000, 16, True)])
+@pytest.mark.parametrize("std", [2, 6])
+def test_weights_of_a_full_softmax(E, K, bias, std):
+    """Rounded once, u, but for the sum's error: the terms of experts that were
+    not chosen are float32 exponentials, each off by (2 t + 2) u at t below the
+    largest logit (the roundings of t and of t log2 e, a step of v_exp)."""
+    g = gen(E + K)
+    l = torch.randn(2100, E, generator=g) * std
+    b = torch.randn(E, generator=g) * 0.1 if bias else None
+    x = l.double()
+    t = x.amax(1, keepdim=True) - x
+    s = torch.exp(-t) / torch.exp(-t).sum(1, keepdim=True)
+    for rows in (7, 2100):
+        with session(1):
+            w, e = rr.route([l[:rows].to(DEV)], K, bias=None if b is None else b.to(DEV), renormalize=False, scale=2.0)
+        at = e[0].cpu().long()
+        want = 2 * torch.gather(s[:rows], 1, at)
+        other = (s * (2 * t + 2))[:rows].scatter(1, at, 0.0).sum(1, keepdim=True)
+        off = (w[0].cpu().double() - want).abs() / want
+        bound = U * (1 + other) * (1 + 2.0 ** -10)
+        assert (off <= bound).all(), f"{rows} rows: {((off - bound) / U).max().item()} roundings past {other.max().item()}"
+
+
 def exact_grad(x, experts, dw, renormalize):
     """d_logits of one token without cancellation: with D_e the sum of the
     d_weights of e's choices, d_e = s_e sum_j s_j (D_e - D_j); with renormalize
