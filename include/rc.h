@@ -346,8 +346,13 @@ int rc_reset(void);
  * Indices on the GPU cannot be checked before the launch: an expert, slot or
  * token id out of range is never followed, and counts as "none".
  *
+ * Descriptors end with `session`: 0, or what rc_session_id gave.  A caller that
+ * made its arrays for the session's rank count and GPU gives it, so that the
+ * call is refused if another thread has closed that session since.  A
+ * struct_size without it (offsetof(..., session)) is a session of 0.
+ *
  * Checks, in this order, before anything is enqueued: NOT_REGISTERED;
- * INVALID_ARGUMENT for malformed fields, NULL or misaligned pointers, counts
+ * INVALID_ARGUMENT for malformed fields, another session than the given, NULL or misaligned pointers, counts
  * whose total passes 2^31 - 1, a workspace too small; INVALID_ARGUMENT for an
  * output that overlaps another output or any input.  A call with nothing to
  * do returns RC_OK.  Only kernels are enqueued, and all scratch is the
@@ -386,6 +391,7 @@ typedef struct rc_route_desc {
     int32_t renormalize;
     float scale;
     const float* bias;
+    int64_t session;
 } rc_route_desc;
 
 /* Chooses K experts for every token.  logits[r]: [tokens[r], E]; weights[r]
@@ -429,6 +435,7 @@ typedef struct rc_exchange_desc {
     const int64_t* capacity;
     const int32_t* const* experts;
     int32_t* const* slots;
+    int64_t session;
 } rc_exchange_desc;
 
 /* Places every (rank, token, k): each rank's rows are ordered by expert, then
@@ -480,6 +487,7 @@ typedef struct rc_embedding_desc {
     int64_t width;
     const int64_t* tokens;
     const void* const* ids;
+    int64_t session;
 } rc_embedding_desc;
 
 /* outs[r][t] = scale * table[ids[r][t]] (bit for bit with a scale of 1); zeros
@@ -499,6 +507,10 @@ int rc_embedding_grad(const rc_embedding_desc* desc, const void* const* d_outs, 
 /* The open session's rank count and GPU (-1 in a validate_only session opened
  * without one).  RC_ERR_NOT_REGISTERED if no session is open. */
 int rc_session_info(int* num_ranks, int* device);
+
+/* A number of the open session, another one for each.  Asked before
+ * rc_session_info, it tells whether that was of the same session. */
+int rc_session_id(int64_t* id);
 
 /* ------------------------------------------------------------------------
  * Per-rank front end.  Each logical rank registers itself and issues its own

@@ -63,10 +63,16 @@ void call(F f) {
     throw Raised{};
 }
 
+// The open session; `id` goes with the call, so that another session, opened by
+// another thread in the meantime, is not taken for it.
 struct Session {
+    int64_t id = 0;
     int ranks = 0, device = -1;
     Session() {
-        call([&] { return rc_session_info(&ranks, &device); });
+        call([&] {
+            const int e = rc_session_id(&id);
+            return e ? e : rc_session_info(&ranks, &device);
+        });
     }
 };
 
@@ -89,8 +95,8 @@ struct Tensors {
     bool owned = false;
     int n = 0;
     Tensor made[RC_MAX_RANKS];
-    const Tensor* t[RC_MAX_RANKS];
-    void* p[RC_MAX_RANKS];
+    const Tensor* t[RC_MAX_RANKS] = {};
+    void* p[RC_MAX_RANKS] = {};
 
     Tensors() = default;
     Tensors(const Tensors&) = delete;
@@ -283,11 +289,12 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
         l.take(a[0], s.ranks, what);
         l.dims(2, what, "[tokens, experts]");
         const at::Device dev = l.t[0]->device();
-        int64_t tokens[RC_MAX_RANKS];
+        int64_t tokens[RC_MAX_RANKS] = {};
         for (int r = 0; r < s.ranks; ++r) tokens[r] = l.t[r]->size(0);
         const int64_t E = l.t[0]->size(1), K = to_int32(a[1], what);
         rc_route_desc d{};
         d.struct_size = sizeof d;
+        d.session = s.id;
         d.dtype = row_type(*l.t[0], what);
         l.expect(l.t[0]->scalar_type(), dev, tokens, E, what);
         if (E > RC_MAX_EXPERTS || K < 1 || K > RC_MAX_TOP_K)
@@ -335,11 +342,12 @@ PyObject* route_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
         l.take(a[0], s.ranks, what);
         l.dims(2, what, "[tokens, experts]");
         const at::Device dev = l.t[0]->device();
-        int64_t tokens[RC_MAX_RANKS];
+        int64_t tokens[RC_MAX_RANKS] = {};
         for (int r = 0; r < s.ranks; ++r) tokens[r] = l.t[r]->size(0);
         const int64_t E = l.t[0]->size(1);
         rc_route_desc d{};
         d.struct_size = sizeof d;
+        d.session = s.id;
         d.dtype = row_type(*l.t[0], what);
         const ScalarType type = l.t[0]->scalar_type();
         l.expect(type, dev, tokens, E, what);
@@ -375,7 +383,7 @@ PyObject* route_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // What a plan's users share: its experts, slots and capacities.
 struct Plan {
     Tensors experts, slots;
-    int64_t tokens[RC_MAX_RANKS], capacity[RC_MAX_RANKS], K = 0;
+    int64_t tokens[RC_MAX_RANKS] = {}, capacity[RC_MAX_RANKS] = {}, K = 0;
     rc_exchange_desc d{};
 
     void capacities(PyObject* seq, int ranks, const char* what) {
@@ -394,8 +402,9 @@ struct Plan {
         experts.expect(ScalarType::Int, experts.t[0]->device(), tokens, K, what);
         if (K > RC_MAX_TOP_K) raise(RC_ERR_INVALID_ARGUMENT, what, "top_k %lld", (long long)K);
     }
-    void describe(int32_t num_experts, int dtype, int64_t width) {
+    void describe(const Session& s, int32_t num_experts, int dtype, int64_t width) {
         d.struct_size = sizeof d;
+        d.session = s.id;
         d.dtype = dtype;
         d.num_experts = num_experts;
         d.top_k = (int32_t)K;
@@ -461,7 +470,7 @@ PyObject* dispatch_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
         offsets.expect(ScalarType::Int, dev, one, -1, what);
         for (int r = 0; r < R; ++r) one[r] = per;
         counts.expect(ScalarType::Int, dev, one, -1, what);
-        p.describe(E, RC_F32, 1);
+        p.describe(s, E, RC_F32, 1);
         int64_t size = 0;
         call([&] { return rc_dispatch_plan_workspace(&p.d, &size); });
         Tensor work;
@@ -494,7 +503,7 @@ PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Plan p;
         p.follow(a + 1, s.ranks, dev, what);
         x.expect(type, dev, p.tokens, D, what);
-        p.describe(to_int32(a[4], what), row_type(*x.t[0], what), D);
+        p.describe(s, to_int32(a[4], what), row_type(*x.t[0], what), D);
         if (a[5] != Py_None) {
             o.take(a[5], s.ranks, "dispatch output");
         } else {
@@ -522,7 +531,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Plan p;
         p.follow(a + 1, s.ranks, dev, what);
         x.expect(type, dev, p.capacity, D, what);
-        p.describe(to_int32(a[4], what), row_type(*x.t[0], what), D);
+        p.describe(s, to_int32(a[4], what), row_type(*x.t[0], what), D);
         if (a[5] != Py_None) {
             w.take(a[5], s.ranks, "combine weights");
             w.expect(ScalarType::Float, dev, p.tokens, p.K, "combine weights");
@@ -556,7 +565,7 @@ PyObject* combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
         dy.expect(type, dev, p.tokens, D, what);
         x.take(a[1], s.ranks, "combine_grad rows");
         x.expect(type, dev, p.capacity, D, "combine_grad rows");
-        p.describe(to_int32(a[5], what), row_type(*dy.t[0], what), D);
+        p.describe(s, to_int32(a[5], what), row_type(*dy.t[0], what), D);
         w.take(a[6], s.ranks, "combine_grad weights");
         w.expect(ScalarType::Float, dev, p.tokens, p.K, "combine_grad weights");
         PyObject *xo, *wo;
@@ -586,11 +595,12 @@ void shards(int64_t vocab, int ranks, int64_t* rows) {
 
 struct Ids {
     Tensors ids;
-    int64_t tokens[RC_MAX_RANKS];
+    int64_t tokens[RC_MAX_RANKS] = {};
     rc_embedding_desc d{};
     at::Device dev{at::kCPU};
 
-    Ids(PyObject* seq, int ranks, const char* what) {
+    Ids(PyObject* seq, const Session& s, const char* what) {
+        const int ranks = s.ranks;
         ids.take(seq, ranks, what);
         ids.dims(1, what, "[tokens]");
         dev = ids.t[0]->device();
@@ -602,6 +612,7 @@ struct Ids {
         for (int r = 0; r < ranks; ++r) tokens[r] = ids.t[r]->size(0);
         ids.expect(type, dev, tokens, -1, what);
         d.struct_size = sizeof d;
+        d.session = s.id;
         d.id_dtype = type == ScalarType::Long ? (int)RC_I64 : (int)RC_I32;
         d.tokens = tokens;
         d.ids = ids.p;
@@ -614,7 +625,7 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t n) {
         arity(n, {"embedding", 4});
         const char* what = "embedding";
         const Session s;
-        Ids i(a[0], s.ranks, what);
+        Ids i(a[0], s, what);
         Tensors t, o;
         t.take(a[1], s.ranks, "embedding tables");
         t.dims(2, "embedding tables", "[rows, width]");
@@ -645,7 +656,7 @@ PyObject* embedding_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
         arity(n, {"embedding_grad", 7});
         const char* what = "embedding_grad";
         const Session s;
-        Ids i(a[0], s.ranks, what);
+        Ids i(a[0], s, what);
         Tensors g, o;
         g.take(a[1], s.ranks, what);
         g.dims(2, what, "[tokens, width]");

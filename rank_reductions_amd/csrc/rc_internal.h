@@ -128,6 +128,8 @@ int64_t element_size(int dtype);
 // session lock once the session is known to be open for whole calls, and its
 // Error becomes the entry point's status and message.
 int whole_call(const std::function<Error(int nranks, bool validate_only)>& body);
+// The number of the open session (rc_session_id); under the session lock, as in `body`.
+int64_t session_id();
 
 // ---------------------------------------------------------------- plan.cpp
 // Unroll (16-byte vectors per lane per round) of a fold of `nin` inputs: about

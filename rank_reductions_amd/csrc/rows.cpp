@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 #include <cstdio>
 #include <string>
 #include <vector>
@@ -96,11 +97,21 @@ Error need(const char* what, P* p, const char* name) {
         if (rc_e_.code) return rc_e_; \
     } while (0)
 
+// A descriptor's size, and the session that its arrays were made for.
+template <class D>
+Error check_desc(const char* what, const D* d, const char* type) {
+    RC_TRY(need(what, d, "desc"));
+    if (d->struct_size == offsetof(D, session)) return {};
+    if (d->struct_size != sizeof(D)) return bad(what, std::string("desc->struct_size must be sizeof(") + type + ")");
+    if (d->session && d->session != session_id())
+        return bad(what, "the session that the call was made for has been closed, and another is open");
+    return {};
+}
+
 // ---------------------------------------------------------------- routing
 
 Error check_route(const char* what, int R, const rc_route_desc* d, const int64_t* tokens, RouteArgs* a) {
-    RC_TRY(need(what, d, "desc"));
-    if (d->struct_size != sizeof(rc_route_desc)) return bad(what, "desc->struct_size must be sizeof(rc_route_desc)");
+    RC_TRY(check_desc(what, d, "rc_route_desc"));
     if (!row_element_size(d->dtype)) return bad(what, fmt("unknown dtype %lld", d->dtype));
     if (d->num_experts < 1 || d->num_experts > RC_MAX_EXPERTS) return bad(what, fmt("num_experts %lld outside [1, 1024]", d->num_experts));
     if (d->top_k < 1 || d->top_k > RC_MAX_TOP_K) return bad(what, fmt("top_k %lld outside [1, 16]", d->top_k));
@@ -145,8 +156,7 @@ struct Exchange {
 };
 
 Error check_exchange(const char* what, int R, const rc_exchange_desc* d, bool plan, Exchange* x) {
-    RC_TRY(need(what, d, "desc"));
-    if (d->struct_size != sizeof(rc_exchange_desc)) return bad(what, "desc->struct_size must be sizeof(rc_exchange_desc)");
+    RC_TRY(check_desc(what, d, "rc_exchange_desc"));
     x->es = row_element_size(d->dtype);
     if (!plan) {
         if (!x->es) return bad(what, fmt("unknown dtype %lld", d->dtype));
@@ -193,8 +203,7 @@ struct Embedding {
 };
 
 Error check_embedding(const char* what, int R, const rc_embedding_desc* d, bool grad, bool with_ids, Embedding* x) {
-    RC_TRY(need(what, d, "desc"));
-    if (d->struct_size != sizeof(rc_embedding_desc)) return bad(what, "desc->struct_size must be sizeof(rc_embedding_desc)");
+    RC_TRY(check_desc(what, d, "rc_embedding_desc"));
     x->es = row_element_size(d->dtype);
     if (!x->es) return bad(what, fmt("unknown dtype %lld", d->dtype));
     if (d->id_dtype != RC_I32 && d->id_dtype != RC_I64) return bad(what, fmt("unknown id_dtype %lld", d->id_dtype));

@@ -354,6 +354,8 @@ Error whole_call_session() {
 
 }  // namespace
 
+int64_t session_id() { return (int64_t)g_generation + 1; }
+
 int whole_call(const std::function<Error(int, bool)>& body) {
     std::lock_guard<std::mutex> lock(g_mu);
     Error e = whole_call_session();
@@ -874,6 +876,14 @@ int rc_session_info(int* num_ranks, int* device) {
         return report(Error{RC_ERR_NOT_REGISTERED, "no session: call rc_register first"});
     if (num_ranks) *num_ranks = g_s.nranks;
     if (device) *device = g_s.cfg.validate_only ? g_s.cfg.device : g_s.dev.device;
+    return ok();
+}
+
+int rc_session_id(int64_t* id) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (g_s.mode == Mode::None)
+        return report(Error{RC_ERR_NOT_REGISTERED, "no session: call rc_register first"});
+    if (id) *id = session_id();
     return ok();
 }
 

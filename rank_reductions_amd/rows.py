@@ -50,6 +50,7 @@ class RcRouteDesc(ctypes.Structure):
         ("renormalize", ctypes.c_int32),
         ("scale", ctypes.c_float),
         ("bias", ctypes.c_void_p),
+        ("session", ctypes.c_int64),
     ]
 
 
@@ -64,6 +65,7 @@ class RcExchangeDesc(ctypes.Structure):
         ("capacity", ctypes.c_void_p),
         ("experts", ctypes.c_void_p),
         ("slots", ctypes.c_void_p),
+        ("session", ctypes.c_int64),
     ]
 
 
@@ -79,6 +81,7 @@ class RcEmbeddingDesc(ctypes.Structure):
         ("width", ctypes.c_int64),
         ("tokens", ctypes.c_void_p),
         ("ids", ctypes.c_void_p),
+        ("session", ctypes.c_int64),
     ]
 
 
@@ -97,6 +100,7 @@ def declare(lib):
         "rc_embedding_grad_workspace": [p, p],
         "rc_embedding_grad": [p, p, p, p, i64, p],
         "rc_session_info": [p, p],
+        "rc_session_id": [p],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes = args

@@ -241,3 +241,41 @@ def test_gradient_of_masked_rows_is_zero(dtype, renormalize, E):
     for t in (0, 1, 2, 5):
         assert not d[t].any(), f"row {t}: {d[t]}"
     assert d[3].any() and d[4].any()
+
+
+# ---------------------------------------------------------------- what changes while a call reads its arguments
+
+class Later:
+    """A number whose reading does something first, as another thread might."""
+
+    def __init__(self, value, act):
+        self.value, self.act = value, act
+
+    def __float__(self):
+        self.act()
+        return float(self.value)
+
+    def __index__(self):
+        self.act()
+        return int(self.value)
+
+
+@pytest.mark.parametrize("ranks", [1, 2, 4])
+def test_a_session_opened_during_the_call_is_not_taken_for_the_first(ranks):
+    def reopen():
+        rr.reset()
+        rr.register(ranks)
+
+    ids = [torch.zeros(3, dtype=torch.int64, device=DEV) for _ in range(2)]
+    tables = [torch.ones(5, 8, device=DEV) for _ in range(2)]
+    dy = [torch.ones(3, 8, device=DEV) for _ in range(2)]
+    experts = [torch.zeros(3, 1, dtype=torch.int32, device=DEV) for _ in range(2)]
+    for call in (lambda: rr.embedding(ids, tables, scale=Later(1, reopen)),
+                 lambda: rr.embedding_grad(ids, dy, 10, scale=Later(1, reopen)),
+                 lambda: rr.route(dy, 2, scale=Later(1, reopen)),
+                 lambda: rr.route_grad(dy, experts, [torch.ones(3, 1, device=DEV)] * 2, scale=Later(1, reopen)),
+                 lambda: rr.dispatch_plan(experts, Later(4, reopen))):
+        with session(2):
+            with pytest.raises(rr.CollectiveError, match="closed") as e:
+                call()
+            assert e.value.code == rr.RC_ERR_INVALID_ARGUMENT
