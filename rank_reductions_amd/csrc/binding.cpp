@@ -91,10 +91,9 @@ Tensor part_of(const Tensor& all, int64_t at, at::IntArrayRef sizes) {
 
 // One tensor per rank.
 struct Tensors {
-    PyObject* list = nullptr;  // what Python gave or gets (borrowed, or owned when made here)
-    bool owned = false;
+    PyObject* list = nullptr;  // what Python gave or gets
     int n = 0;
-    Tensor made[RC_MAX_RANKS];
+    Tensor held[RC_MAX_RANKS];  // given ones too: the list may change while the call is made
     const Tensor* t[RC_MAX_RANKS] = {};
     void* p[RC_MAX_RANKS] = {};
 
@@ -102,11 +101,12 @@ struct Tensors {
     Tensors(const Tensors&) = delete;
     Tensors& operator=(const Tensors&) = delete;
     ~Tensors() {
-        if (owned) Py_XDECREF(list);
+        Py_XDECREF(list);
     }
 
     // A list or tuple of `ranks` tensors.
     void take(PyObject* seq, int ranks, const char* what) {
+        Py_INCREF(seq);
         list = seq;
         if (!PyList_Check(seq) && !PyTuple_Check(seq)) raise(RC_ERR_INVALID_ARGUMENT, what, "not a list of tensors");
         const Py_ssize_t size = PySequence_Fast_GET_SIZE(seq);
@@ -115,14 +115,20 @@ struct Tensors {
         for (int r = 0; r < n; ++r) {
             PyObject* o = PySequence_Fast_GET_ITEM(seq, r);
             if (!THPVariable_Check(o)) raise(RC_ERR_INVALID_ARGUMENT, what, "no tensor for rank %d", r);
-            t[r] = &THPVariable_Unpack(o);
+            held[r] = THPVariable_Unpack(o);
+            t[r] = &held[r];
         }
+    }
+    void take_one(PyObject* o) {
+        n = 1;
+        held[0] = THPVariable_Unpack(o);
+        t[0] = &held[0];
     }
 
     // Tensors made here, given to Python with give().
     void make(int ranks) {
         n = ranks;
-        for (int r = 0; r < n; ++r) t[r] = &made[r];
+        for (int r = 0; r < n; ++r) t[r] = &held[r];
     }
     // The same, [rows[r], cols] each; small ones as parts of one allocation (and
     // one fill), on boundaries of 256 bytes: eight ranks' calls on a token each
@@ -144,19 +150,18 @@ struct Tensors {
             return zeros ? at::zeros(sizes, options(type, device)) : at::empty(sizes, options(type, device));
         };
         if (size > kTogether) {
-            for (int r = 0; r < n; ++r) made[r] = fresh({rows[r], cols});
+            for (int r = 0; r < n; ++r) held[r] = fresh({rows[r], cols});
         } else {
             const Tensor all = fresh({size / es});
-            for (int r = 0; r < n; from += padded(r++)) made[r] = part_of(all, from, {rows[r], cols});
+            for (int r = 0; r < n; from += padded(r++)) held[r] = part_of(all, from, {rows[r], cols});
         }
     }
     PyObject* give() {
         if (!list) {
             list = PyList_New(n);
             if (!list) throw Raised{};
-            owned = true;
             for (int r = 0; r < n; ++r) {
-                PyObject* o = THPVariable_Wrap(made[r]);
+                PyObject* o = THPVariable_Wrap(held[r]);
                 if (!o) throw Raised{};
                 PyList_SET_ITEM(list, r, o);
             }
@@ -305,8 +310,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Tensors b;
         if (a[3] != Py_None) {
             if (!THPVariable_Check(a[3])) raise(RC_ERR_INVALID_ARGUMENT, what, "bias is not a tensor");
-            b.n = 1;
-            b.t[0] = &THPVariable_Unpack(a[3]);
+            b.take_one(a[3]);
             b.expect(ScalarType::Float, dev, &E, -1, "route bias");
             d.bias = static_cast<const float*>(b.p[0]);
         }
@@ -460,11 +464,11 @@ PyObject* dispatch_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
         counts.make(R);
         int64_t at_ = 0, one[RC_MAX_RANKS];
         for (int r = 0; r < R; ++r) {
-            p.slots.made[r] = part_of(all, at_, {p.tokens[r], p.K});
+            p.slots.held[r] = part_of(all, at_, {p.tokens[r], p.K});
             at_ += p.tokens[r] * p.K;
         }
-        for (int r = 0; r < R; ++r, at_ += per + 1) offsets.made[r] = part_of(all, at_, {per + 1});
-        for (int r = 0; r < R; ++r, at_ += per) counts.made[r] = part_of(all, at_, {per});
+        for (int r = 0; r < R; ++r, at_ += per + 1) offsets.held[r] = part_of(all, at_, {per + 1});
+        for (int r = 0; r < R; ++r, at_ += per) counts.held[r] = part_of(all, at_, {per});
         p.slots.expect(ScalarType::Int, dev, p.tokens, p.K, what);
         for (int r = 0; r < R; ++r) one[r] = per + 1;
         offsets.expect(ScalarType::Int, dev, one, -1, what);

@@ -1,7 +1,8 @@
-"""What may change between a row exchange's arguments and its launch: the
-session, on the CPU with validate_only sessions."""
+"""What may change between a row exchange's arguments and its launch - the
+session, the lists - on the CPU with validate_only sessions."""
 
 import ctypes
+import weakref
 
 import pytest
 import torch
@@ -75,3 +76,50 @@ def test_descriptors_without_a_session(lib, monkeypatch):
     register(lib, R)
     assert set(statuses(lib, 12345, monkeypatch, older=True).values()) == {OK}
     assert set(statuses(lib, 12345, monkeypatch).values()) == {INVAL}
+
+
+class Drops:
+    """A number; while it is read, the lists are emptied, as by another thread."""
+
+    def __init__(self, value, *lists):
+        self.value, self.lists, self.alive = value, lists, []
+
+    def act(self):
+        refs = [weakref.ref(t) for x in self.lists for t in x]
+        for x in self.lists:
+            x.clear()
+        self.alive += [r() is not None for r in refs]
+
+    def __float__(self):
+        self.act()
+        return float(self.value)
+
+    def __index__(self):
+        self.act()
+        return int(self.value)
+
+
+def test_tensors_live_until_the_call_returns(lib):
+    register(lib, 2)
+    f = lambda *n: [torch.zeros(*n), torch.zeros(*n)]
+    i = lambda *n: [torch.zeros(*n, dtype=torch.int32), torch.zeros(*n, dtype=torch.int32)]
+    ids, tables, dy, logits, experts, dw, out = i(3), f(5, 8), f(3, 8), f(3, 8), i(3, 1), f(3, 1), f(3, 8)
+    calls = [
+        (lambda n: rr.embedding(ids, tables, scale=n), ids, tables),
+        (lambda n: rr.embedding_grad(ids, dy, 10, scale=n), ids, dy),
+        (lambda n: rr.route(logits, 1, scale=n), logits),
+        (lambda n: rr.route_grad(logits, experts, dw, scale=n), logits, experts, dw),
+        (lambda n: rr.dispatch_plan(experts, n), experts),
+    ]
+    for call, *lists in calls:
+        kept = [list(x) for x in lists]
+        copies = [[t.clone() for t in x] for x in lists]
+        for x, c in zip(lists, copies):
+            x[:] = c
+        del copies, c
+        drops = Drops(2, *lists)
+        with pytest.raises(ValueError, match="CUDA"):
+            call(drops)
+        assert drops.alive and all(drops.alive)
+        for x, k in zip(lists, kept):
+            x[:] = k
