@@ -133,17 +133,25 @@ def _native():
     return _native_module
 
 
-def _on(stream):
-    """The context that makes `stream` current."""
+def _on(stream, what):
+    """The context that makes `stream`, one of the session's GPU, current."""
     torch = _rr._torch()
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    device = ctypes.c_int()
+    _rr.check(_rr.library().rc_session_info(None, ctypes.byref(device)))
+    index = device.value if device.value >= 0 else None  # None: the current one
+    if not hasattr(stream, "cuda_stream"):
+        return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=index))
+    if index is not None and stream.device.index != index:
+        raise _rr.CollectiveError(_rr.RC_ERR_INVALID_ARGUMENT,
+                                  f"{what}: stream of {stream.device}, the session is on GPU {index}")
+    return torch.cuda.stream(stream)
 
 
 def _call(name, stream, *args):
     fn = getattr(_native_module or _native(), name)
     if stream is None:
         return fn(*args)
-    with _on(stream):
+    with _on(stream, name):
         return fn(*args)
 
 

@@ -123,3 +123,47 @@ def test_tensors_live_until_the_call_returns(lib):
         assert drops.alive and all(drops.alive)
         for x, k in zip(lists, kept):
             x[:] = k
+
+
+def test_streams_are_the_sessions_gpu_s(lib, monkeypatch):
+    """A handle is taken for one of the session's GPU, whichever is current, and a
+    stream of another GPU refused: neither becomes the current stream unseen."""
+    rr.register(2, device=1, validate_only=True)
+    x = [torch.zeros(3, 8), torch.zeros(3, 8)]
+    made = []
+
+    class Entered(Exception):
+        pass
+
+    def external(handle, device=None):
+        made.append((handle, device))
+        return "external"
+
+    def stream(s):
+        made.append(s)
+        raise Entered
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+
+    class Stream:
+        cuda_stream = 77
+
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+    with pytest.raises(Entered):
+        rr.route(x, 2, stream=77)
+    assert made == [(77, 1), "external"]
+    made.clear()
+    with pytest.raises(rr.CollectiveError) as e:
+        rr.route(x, 2, stream=Stream(0))
+    assert e.value.code == INVAL and not made
+    right = Stream(1)
+    with pytest.raises(Entered):
+        rr.route(x, 2, stream=right)
+    assert made == [right]
+    rr.reset()
+    with pytest.raises(rr.CollectiveError) as e:
+        rr.route(x, 2, stream=right)
+    assert e.value.code == NR
