@@ -442,7 +442,7 @@ PyObject* dispatch_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
         p.choices(a[0], R, what);
         const at::Device dev = p.experts.t[0]->device();
         const int32_t E = to_int32(a[1], what);
-        if (E < 1 || E % R) raise(RC_ERR_INVALID_ARGUMENT, what, "%d experts over %d ranks", E, R);
+        if (E < 1 || E > RC_MAX_EXPERTS || E % R) raise(RC_ERR_INVALID_ARGUMENT, what, "%d experts over %d ranks", E, R);
         const int64_t per = E / R;
         int64_t entries = 0;
         for (int r = 0; r < R; ++r) entries += p.tokens[r] * p.K;

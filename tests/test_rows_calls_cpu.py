@@ -12,6 +12,9 @@ from rank_reductions_amd import rows
 from test_rows_cpu import INVAL, NR, OK, R, embedding_calls, exchange_calls, route_call
 
 
+MAX_EXPERTS = 1024  # RC_MAX_EXPERTS
+
+
 @pytest.fixture
 def lib():
     lib = rr.library()
@@ -76,6 +79,17 @@ def test_descriptors_without_a_session(lib, monkeypatch):
     register(lib, R)
     assert set(statuses(lib, 12345, monkeypatch, older=True).values()) == {OK}
     assert set(statuses(lib, 12345, monkeypatch).values()) == {INVAL}
+
+
+def test_too_many_experts_are_refused_before_their_counts_are_allocated(lib):
+    register(lib, 2)
+    experts = [torch.zeros(3, 2, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32)]
+    for n in (MAX_EXPERTS + 2, 2**30, 2**31 - 2):
+        with pytest.raises(rr.CollectiveError) as e:
+            rr.dispatch_plan(experts, n)
+        assert e.value.code == INVAL
+    with pytest.raises(ValueError, match="CUDA"):  # as far as host tensors go
+        rr.dispatch_plan(experts, MAX_EXPERTS)
 
 
 class Drops:
