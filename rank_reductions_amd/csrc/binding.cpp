@@ -13,6 +13,7 @@
 #include <ATen/core/Tensor.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -270,16 +271,17 @@ void arity(Py_ssize_t got, Arity want) {
     throw Raised{};
 }
 
+// torch's exceptions become the Python ones that torch's own functions raise
+// (OutOfMemoryError among them).
 template <class F>
 PyObject* guarded(F f) {
+    HANDLE_TH_ERRORS
     try {
         return f();
     } catch (const Raised&) {
         return nullptr;
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
     }
+    END_HANDLE_TH_ERRORS
 }
 
 // ---------------------------------------------------------------- routing

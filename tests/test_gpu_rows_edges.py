@@ -279,3 +279,19 @@ def test_a_session_opened_during_the_call_is_not_taken_for_the_first(ranks):
             with pytest.raises(rr.CollectiveError, match="closed") as e:
                 call()
             assert e.value.code == rr.RC_ERR_INVALID_ARGUMENT
+
+
+def test_an_allocation_that_fails_raises_torchs_error():
+    """As torch's own functions do, so that a program can make its batch smaller;
+    with this process held to a thousandth of the memory."""
+    with session(1):
+        ids, dy = [torch.zeros(4, dtype=torch.int32, device=DEV)], [torch.ones(4, 64, device=DEV)]
+        want = rr.embedding_grad(ids, dy, 100)[0]
+        torch.cuda.empty_cache()
+        torch.cuda.set_per_process_memory_fraction(0.001)
+        try:
+            with pytest.raises(torch.OutOfMemoryError):
+                rr.embedding_grad(ids, dy, 2**24)
+        finally:
+            torch.cuda.set_per_process_memory_fraction(1.0)
+        assert torch.equal(rr.embedding_grad(ids, dy, 100)[0], want)
