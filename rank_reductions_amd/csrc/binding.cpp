@@ -701,6 +701,11 @@ PyObject* embedding_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// device() -> the session's GPU, -1 for none
+PyObject* device(PyObject*, PyObject* const*, Py_ssize_t) {
+    return guarded([&] { return PyLong_FromLong(Session().device); });
+}
+
 PyObject* set_error(PyObject*, PyObject* type) {
     Py_INCREF(type);
     Py_XDECREF(g_error);
@@ -711,7 +716,7 @@ PyObject* set_error(PyObject*, PyObject* type) {
 #define RC_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     RC_METHOD(route), RC_METHOD(route_grad), RC_METHOD(dispatch_plan), RC_METHOD(dispatch), RC_METHOD(combine),
-    RC_METHOD(combine_grad), RC_METHOD(embedding), RC_METHOD(embedding_grad),
+    RC_METHOD(combine_grad), RC_METHOD(embedding), RC_METHOD(embedding_grad), RC_METHOD(device),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

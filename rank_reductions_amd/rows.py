@@ -136,9 +136,8 @@ def _native():
 def _on(stream, what):
     """The context that makes `stream`, one of the session's GPU, current."""
     torch = _rr._torch()
-    device = ctypes.c_int()
-    _rr.check(_rr.library().rc_session_info(None, ctypes.byref(device)))
-    index = device.value if device.value >= 0 else None  # None: the current one
+    device = (_native_module or _native()).device()
+    index = device if device >= 0 else None  # None: the current one
     if not hasattr(stream, "cuda_stream"):
         return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=index))
     if index is not None and stream.device.index != index:
