@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <cstdarg>
+#include <exception>
 #include <string>
 #include <vector>
 
@@ -70,11 +71,21 @@ struct Session {
     int64_t id = 0;
     int ranks = 0, device = -1;
     Session() {
+        thread_local Session seen{0, 0, -1};  // a number is of one session only
         call([&] {
-            const int e = rc_session_id(&id);
-            return e ? e : rc_session_info(&ranks, &device);
+            int64_t open = 0;
+            int e = rc_session_id(&open);
+            if (!e && open != seen.id) {
+                e = rc_session_info(&seen.ranks, &seen.device);
+                seen.id = e ? 0 : open;
+            }
+            return e;
         });
+        *this = seen;
     }
+
+  private:
+    Session(int64_t i, int r, int d) : id(i), ranks(r), device(d) {}
 };
 
 const char* type_name(ScalarType t) { return at::toString(t); }
@@ -94,7 +105,8 @@ Tensor part_of(const Tensor& all, int64_t at, at::IntArrayRef sizes) {
 struct Tensors {
     PyObject* list = nullptr;  // what Python gave or gets
     int n = 0;
-    Tensor held[RC_MAX_RANKS];  // given ones too: the list may change while the call is made
+    Tensor made[RC_MAX_RANKS];
+    PyObject* given[RC_MAX_RANKS] = {};  // owned: the list may change while the call is made
     const Tensor* t[RC_MAX_RANKS] = {};
     void* p[RC_MAX_RANKS] = {};
 
@@ -102,6 +114,7 @@ struct Tensors {
     Tensors(const Tensors&) = delete;
     Tensors& operator=(const Tensors&) = delete;
     ~Tensors() {
+        for (int r = 0; r < n && given[r]; ++r) Py_DECREF(given[r]);
         Py_XDECREF(list);
     }
 
@@ -116,20 +129,23 @@ struct Tensors {
         for (int r = 0; r < n; ++r) {
             PyObject* o = PySequence_Fast_GET_ITEM(seq, r);
             if (!THPVariable_Check(o)) raise(RC_ERR_INVALID_ARGUMENT, what, "no tensor for rank %d", r);
-            held[r] = THPVariable_Unpack(o);
-            t[r] = &held[r];
+            hold(r, o);
         }
+    }
+    void hold(int r, PyObject* o) {
+        Py_INCREF(o);
+        given[r] = o;
+        t[r] = &THPVariable_Unpack(o);
     }
     void take_one(PyObject* o) {
         n = 1;
-        held[0] = THPVariable_Unpack(o);
-        t[0] = &held[0];
+        hold(0, o);
     }
 
     // Tensors made here, given to Python with give().
     void make(int ranks) {
         n = ranks;
-        for (int r = 0; r < n; ++r) t[r] = &held[r];
+        for (int r = 0; r < n; ++r) t[r] = &made[r];
     }
     // The same, [rows[r], cols] each; small ones as parts of one allocation (and
     // one fill), on boundaries of 256 bytes: eight ranks' calls on a token each
@@ -151,10 +167,10 @@ struct Tensors {
             return zeros ? at::zeros(sizes, options(type, device)) : at::empty(sizes, options(type, device));
         };
         if (size > kTogether) {
-            for (int r = 0; r < n; ++r) held[r] = fresh({rows[r], cols});
+            for (int r = 0; r < n; ++r) made[r] = fresh({rows[r], cols});
         } else {
             const Tensor all = fresh({size / es});
-            for (int r = 0; r < n; from += padded(r++)) held[r] = part_of(all, from, {rows[r], cols});
+            for (int r = 0; r < n; from += padded(r++)) made[r] = part_of(all, from, {rows[r], cols});
         }
     }
     PyObject* give() {
@@ -162,7 +178,7 @@ struct Tensors {
             list = PyList_New(n);
             if (!list) throw Raised{};
             for (int r = 0; r < n; ++r) {
-                PyObject* o = THPVariable_Wrap(held[r]);
+                PyObject* o = THPVariable_Wrap(made[r]);
                 if (!o) throw Raised{};
                 PyList_SET_ITEM(list, r, o);
             }
@@ -275,13 +291,13 @@ void arity(Py_ssize_t got, Arity want) {
 // (OutOfMemoryError among them).
 template <class F>
 PyObject* guarded(F f) {
-    HANDLE_TH_ERRORS
     try {
         return f();
     } catch (const Raised&) {
-        return nullptr;
+    } catch (...) {
+        torch::translate_exception_to_python(std::current_exception());
     }
-    END_HANDLE_TH_ERRORS
+    return nullptr;
 }
 
 // ---------------------------------------------------------------- routing
@@ -466,11 +482,11 @@ PyObject* dispatch_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
         counts.make(R);
         int64_t at_ = 0, one[RC_MAX_RANKS];
         for (int r = 0; r < R; ++r) {
-            p.slots.held[r] = part_of(all, at_, {p.tokens[r], p.K});
+            p.slots.made[r] = part_of(all, at_, {p.tokens[r], p.K});
             at_ += p.tokens[r] * p.K;
         }
-        for (int r = 0; r < R; ++r, at_ += per + 1) offsets.held[r] = part_of(all, at_, {per + 1});
-        for (int r = 0; r < R; ++r, at_ += per) counts.held[r] = part_of(all, at_, {per});
+        for (int r = 0; r < R; ++r, at_ += per + 1) offsets.made[r] = part_of(all, at_, {per + 1});
+        for (int r = 0; r < R; ++r, at_ += per) counts.made[r] = part_of(all, at_, {per});
         p.slots.expect(ScalarType::Int, dev, p.tokens, p.K, what);
         for (int r = 0; r < R; ++r) one[r] = per + 1;
         offsets.expect(ScalarType::Int, dev, one, -1, what);
