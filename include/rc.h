@@ -402,14 +402,19 @@ typedef struct rc_route_desc {
  * weights = scale * s, or scale * s / (sum of the K s).  An expert whose
  * logit is -inf, or whose s + bias is -inf or NaN, is never chosen; a token
  * with fewer than K others has expert -1 and weight 0 in the rest, and a sum
- * of zero gives weights of zero. */
+ * of zero gives weights of zero.  (A sum of K softmax scores is never zero with
+ * renormalize: they are taken relative to the largest of the K there, also
+ * where each by itself would be too small for 64 bits.) */
 int rc_route(const rc_route_desc* desc, const int64_t* tokens, const void* const* logits, float* const* weights,
              int32_t* const* experts, void* stream);
 
 /* The gradient of rc_route's weights: d_logits[r] ([tokens[r], E]) from
  * d_weights[r] and the experts rc_route chose ([tokens[r], K]); an expert
- * outside [0, E) has no part.  The choice itself has no gradient; desc's
- * groups, group_by and bias are not used. */
+ * outside [0, E) has no part, parts of one named twice are added, and a row
+ * whose named experts (without renormalize: whose logits) are all -inf has a
+ * gradient of zero, as without renormalize has a row that holds +inf or NaN.
+ * The choice itself has no gradient; desc's groups, group_by and bias are not
+ * used. */
 int rc_route_grad(const rc_route_desc* desc, const int64_t* tokens, const void* const* logits,
                   const int32_t* const* experts, const float* const* d_weights, void* const* d_logits, void* stream);
 

@@ -2,7 +2,8 @@
 // by sorted ids.
 //
 // Lookup: one wave per piece of a token's row; bound by memory: 65536 tokens of
-// 4096 bf16 take 148 us (0.8 GB at 5.4 TB/s).
+// 4096 bf16 take 149 us (0.54 GB written and 0.34 read, 5.9 TB/s; the 13600 rows
+// that they name are 0.11).
 //
 // Gradient: dW[v] = scale * sum of dy over the tokens whose id is v.  The ids
 // of all ranks are sorted (stably, with their positions), so that the rows of
@@ -16,7 +17,7 @@
 // thus depends on its own tokens only.  Other workgroups of the same launch
 // clear the table's rows that no id names.  Bound by memory: dy is read once
 // and the table written once, 65536 tokens of 4096 bf16 into 32000 rows of
-// float32 in 222 us (1.06 GB at 4.8 TB/s); the sort before it takes 33 and the
+// float32 in 221 us (1.06 GB at 4.8 TB/s); the sort before it takes 33 and the
 // joins 15.
 #include "rows_sort.h"
 

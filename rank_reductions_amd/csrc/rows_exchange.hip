@@ -3,9 +3,11 @@
 //
 // A row move gives one wave a piece of one token's row: a dispatched row is read
 // once and written to its K places, a combined one is the sum of K places, held
-// in float32 and rounded once.  All are bound by memory: 16384 tokens of 4096
-// bf16, eight places each, take 221 us to dispatch (1.2 GB at 5.5 TB/s), 259 to
-// combine (4.7 TB/s) and 432 for the combination's gradient (2.3 GB at 5.3).
+// in float32 and rounded once.  All wait for memory: 16384 tokens of 4096
+// bf16, eight places each, take 221 us to dispatch (1.2 GB at 5.5 TB/s), 258 to
+// combine (4.7 TB/s) and 433 for the combination's gradient (2.3 GB at 5.3),
+// where this library's copies, which limit what is under way, move 6.7.  With
+// 10 and 16 places the rates are alike (4.9 to 5.3 in a row of calls).
 // The plan is bound by latency: 131072 entries 15.8 us in two launches, 512 in
 // one, 5.3 us.
 #include "rows_sort.h"

@@ -21,11 +21,11 @@
 // matter - a handful - are computed again in 64 bits and decide, to their last
 // bit.  A double exp and division for every expert cost more than all the rest:
 // 131072 tokens of 256 experts in 8 groups with a bias, eight chosen, took 151 us
-// that way and take 66 (without bias or groups 40).
+// that way and take 67 (without bias or groups 35).
 //
 // Bound by instruction issue where there are many tokens: that case issues
-// 1750 vector instructions a wave of eight tokens, 48 us of the 66 if none ever
-// waited; its 142 MB are 27 us at the rate of a large copy.
+// 1760 vector instructions a wave of eight tokens, 48 us of the 67 if none ever
+// waited; its 143 MB are 21 us at the 6.7 TB/s of this library's copies.
 #include "rows_impl.h"
 
 namespace rc {
@@ -854,9 +854,10 @@ __global__ __launch_bounds__(kRouteThreads, KP == 16 ? 3 : 1) void route_kernel(
 // cleared (or filled with the softmax's part that every expert has), then each
 // lane writes its choices' parts; where a token names an expert twice, its parts
 // are added in order of k.  Bound by the writes and the 64-bit scores of the
-// chosen: 131072 tokens of 256 experts, eight chosen by sigmoid, 37.5 us (27 at
-// the rate of a copy); two exponentials and divisions a score instead of one,
-// and all adds in order of k, took 42.
+// chosen: 131072 tokens of 256 experts, eight chosen by sigmoid, 37 us (22 at
+// the 6.7 TB/s of this library's copies); two exponentials and divisions a score
+// instead of one, and all adds in order of k, took 42.  The softmax over all
+// experts reads the rows three times and takes two exponentials an expert: 100.
 template <class T, int L, int KP>
 __global__ __launch_bounds__(kRouteThreads) void route_grad_kernel(RouteArgs a) {
     using E = typename T::E;
@@ -1084,7 +1085,9 @@ int run_route(RouteArgs a, hipStream_t s) {
 
 // Lanes per token: 8, so that a wave's instructions serve eight tokens; 64
 // where there are so few tokens that latency counts (64 tokens of 256 experts:
-// 7.3 us against 18.5), or too many experts.
+// 7.3 us against 18.5), or more experts than eight lanes hold (more than 256, or
+// 32 in a group).  Those cost four times as much on many tokens: 131072 of 512
+// experts, eight chosen, take 167 us, of 256 experts 35; nothing lies between.
 constexpr int64_t kFewTokens = 2048;
 template <class T>
 int pick_route(const RouteArgs& a, hipStream_t s) {

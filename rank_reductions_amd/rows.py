@@ -18,8 +18,14 @@ A vocabulary table sharded over the ranks - `embedding` looks rows up, and
 
 Argument marshalling only, most of it in the native module _rows: the kernels
 run in librankred.so.  Tensors are given as one per rank, on the session's
-GPU; new ones are allocated, and kernels enqueued, on `stream` (the current
-one if None).
+GPU; new ones are allocated, and kernels enqueued, on `stream` (a stream of that
+GPU; the current one if None).
+
+New tensors of one call are parts of one allocation while all ranks' together
+are at most 16 MiB, and a plan's slots, offsets and counts always are: like the
+parts that torch.split gives, each keeps the whole alive, is saved with the
+whole, and must not be grown in place (resize_), which would run into the next.
+Give `out` where that matters.
 """
 
 import ctypes
@@ -208,7 +214,9 @@ def dispatch_plan(experts, num_experts, capacity=None, stream=None):
     top_k] int32, -1 for none; rank d holds num_experts / R consecutive
     experts).  Each rank's rows are ordered by expert, then source rank, token
     and k.  capacity: rows per rank, one number or one per rank; entries past
-    it have no place (slot -1).  None makes room for all."""
+    it have no place (slot -1).  None makes room for all entries on every rank:
+    R times the rows that are there, which dispatch and combine_grad hold, and
+    clear, where they allocate.  Give a capacity, or `out`, for large batches."""
     slots, offsets, counts, capacity = _call("dispatch_plan", stream, experts, num_experts, capacity)
     return DispatchPlan(experts, slots, offsets, counts, num_experts, capacity)
 
