@@ -19,7 +19,9 @@ A vocabulary table sharded over the ranks - `embedding` looks rows up, and
 Argument marshalling only, most of it in the native module _rows: the kernels
 run in librankred.so.  Tensors are given as one per rank, on the session's
 GPU; new ones are allocated, and kernels enqueued, on `stream` (a stream of that
-GPU; the current one if None).
+GPU; the current one if None).  As with torch's functions, tensors that belong
+to another stream have to live until `stream` is done with them
+(Tensor.record_stream).
 
 New tensors of one call are parts of one allocation while all ranks' together
 are at most 16 MiB, and a plan's slots, offsets and counts always are: like the
