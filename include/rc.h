@@ -509,6 +509,66 @@ int rc_embedding_grad_workspace(const rc_embedding_desc* desc, int64_t* bytes);
 int rc_embedding_grad(const rc_embedding_desc* desc, const void* const* d_outs, void* const* d_tables,
                       void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Block operators: whole-call operators on each rank's own rows and
+ * parameters, which stand around the row exchanges and behind the gradient
+ * sync.  The rules of the row exchanges hold: arrays of R pointers, dense
+ * row-major buffers aligned to their elements, NULL for one of zero elements;
+ * the same checks in the same order; only kernels are enqueued and all scratch
+ * is the caller's workspace (16-byte aligned); the results depend on the inputs
+ * alone.  A buffer may be another's, at the same address, only where that is
+ * said.  RC_E4M3 is the 8-bit type of 4 exponent and 3 mantissa bits without
+ * infinities (largest value 448); a scale is what its values are multiplied
+ * with. */
+
+enum { RC_E4M3 = 5 };
+enum { RC_QUANTIZE_NONE = 0, RC_QUANTIZE_E4M3 = 1 };
+#define RC_MAX_NORM_WIDTH 32768
+
+/* Root-mean-square norm.  struct_size = sizeof(rc_norm_desc).
+ *   dtype         of the rows: RC_F32, RC_F16 or RC_BF16
+ *   weight_dtype  RC_F32 or dtype
+ *   quantize      RC_QUANTIZE_E4M3: the output in 8 bits with scales
+ *   group         elements that share a scale: 32, 64, 128 or 256 consecutive
+ *                 ones (a row's last group may hold fewer), or 0 for a row
+ *   width         elements of a row, in [1, RC_MAX_NORM_WIDTH]
+ *   eps           >= 0
+ *   tokens        [R] rows of each rank */
+typedef struct rc_norm_desc {
+    uint32_t struct_size;
+    int32_t dtype;
+    int32_t weight_dtype;
+    int32_t quantize;
+    int32_t group;
+    float eps;
+    int64_t width;
+    const int64_t* tokens;
+    int64_t session;
+} rc_norm_desc;
+
+/* ys[r][t] = s / sqrt(mean(s^2) + eps) * weights[r], where s = xs[r][t], or with
+ * residuals (NULL for none) sums[r][t] = xs[r][t] + residuals[r][t], rounded to
+ * dtype.  Statistics and the output's values are float32: rows whose squares
+ * add up past its range come out as zeros.  Quantised, ys are RC_E4M3 and
+ * scales[r] ([tokens[r], groups], float32) the largest absolute value of a
+ * group over 448, the values y * (448 / largest) to nearest even; a group
+ * whose largest is below 2^-117 has scale 0 and zeros, and a NaN has the code
+ * of NaN.  sums[r] may be residuals[r], and ys[r] (of dtype) may be xs[r]. */
+int rc_rms_norm(const rc_norm_desc* desc, const void* const* xs, const void* const* residuals,
+                const void* const* weights, void* const* ys, float* const* scales, void* const* sums, void* stream);
+
+/* The gradients of rc_rms_norm's rows and weights (quantize and group are not
+ * used): with s the rows that were normalised (sums[r], or xs[r] without a
+ * residual), n = s / sqrt(mean(s^2) + eps) and g = d_ys[r][t] * weights[r],
+ * d_xs[r][t] = (g - n * mean(g * n)) / sqrt(mean(s^2) + eps) + d_sums[r][t], the
+ * gradient of x and of the residual alike (d_sums: what comes back by the sum
+ * itself, NULL for none), and d_weights[r] = the sum over t of d_ys[r][t] * n, of
+ * weight_dtype.  d_xs[r] may be d_ys[r] or d_sums[r]. */
+int rc_rms_norm_grad_workspace(const rc_norm_desc* desc, int64_t* bytes);
+int rc_rms_norm_grad(const rc_norm_desc* desc, const void* const* d_ys, const void* const* sums,
+                     const void* const* weights, const void* const* d_sums, void* const* d_xs, void* const* d_weights,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
 /* The open session's rank count and GPU (-1 in a validate_only session opened
  * without one).  RC_ERR_NOT_REGISTERED if no session is open. */
 int rc_session_info(int* num_ranks, int* device);

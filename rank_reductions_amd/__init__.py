@@ -37,7 +37,7 @@ __all__ = [
     "all_gather_list", "all_to_all_single", "send_recv", "barrier", "rank_all_gather_list",
     "rank_all_to_all_single", "rank_send", "rank_recv", "rank_barrier", "rank_split", "rank_split_all",
     "Communicator", "route", "route_grad", "DispatchPlan", "dispatch_plan", "dispatch", "combine", "combine_grad",
-    "embedding", "embedding_grad",
+    "embedding", "embedding_grad", "rms_norm", "rms_norm_grad",
 ]
 
 RC_MAX_RANKS = 16
@@ -194,6 +194,7 @@ def _load():
     lib.rc_rank_finish.argtypes = [ctypes.c_int]
     lib.rc_rank_finish.restype = ctypes.c_int
     rows.declare(lib)
+    blocks.declare(lib)
     return lib
 
 
@@ -831,4 +832,9 @@ class Communicator:
 from . import rows  # noqa: E402 - it uses this module's names
 from .rows import (  # noqa: E402,F401
     DispatchPlan, combine, combine_grad, dispatch, dispatch_plan, embedding, embedding_grad, route, route_grad,
+)
+from . import blocks  # noqa: E402
+from .blocks import (  # noqa: E402,F401
+    rms_norm,
+    rms_norm_grad,
 )

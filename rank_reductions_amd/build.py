@@ -1,5 +1,5 @@
 """Builds librankred.so in-tree: host-only C++ with g++, HIP with hipcc for gfx950;
-and _rows.so, the Python module that marshals the row exchanges' tensors.
+and _rows.so, the Python module that marshals the row exchanges' and block operators' tensors.
 
     python -m rank_reductions_amd.build        # or: python rank_reductions_amd/build.py
 
@@ -22,7 +22,8 @@ BUILD = PKG / "_build"
 LIB = PKG / "librankred.so"
 BINDING = PKG / "_rows.so"
 
-HOST_SOURCES = ["session.cpp", "validate.cpp", "plan.cpp", "rows.cpp"]
+BINDING_SOURCES = ["binding.cpp", "binding_blocks.cpp"]
+HOST_SOURCES = ["session.cpp", "validate.cpp", "plan.cpp", "rows.cpp", "blocks.cpp"]
 # (source, object, defines): the fold and batch kernels are built once per
 # element type and cache hint, so that their instantiations compile in parallel
 RC_F32, RC_I32 = 0, 1
@@ -39,6 +40,9 @@ HIP_SOURCES = [
     ("rows_route.hip", "rows_route_bf16", {"RC_ROW_TYPE": "BF16"}),
     ("rows_exchange.hip", "rows_exchange", {}),
     ("rows_embedding.hip", "rows_embedding", {}),
+    ("block_norm.hip", "block_norm_f32", {"RC_ROW_TYPE": "F32"}),
+    ("block_norm.hip", "block_norm_f16", {"RC_ROW_TYPE": "F16"}),
+    ("block_norm.hip", "block_norm_bf16", {"RC_ROW_TYPE": "BF16"}),
     ("device.hip", "device", {}),
 ]
 
@@ -74,21 +78,22 @@ def _run(cmd, verbose):
 
 
 def _binding_jobs(inc, cxx):
-    """Compile and link commands of _rows.so, against the installed torch."""
+    """Compile commands and the link command of _rows.so, against the installed torch."""
     import sysconfig
 
     import torch
 
     home = Path(torch.__file__).resolve().parent
-    obj = BUILD / "binding.o"
     system = [home / "include", home / "include" / "torch" / "csrc" / "api" / "include",
               sysconfig.get_path("include"), Path(_hipcc()).resolve().parent.parent / "include"]
-    compile_ = [cxx, *HOST_FLAGS, "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
-                *(a for d in system for a in ("-isystem", d)), "-c", CSRC / "binding.cpp", "-o", obj]
+    objs = [BUILD / (Path(src).stem + ".o") for src in BINDING_SOURCES]
+    compile_ = [[cxx, *HOST_FLAGS, "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+                 *(a for d in system for a in ("-isystem", d)), "-c", CSRC / src, "-o", obj]
+                for src, obj in zip(BINDING_SOURCES, objs)]
     tmp = BINDING.with_suffix(".so.tmp")
     # librankred.so from the same folder; torch's libraries are loaded by then
-    link = [cxx, "-shared", "-fPIC", obj, f"-L{PKG}", f"-l:{LIB.name}", "-Wl,-rpath,$ORIGIN",
+    link = [cxx, "-shared", "-fPIC", *objs, f"-L{PKG}", f"-l:{LIB.name}", "-Wl,-rpath,$ORIGIN",
             f"-L{home / 'lib'}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-o", tmp]
     return compile_, link, tmp
 
@@ -111,7 +116,7 @@ def build(verbose=False, extra_hip_flags=()):
         jobs.append([hipcc, *HIP_FLAGS, *extra_hip_flags, *dflags, *inc, "-c", CSRC / src, "-o", obj])
         objs.append(obj)
     binding, link_binding, binding_tmp = _binding_jobs(inc, cxx)
-    jobs.append(binding)
+    jobs += binding
     # the largest objects first, so the pool ends together
     jobs.sort(key=lambda c: 0 if "kernels_fold.hip" in str(c) or "rows_route.hip" in str(c) else 1)
     with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 8, 16)) as ex:

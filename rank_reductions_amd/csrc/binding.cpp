@@ -1,4 +1,5 @@
-// Python module _rows: argument marshalling of the row exchanges.
+// Python module _rows: argument marshalling of the row exchanges (the block
+// operators' is in binding_blocks.cpp).
 //
 // The calls take R tensors per argument, and a decoding step makes several of
 // them on a few tokens, where checking and packing some fifty tensors in
@@ -7,7 +8,7 @@
 // module checks every tensor (type, shape, device, density), allocates what
 // the caller did not give, fills the C ABI's descriptors and calls
 // librankred.so on the current stream of the tensors' device.
-#include "binding.h"
+#include "binding_blocks.h"
 
 using namespace rows_binding;
 
@@ -454,4 +455,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rows", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__rows(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__rows(void) {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddFunctions(m, block_methods) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
