@@ -259,11 +259,11 @@ def _prepare_adamw(case, st, normal, uniform, dev):
 
         def state(of):
             scales = {k: maps(of[k], True) for k in ("m_scale", "v_scale") if k in of}
-            return rr.AdamWState(case["bits"], maps(of["m"]), maps(of["v"]), of["step"],
+            return rr.AdamWState(maps(of["params"]), case["bits"], maps(of["m"]), maps(of["v"]), of["step"],
                                  master=maps(of["master"]) if of.get("master") is not None else None, **scales)
 
-        st["maps"] = dict(params=maps(st["params"]), grads=maps(st["grads"]), state=state(st),
-                          new=(maps(st["new"]["params"]), state(st["new"])))
+        _session(R)
+        st["maps"] = dict(grads=maps(st["grads"]), state=state(st), new=state(st["new"]))
 
 
 def run(st):
@@ -291,7 +291,7 @@ def _run_own(case, st):
     m = st["maps"]
     norms = rr.grad_norm(m["grads"], out=st["norms"]) if case["clip"] else None
     # into other buffers than the state's own, so that a pass can be made again
-    rr.adamw_step(m["params"], m["grads"], m["state"], lr=1e-3, betas=BETAS, eps=ADAM_EPS, weight_decay=0.1,
+    rr.adamw_step(m["state"], m["grads"], lr=1e-3, betas=BETAS, eps=ADAM_EPS, weight_decay=0.1,
                   norms=norms, max_norm=st["max_norm"] if case["clip"] else None, seed=5, out=m["new"])
     return dict(st["new"], norms=norms) if case["clip"] else st["new"]
 
