@@ -569,6 +569,117 @@ int rc_rms_norm_grad(const rc_norm_desc* desc, const void* const* d_ys, const vo
                      const void* const* weights, const void* const* d_sums, void* const* d_xs, void* const* d_weights,
                      void* workspace, int64_t workspace_bytes, void* stream);
 
+/* One gradient: dense, `count` elements of RC_F32, RC_F16 or RC_BF16.  NULL with
+ * a count of 0 where a parameter has none. */
+typedef struct rc_grad {
+    const void* grad;
+    int64_t count;
+    int32_t dtype;
+    int32_t reserved;
+} rc_grad;
+
+/* norms[r] = the square root of the sum of the squares of all elements of rank
+ * r's num_grads[r] gradients, added up in 64 bits and rounded to float32 once;
+ * norms is [R] on the GPU.  With over_all every rank's is that of all ranks'
+ * gradients (parameters sharded over the ranks).  Sums run in a fixed order
+ * over the gradients as they are listed.  struct_size = sizeof(rc_grad_norm_desc). */
+typedef struct rc_grad_norm_desc {
+    uint32_t struct_size;
+    int32_t over_all;
+    int64_t session;
+} rc_grad_norm_desc;
+int rc_grad_norm_workspace(const rc_grad_norm_desc* desc, const int* num_grads, const rc_grad* const* grads,
+                           int64_t* bytes);
+int rc_grad_norm(const rc_grad_norm_desc* desc, const int* num_grads, const rc_grad* const* grads, float* norms,
+                 void* workspace, int64_t workspace_bytes, void* stream);
+
+/* One parameter of a rank with its AdamW state: `count` >= 0 elements each.
+ *   param    of dtype RC_F32, RC_F16 or RC_BF16
+ *   master   float32 copy of a 16-bit parameter; NULL for RC_F32
+ *   m, v     the means of the gradients and of their squares.  With states of
+ *            32 bits: float32.  With 8: RC_E4M3 codes of m and of the square
+ *            root of v, each times its scale
+ *   m_scale, v_scale  float32, one for each RC_ADAMW_BLOCK consecutive elements
+ *            (the last block may hold fewer); NULL with states of 32 bits */
+#define RC_ADAMW_BLOCK 256
+typedef struct rc_adamw_param {
+    int64_t count;
+    int32_t dtype;
+    int32_t reserved;
+    void* param;
+    float* master;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+} rc_adamw_param;
+
+/* struct_size = sizeof(rc_adamw_table_desc); state_bits: 32 or 8. */
+typedef struct rc_adamw_table_desc {
+    uint32_t struct_size;
+    int32_t state_bits;
+    int64_t session;
+} rc_adamw_table_desc;
+
+/* A table of all ranks' parameters, num_params[r] of rank r, which steps go by.
+ * With `table` NULL *bytes receives its size; else *bytes >= that size, and the
+ * table is written to host memory.  The caller copies it to the GPU (16-byte
+ * aligned) and keeps both as long as it makes steps by them; the step writes to
+ * the GPU's copy, so steps by one table run one after the other.  The buffers
+ * must not overlap. */
+int rc_adamw_table(const rc_adamw_table_desc* desc, const int* num_params, const rc_adamw_param* const* params, void* table,
+                   int64_t* bytes);
+
+/* struct_size = sizeof(rc_adamw_desc).
+ *   lr, beta1, beta2, eps, weight_decay  lr >= 0, betas in [0, 1), eps >= 0
+ *   lr_on_gpu   NULL, or one float32 on the GPU that is used in place of lr
+ *   norms       NULL, or [R] on the GPU: the norms of the ranks' gradients.  A
+ *               rank whose norm is not finite is left as it is
+ *   max_norm    0, or with norms: gradients of a rank whose norm (times
+ *               |grad_scale|) is larger are scaled down to it
+ *   grad_scale  factor of the gradients
+ *   seed        of the roundings of 8-bit states
+ *   steps, steps_out  [R] int32 on the GPU: the steps made before and after;
+ *               may be the same */
+typedef struct rc_adamw_desc {
+    uint32_t struct_size;
+    uint32_t seed;
+    double lr;
+    double beta1;
+    double beta2;
+    double eps;
+    double weight_decay;
+    double max_norm;
+    double grad_scale;
+    const float* lr_on_gpu;
+    const float* norms;
+    const int32_t* steps;
+    int32_t* steps_out;
+    int64_t session;
+} rc_adamw_desc;
+
+/* One AdamW step of every parameter that has a gradient (of its own dtype or
+ * RC_F32, grads[r][i] for params[r][i]): with t the rank's step from 1 on,
+ *   g = grad * grad_scale (scaled down by max_norm),
+ *   m = beta1 * m + (1 - beta1) * g,   v = beta2 * v + (1 - beta2) * g * g,
+ *   p = p * (1 - lr * weight_decay)
+ *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in float32, p being the master copy where there is one and the parameter then
+ * p to nearest even.  8-bit states: a block's scale is its largest absolute
+ * value over 448 (0, and all zeros, where that value is below 2^-117); m is
+ * rounded to nearest even.  sqrt(v) is rounded up or down by chance, in
+ * proportion to the distance (rounding to nearest would never let go of a value
+ * that changes by a thousandth each step), and to no less than the smallest
+ * code unless it is zero.  The chance of element i, u / 2^16 <= the part above the
+ * code below, is a function of seed, t and i alone, so ranks that hold the same
+ * parameters keep them alike.  A gradient that is not finite spoils its element,
+ * or block of an 8-bit state; give norms to leave such a step out.
+ * The states are read from `table` and written to `out_table`, another
+ * table of parameters of the same sizes and types that shares no buffer with it,
+ * or the same one: in place.  What has no gradient, or is left as it is, is copied. */
+int rc_adamw_step(const rc_adamw_desc* desc, const void* table, void* table_on_gpu, const void* out_table,
+                  const void* out_table_on_gpu, const rc_grad* const* grads, void* stream);
+
 /* The open session's rank count and GPU (-1 in a validate_only session opened
  * without one).  RC_ERR_NOT_REGISTERED if no session is open. */
 int rc_session_info(int* num_ranks, int* device);

@@ -32,3 +32,41 @@ def rms_norm_grad(dy, s, w, eps, d_sum=None):
     if d_sum is not None:
         dx = dx + np.asarray(d_sum, np.float64)
     return dx, (dy * s * factor).sum(axis=0)
+
+
+# ---------------------------------------------------------------- AdamW
+
+BLOCK = 256
+
+
+def mix(x):
+    x = np.asarray(x, np.uint64) & 0xFFFFFFFF
+    x = (x * 0x9E3779B9) & 0xFFFFFFFF
+    x = ((x ^ (x >> 15)) * 0x6A09E667) & 0xFFFFFFFF
+    x = ((x ^ (x >> 13)) * 0xBB67AE85) & 0xFFFFFFFF
+    return x ^ (x >> 16)
+
+
+def chances(n, step, seed):
+    """The chance of each of n elements at a step, in [0, 1)."""
+    key = mix(int(mix(step)) + seed)
+    pair = np.arange((n + 1) // 2, dtype=np.uint64)
+    h = mix(key + pair + 0xBB67AE85 * (pair >> 32))
+    return np.stack([h & 0xFFFF, h >> 16], axis=1).reshape(-1)[:n] / 65536.0
+
+
+def blocks(x):
+    """x in rows of BLOCK elements, zeros behind its end."""
+    x = np.asarray(x, np.float64).reshape(-1)
+    out = np.zeros(-(-x.size // BLOCK) * BLOCK)
+    out[:x.size] = x
+    return out.reshape(-1, BLOCK)
+
+
+def adamw(p, g, m, v, t, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2):
+    """(p, m, v) after step t, v being the mean of the squares."""
+    p, g, m, v = (np.asarray(a, np.float64) for a in (p, g, m, v))
+    m = betas[0] * m + (1 - betas[0]) * g
+    v = betas[1] * v + (1 - betas[1]) * g * g
+    update = m / (1 - betas[0] ** t) / (np.sqrt(v / (1 - betas[1] ** t)) + eps)
+    return p - lr * weight_decay * p - lr * update, m, v

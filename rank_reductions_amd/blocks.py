@@ -5,6 +5,11 @@ gradient sync (whole-call form; include/rc.h, "Block operators").
     codes, scales, sums = rr.rms_norm(xs, weights, residuals=hs, quantize="e4m3")
     d_xs, d_weights = rr.rms_norm_grad(d_ys, sums, weights, d_sums=d_hs)
 
+    state = rr.adamw_state(params, bits=8)                 # params[r]: {id: tensor}
+    rr.all_reduce_params(grads, "mean", out=grads)
+    norms = rr.grad_norm(grads)
+    rr.adamw_step(state, grads, lr=1e-3, norms=norms, max_norm=1.0)
+
 Argument marshalling only, as of the row exchanges (rows.py): tensors are given
 as one per rank, on the session's GPU; new ones are allocated, and kernels
 enqueued, on `stream` (the current one if None), and the parts of one call may
@@ -16,7 +21,8 @@ import ctypes
 import rank_reductions_amd as _rr
 from rank_reductions_amd.rows import _call, _choice
 
-__all__ = ["rms_norm", "rms_norm_grad"]
+__all__ = ["rms_norm", "rms_norm_grad", "grad_norm", "AdamWState", "adamw_state", "adamw_step"]
+
 
 RC_E4M3 = 5
 QUANTIZE = {None: 0, "e4m3": 1}
@@ -36,6 +42,64 @@ class RcNormDesc(ctypes.Structure):
     ]
 
 
+class RcGrad(ctypes.Structure):
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("count", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class RcGradNormDesc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("over_all", ctypes.c_int32),
+        ("session", ctypes.c_int64),
+    ]
+
+
+class RcAdamwTableDesc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("state_bits", ctypes.c_int32),
+        ("session", ctypes.c_int64),
+    ]
+
+
+class RcAdamwParam(ctypes.Structure):
+    _fields_ = [
+        ("count", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("param", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class RcAdamwDesc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("seed", ctypes.c_uint32),
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("max_norm", ctypes.c_double),
+        ("grad_scale", ctypes.c_double),
+        ("lr_on_gpu", ctypes.c_void_p),
+        ("norms", ctypes.c_void_p),
+        ("steps", ctypes.c_void_p),
+        ("steps_out", ctypes.c_void_p),
+        ("session", ctypes.c_int64),
+    ]
+
+
 def declare(lib):
     """Argument types of the library's block operators."""
     p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -43,6 +107,10 @@ def declare(lib):
         "rc_rms_norm": [p, p, p, p, p, p, p, p],
         "rc_rms_norm_grad_workspace": [p, p],
         "rc_rms_norm_grad": [p, p, p, p, p, p, p, p, i64, p],
+        "rc_grad_norm_workspace": [p, p, p, p],
+        "rc_grad_norm": [p, p, p, p, p, i64, p],
+        "rc_adamw_table": [p, p, p, p, p],
+        "rc_adamw_step": [p, p, p, p, p, p, p],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -83,3 +151,70 @@ def rms_norm_grad(d_ys, sums, weights, eps=1e-6, d_sums=None, out=None, stream=N
     themselves; d_xs is the gradient of the residuals too.  d_weights[r] is summed
     over rank r's rows, of the weights' type.  d_xs may be d_ys or d_sums."""
     return _call("rms_norm_grad", stream, d_ys, sums, weights, eps, d_sums, out)
+
+
+# ---------------------------------------------------------------- gradient norms and AdamW
+
+def grad_norm(grads, over="rank", out=None, stream=None):
+    """The 2-norm of each rank's gradients, grads[r] a map {parameter id: tensor}
+    (None for a parameter without one): a float32 tensor of R on the GPU, summed
+    in 64 bits.  over="all": every rank's is that of all ranks' gradients, for
+    parameters sharded over the ranks."""
+    if over not in ("rank", "all"):
+        raise _rr.CollectiveError(_rr.RC_ERR_INVALID_ARGUMENT, f"grad_norm: over {over!r} is neither 'rank' nor 'all'")
+    return _call("grad_norm", stream, grads, over == "all", out)
+
+
+class AdamWState:
+    """The ranks' parameters with their AdamW state, one map {parameter id:
+    tensor} per rank each:
+      params          float32, or 16 bits with a float32 copy in `master`;
+      m, v            means of the gradients and of their squares: float32, or
+                      with bits=8 float8_e4m3fn codes of m and of the root of v
+                      with float32 scales of 256 elements each in m_scale, v_scale;
+      step            int32, one number for each rank: the steps made.
+    The tensors are updated in place by adamw_step, which goes by their addresses
+    from here: it refuses a state whose tensors have been given other memory.
+    One made from saved tensors goes on where they were saved."""
+
+    __slots__ = ("bits", "params", "m", "v", "step", "master", "m_scale", "v_scale", "_table")
+
+    def __init__(self, params, bits, m, v, step, master=None, m_scale=None, v_scale=None):
+        self.bits, self.params, self.m, self.v, self.step = bits, params, m, v, step
+        self.master, self.m_scale, self.v_scale = master, m_scale, v_scale
+        self._table = _call("adamw_table", None, bits, params, master, m, v, m_scale, v_scale)
+
+
+def adamw_state(params, bits=32):
+    """A new state for params, one map {parameter id: tensor} per rank: means of
+    zero, 32 or 8 bits each, and float32 copies of 16-bit parameters."""
+    torch = _rr._torch()
+    dtype = torch.float8_e4m3fn if bits == 8 else torch.float32
+
+    def zeros():
+        return [{k: torch.zeros(p.shape, dtype=dtype, device=p.device) for k, p in m.items()} for m in params]
+
+    def scales():
+        return [{k: torch.zeros(-(-p.numel() // 256), device=p.device) for k, p in m.items()} for m in params]
+
+    master = [{k: p.detach().float() for k, p in m.items() if p.dtype != torch.float32} for m in params]
+    device = next((p.device for m in params for p in m.values()), None)
+    return AdamWState(params, bits, zeros(), zeros(), torch.zeros(len(params), dtype=torch.int32, device=device),
+                      master=master, m_scale=scales() if bits == 8 else None, v_scale=scales() if bits == 8 else None)
+
+
+def adamw_step(state, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, norms=None, max_norm=None,
+               grad_scale=1.0, seed=0, out=None, stream=None):
+    """One AdamW step of every parameter that has a gradient, grads[r] a map
+    {parameter id: tensor} of the parameters' types or float32 (include/rc.h has
+    the formulas).  norms are grad_norm's: a rank whose norm is not finite makes
+    no step, and with max_norm larger gradients are scaled down to it, both
+    decided on the GPU.  grad_scale: a factor of the gradients before all that.
+    lr: a number, or a float32 tensor of one element on the GPU, for steps
+    captured into a graph.  8-bit states are rounded by chance, as `seed`, the
+    step and the element's place say.  In place, or into `out`, another state of
+    the same parameters.  Steps of one state run one after the other."""
+    to = state if out is None else out
+    _call("adamw_step", stream, state._table, state.step, to._table, to.step, grads, lr, betas[0], betas[1], eps,
+          weight_decay, norms, 0.0 if max_norm is None else max_norm, grad_scale, seed)
+    return to

@@ -245,11 +245,12 @@ inline int32_t to_int32(PyObject* o, const char* what) {
     if (v < INT32_MIN || v > INT32_MAX) raise(RC_ERR_INVALID_ARGUMENT, what, "%lld is out of range", v);
     return (int32_t)v;
 }
-inline float to_float(PyObject* o) {
+inline double to_double(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw Raised{};
-    return (float)v;
+    return v;
 }
+inline float to_float(PyObject* o) { return (float)to_double(o); }
 inline bool to_bool(PyObject* o) {
     const int v = PyObject_IsTrue(o);
     if (v < 0) throw Raised{};

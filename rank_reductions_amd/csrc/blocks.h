@@ -50,4 +50,95 @@ inline int launch_rms_norm_grad(const NormArgs& a, int dtype, int weight_dtype, 
 // Workgroups of each rank that sum its weights' gradient.
 RankSpans norm_parts(const RankSpans& tokens);
 
+// ---------------------------------------------------------------- gradient norms
+constexpr int64_t kNormChunk = 32768;  // elements of a workgroup
+constexpr int kNormList = 150;         // gradients of a launch: kernel arguments hold 4096 bytes
+
+struct GradNormArgs {
+    const void* grad[kNormList];
+    int64_t count[kNormList];
+    int32_t first[kNormList];  // the gradient's first chunk within the launch
+    uint8_t dtype[kNormList];
+    int32_t n;
+    int32_t chunks;
+    double* partial;           // the launch's first chunk
+};
+struct GradNormJoin {
+    const double* partial;
+    float* norms;
+    int64_t first[kMaxRanks + 1];  // chunks of each rank
+    int32_t nranks;
+    int32_t over_all;
+};
+int launch_grad_norm(const GradNormArgs& a, void* stream);
+int launch_grad_norm_join(const GradNormJoin& a, void* stream);
+
+// ---------------------------------------------------------------- AdamW
+constexpr int64_t kAdamwChunk = 8192;  // elements of a workgroup, a multiple of RC_ADAMW_BLOCK
+constexpr int kAdamwList = 440;        // parameters of a launch
+
+struct AdamwEntry {
+    void* param;
+    float* master;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    int64_t count;
+    int64_t first_chunk;
+    int32_t dtype;
+    int32_t rank;
+};
+// What a rank's elements are computed with, written at each step's start.
+struct AdamwFactors {
+    float grad;    // of the gradient
+    float keep;    // 1 - lr * weight_decay
+    float rate;    // lr / (1 - beta1^t)
+    float root;    // 1 / sqrt(1 - beta2^t)
+    uint32_t key;  // of the roundings
+    int32_t skip;
+    int32_t pad[2];
+};
+// A table: this, then the entries, the entry of each chunk, and on the host's
+// side alone the spans of all buffers in order.
+struct AdamwHeader {
+    uint64_t magic;
+    int64_t bytes;
+    int32_t nranks;
+    int32_t bits;
+    int32_t first[kMaxRanks + 1];  // parameters of each rank
+    int32_t spans;
+    int64_t chunks;
+    int64_t entries_at, chunks_at, spans_at;  // byte offsets
+    AdamwFactors factors[kMaxRanks];
+};
+struct AdamwSpan {
+    uint64_t lo, hi;
+};
+constexpr uint64_t kAdamwMagic = 0x6164616d77746231ull;
+
+struct AdamwBegin {
+    AdamwHeader* table;
+    double lr, beta1, beta2, weight_decay, max_norm, grad_scale;
+    const float* lr_on_gpu;
+    const float* norms;
+    const int32_t* steps;
+    int32_t* steps_out;
+    uint32_t seed;
+    int32_t nranks;
+};
+struct AdamwArgs {
+    uint64_t grad[kAdamwList];  // addresses; the top byte is the type
+    const AdamwHeader* table;
+    const AdamwHeader* out;
+    int64_t entries_at, chunks_at;
+    int32_t first;              // the launch's first parameter
+    int32_t pad;
+    int64_t first_chunk, chunks;
+    float beta1, rest1, beta2, rest2, eps;
+};
+static_assert(sizeof(GradNormArgs) <= 4096 && sizeof(AdamwArgs) <= 4096, "kernel arguments");
+int launch_adamw_begin(const AdamwBegin& a, void* stream);
+int launch_adamw(const AdamwArgs& a, int bits, void* stream);
+
 }  // namespace rc
