@@ -569,6 +569,52 @@ int rc_rms_norm_grad(const rc_norm_desc* desc, const void* const* d_ys, const vo
                      const void* const* weights, const void* const* d_sums, void* const* d_xs, void* const* d_weights,
                      void* workspace, int64_t workspace_bytes, void* stream);
 
+/* A mixture-of-experts layer for a few tokens: what a dispatch, the experts'
+ * products and a combine give, in two kernels that read the chosen experts'
+ * weights once, where they lie.  struct_size = sizeof(rc_moe_desc).
+ *   dtype         of the rows xs: RC_F32, RC_F16, RC_BF16 or RC_E4M3
+ *   weight_dtype  dtype, or RC_E4M3 (not with RC_F32)
+ *   out_dtype     of ys: dtype; with RC_E4M3 rows RC_F32, RC_F16 or RC_BF16
+ *   num_experts   E in [1, RC_MAX_EXPERTS], divisible by R; rank d has the
+ *                 experts [d*E/R, (d+1)*E/R)
+ *   top_k         K in [1, RC_MAX_TOP_K]
+ *   width, inner  elements of a row, and of an expert's hidden layer, in
+ *                 [1, RC_MAX_MOE_WIDTH]
+ *   tokens        [R]; all ranks' tokens times K: at most RC_MAX_MOE_ENTRIES */
+#define RC_MAX_MOE_ENTRIES 2048
+#define RC_MAX_MOE_WIDTH 65536
+typedef struct rc_moe_desc {
+    uint32_t struct_size;
+    int32_t dtype;
+    int32_t weight_dtype;
+    int32_t out_dtype;
+    int32_t num_experts;
+    int32_t top_k;
+    int64_t width;
+    int64_t inner;
+    const int64_t* tokens;
+    int64_t session;
+} rc_moe_desc;
+
+/* ys[r][t] = the sum over k = 0, 1, ... of weights[r][t, k] * D (silu(G x) * (U x))
+ * with x = xs[r][t] (times scales[r][t]) and G, U, D the matrices of expert
+ * experts[r][t, k]; an expert outside [0, E) adds nothing.  silu(z) = z / (1 +
+ * exp(-z)).
+ *   xs[r]       [tokens[r], width]; scales[r] [tokens[r]] float32 with RC_E4M3
+ *               rows, else scales is NULL
+ *   experts[r]  [tokens[r], K] int32; weights[r] the same, float32
+ *   gate_up[d]  [E/R, 2 * inner, width], G above U; gate_up_scales[d]
+ *               [E/R, 2 * inner] float32 with RC_E4M3 weights, a factor of each
+ *               row, else NULL
+ *   down[d]     [E/R, width, inner]; down_scales[d] [E/R, width] likewise
+ * Sums are float32.  silu(G x) * (U x) is held in float32, or as two bfloat16
+ * numbers whose sum is within 2^-16 of it; ys are rounded once. */
+int rc_moe_layer_workspace(const rc_moe_desc* desc, int64_t* bytes);
+int rc_moe_layer(const rc_moe_desc* desc, const void* const* xs, const float* const* scales,
+                 const int32_t* const* experts, const float* const* weights, const void* const* gate_up,
+                 const float* const* gate_up_scales, const void* const* down, const float* const* down_scales,
+                 void* const* ys, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* One gradient: dense, `count` elements of RC_F32, RC_F16 or RC_BF16.  NULL with
  * a count of 0 where a parameter has none. */
 typedef struct rc_grad {

@@ -70,3 +70,23 @@ def adamw(p, g, m, v, t, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-
     v = betas[1] * v + (1 - betas[1]) * g * g
     update = m / (1 - betas[0] ** t) / (np.sqrt(v / (1 - betas[1] ** t)) + eps)
     return p - lr * weight_decay * p - lr * update, m, v
+
+
+# ---------------------------------------------------------------- experts
+
+def moe_token(x, weights, experts, gate_up, down):
+    """One token's output and, for error bounds, the sum of its terms' sizes: gate_up [E, 2I, H], down [E, H, I]."""
+    y, size = np.zeros(down.shape[1]), np.zeros(down.shape[1])
+    inner = down.shape[2]
+    for w, e in zip(weights, experts):
+        if not 0 <= e < gate_up.shape[0]:
+            continue
+        g, u = gate_up[e, :inner] @ x, gate_up[e, inner:] @ x
+        ag, au = np.abs(gate_up[e, :inner]) @ np.abs(x), np.abs(gate_up[e, inner:]) @ np.abs(x)
+        s = 1 / (1 + np.exp(-g))
+        h = g * s * u
+        # by how much h moves, for a relative error of one in each term of its two sums
+        moved = np.abs(u) * (s + np.abs(g) * s * (1 - s)) * ag + np.abs(g * s) * au + np.abs(h) * (1 + np.abs(g))
+        y += w * (down[e] @ h)
+        size += np.abs(w) * (np.abs(down[e]) @ (moved + np.abs(h)))
+    return y, size

@@ -38,7 +38,7 @@ __all__ = [
     "rank_all_to_all_single", "rank_send", "rank_recv", "rank_barrier", "rank_split", "rank_split_all",
     "Communicator", "route", "route_grad", "DispatchPlan", "dispatch_plan", "dispatch", "combine", "combine_grad",
     "embedding", "embedding_grad", "rms_norm", "rms_norm_grad",
-    "grad_norm", "AdamWState", "adamw_state", "adamw_step",
+    "moe_layer", "grad_norm", "AdamWState", "adamw_state", "adamw_step",
 ]
 
 RC_MAX_RANKS = 16
@@ -836,5 +836,5 @@ from .rows import (  # noqa: E402,F401
 )
 from . import blocks  # noqa: E402
 from .blocks import (  # noqa: E402,F401
-    AdamWState, adamw_state, adamw_step, grad_norm, rms_norm, rms_norm_grad,
+    AdamWState, adamw_state, adamw_step, grad_norm, moe_layer, rms_norm, rms_norm_grad,
 )

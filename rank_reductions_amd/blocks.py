@@ -5,6 +5,9 @@ gradient sync (whole-call form; include/rc.h, "Block operators").
     codes, scales, sums = rr.rms_norm(xs, weights, residuals=hs, quantize="e4m3")
     d_xs, d_weights = rr.rms_norm_grad(d_ys, sums, weights, d_sums=d_hs)
 
+    weights, experts = rr.route(logits, top_k=8)
+    ys = rr.moe_layer(xs, weights, experts, gate_up, down) # a few tokens, the experts' weights read once
+
     state = rr.adamw_state(params, bits=8)                 # params[r]: {id: tensor}
     rr.all_reduce_params(grads, "mean", out=grads)
     norms = rr.grad_norm(grads)
@@ -21,7 +24,7 @@ import ctypes
 import rank_reductions_amd as _rr
 from rank_reductions_amd.rows import _call, _choice
 
-__all__ = ["rms_norm", "rms_norm_grad", "grad_norm", "AdamWState", "adamw_state", "adamw_step"]
+__all__ = ["rms_norm", "rms_norm_grad", "moe_layer", "grad_norm", "AdamWState", "adamw_state", "adamw_step"]
 
 
 RC_E4M3 = 5
@@ -37,6 +40,21 @@ class RcNormDesc(ctypes.Structure):
         ("group", ctypes.c_int32),
         ("eps", ctypes.c_float),
         ("width", ctypes.c_int64),
+        ("tokens", ctypes.c_void_p),
+        ("session", ctypes.c_int64),
+    ]
+
+
+class RcMoeDesc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("num_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("width", ctypes.c_int64),
+        ("inner", ctypes.c_int64),
         ("tokens", ctypes.c_void_p),
         ("session", ctypes.c_int64),
     ]
@@ -107,6 +125,8 @@ def declare(lib):
         "rc_rms_norm": [p, p, p, p, p, p, p, p],
         "rc_rms_norm_grad_workspace": [p, p],
         "rc_rms_norm_grad": [p, p, p, p, p, p, p, p, i64, p],
+        "rc_moe_layer_workspace": [p, p],
+        "rc_moe_layer": [p, p, p, p, p, p, p, p, p, p, p, i64, p],
         "rc_grad_norm_workspace": [p, p, p, p],
         "rc_grad_norm": [p, p, p, p, p, i64, p],
         "rc_adamw_table": [p, p, p, p, p],
@@ -151,6 +171,24 @@ def rms_norm_grad(d_ys, sums, weights, eps=1e-6, d_sums=None, out=None, stream=N
     themselves; d_xs is the gradient of the residuals too.  d_weights[r] is summed
     over rank r's rows, of the weights' type.  d_xs may be d_ys or d_sums."""
     return _call("rms_norm_grad", stream, d_ys, sums, weights, eps, d_sums, out)
+
+
+# ---------------------------------------------------------------- experts
+
+def moe_layer(xs, weights, experts, gate_up, down, scales=None, gate_up_scales=None, down_scales=None, dtype=None,
+              out=None, stream=None):
+    """A mixture-of-experts layer for a few tokens (all ranks' tokens times top_k
+    up to 2048; dispatch and combine take any number): ys[r][t] = the sum over k
+    of weights[r][t, k] * down (silu(gate x) * (up x)) with the matrices of
+    expert experts[r][t, k], as route gives them (-1: none).  xs[r] is [tokens,
+    width]; rank d holds the weights of its experts, gate_up[d] [experts of a
+    rank, 2 * inner, width] (gate above up) and down[d] [experts, width, inner],
+    of the rows' type or, with 16-bit rows, float8_e4m3fn with gate_up_scales
+    [experts, 2 * inner] and down_scales [experts, width], float32 factors of the
+    rows.  8-bit rows (rms_norm's with a scale a row: scales [tokens, 1]) take
+    8-bit weights, and give ys of `dtype` (bfloat16 unless said or as `out` has
+    it).  The chosen experts' weights are read once, where they lie."""
+    return _call("moe_layer", stream, xs, weights, experts, gate_up, down, scales, gate_up_scales, down_scales, dtype, out)
 
 
 # ---------------------------------------------------------------- gradient norms and AdamW

@@ -43,6 +43,7 @@ HIP_SOURCES = [
     ("block_norm.hip", "block_norm_f32", {"RC_ROW_TYPE": "F32"}),
     ("block_norm.hip", "block_norm_f16", {"RC_ROW_TYPE": "F16"}),
     ("block_norm.hip", "block_norm_bf16", {"RC_ROW_TYPE": "BF16"}),
+    ("block_moe.hip", "block_moe", {}),
     ("block_adamw.hip", "block_adamw", {}),
     ("device.hip", "device", {}),
 ]

@@ -141,6 +141,111 @@ PyObject* rms_norm_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// ---------------------------------------------------------------- experts
+
+int moe_type(ScalarType t, const char* what) {
+    switch (t) {
+        case ScalarType::Float: return RC_F32;
+        case ScalarType::Half: return RC_F16;
+        case ScalarType::BFloat16: return RC_BF16;
+        case kE4M3: return RC_E4M3;
+        default: break;
+    }
+    PyErr_Format(PyExc_TypeError, "%s: unsupported dtype %s; float32, float16, bfloat16 and float8_e4m3fn are supported", what, type_name(t));
+    throw Raised{};
+}
+
+// R lists of weights, [experts, rows, cols] each.
+void expect3(Tensors& t, ScalarType type, const at::Device& dev, int64_t experts, int64_t rows, int64_t cols, const char* what) {
+    for (int r = 0; r < t.n; ++r) {
+        const Tensor& x = *t.t[r];
+        if (x.scalar_type() != type)
+            raise(RC_ERR_DTYPE_MISMATCH, what, "rank %d has dtype %s, expected %s", r, type_name(x.scalar_type()), type_name(type));
+        if (x.dim() != 3 || x.size(0) != experts || x.size(1) != rows || x.size(2) != cols)
+            raise(RC_ERR_SHAPE_MISMATCH, what, "rank %d: expected (%lld, %lld, %lld)", r, (long long)experts, (long long)rows, (long long)cols);
+        if (x.device() != dev) raise(RC_ERR_INVALID_ARGUMENT, what, "rank %d on %s, others on %s", r, x.device().str().c_str(), dev.str().c_str());
+        if (x.layout() != at::kStrided || !x.is_contiguous()) raise(RC_ERR_INVALID_ARGUMENT, what, "rank %d is not contiguous", r);
+        t.p[r] = x.data_ptr();
+    }
+}
+
+// moe_layer(xs, weights, experts, gate_up, down, scales or None, gate_up_scales or None, down_scales or None, dtype or None, out or None)
+PyObject* moe_layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        arity(n, {"moe_layer", 10});
+        const char* what = "moe_layer";
+        const Session s;
+        const int R = s.ranks;
+        Tensors x, w, e, up, down, xs, us, ds, y;
+        x.take(a[0], R, what);
+        x.dims(2, what, "[tokens, width]");
+        const at::Device dev = x.t[0]->device();
+        const ScalarType type = x.t[0]->scalar_type();
+        int64_t tokens[RC_MAX_RANKS] = {}, one[RC_MAX_RANKS];
+        rows_of(x, tokens);
+        rc_moe_desc d{};
+        d.struct_size = sizeof d;
+        d.session = s.id;
+        d.dtype = moe_type(type, what);
+        d.width = x.t[0]->size(1);
+        d.tokens = tokens;
+        x.expect(type, dev, tokens, d.width, what);
+        e.take(a[2], R, "moe_layer experts");
+        e.dims(2, "moe_layer experts", "[tokens, top_k]");
+        const int64_t K = e.t[0]->size(1);
+        if (K > RC_MAX_TOP_K) raise(RC_ERR_INVALID_ARGUMENT, what, "top_k %lld", (long long)K);
+        d.top_k = (int32_t)K;
+        e.expect(ScalarType::Int, dev, tokens, K, "moe_layer experts");
+        w.take(a[1], R, "moe_layer weights");
+        w.expect(ScalarType::Float, dev, tokens, K, "moe_layer weights");
+        up.take(a[3], R, "moe_layer gate_up");
+        up.dims(3, "moe_layer gate_up", "[experts, 2 * inner, width]");
+        const int64_t per = up.t[0]->size(0), rows = up.t[0]->size(1);
+        if (per > RC_MAX_EXPERTS || rows % 2) raise(RC_ERR_SHAPE_MISMATCH, what, "gate_up of %lld experts, %lld rows", (long long)per, (long long)rows);
+        const ScalarType weight_type = up.t[0]->scalar_type();
+        d.weight_dtype = moe_type(weight_type, "moe_layer gate_up");
+        d.num_experts = (int32_t)(per * R);
+        d.inner = rows / 2;
+        expect3(up, weight_type, dev, per, rows, d.width, "moe_layer gate_up");
+        down.take(a[4], R, "moe_layer down");
+        expect3(down, weight_type, dev, per, d.width, d.inner, "moe_layer down");
+        if (a[5] != Py_None) {
+            xs.take(a[5], R, "moe_layer scales");
+            xs.expect(ScalarType::Float, dev, tokens, 1, "moe_layer scales");
+        }
+        for (int r = 0; r < R; ++r) one[r] = per;
+        if (a[6] != Py_None) {
+            us.take(a[6], R, "moe_layer gate_up_scales");
+            us.expect(ScalarType::Float, dev, one, rows, "moe_layer gate_up_scales");
+        }
+        if (a[7] != Py_None) {
+            ds.take(a[7], R, "moe_layer down_scales");
+            ds.expect(ScalarType::Float, dev, one, d.width, "moe_layer down_scales");
+        }
+        ScalarType out_type = type == kE4M3 ? ScalarType::BFloat16 : type;
+        if (a[8] != Py_None) {
+            if (!THPDtype_Check(a[8])) raise(RC_ERR_INVALID_ARGUMENT, what, "dtype is not a torch.dtype");
+            out_type = reinterpret_cast<THPDtype*>(a[8])->scalar_type;
+        }
+        if (a[9] != Py_None) {
+            y.take(a[9], R, "moe_layer output");
+            if (a[8] == Py_None) out_type = y.t[0]->scalar_type();
+        }
+        d.out_dtype = moe_type(out_type, "moe_layer output");
+        int64_t size = 0;
+        call([&] { return rc_moe_layer_workspace(&d, &size); });
+        if (a[9] == Py_None) y.make(R, tokens, d.width, out_type, dev, what);
+        y.expect(out_type, dev, tokens, d.width, "moe_layer output");
+        void* stream = stream_on(s, dev, what);
+        Tensor work;
+        if (size) work = at::empty({size}, options(ScalarType::Byte, dev));
+        auto floats = [](const Tensors& t) { return t.n ? reinterpret_cast<const float* const*>(t.p) : nullptr; };
+        call([&] { return rc_moe_layer(&d, x.p, floats(xs), reinterpret_cast<const int32_t* const*>(e.p), floats(w), up.p, floats(us), down.p,
+                               floats(ds), y.p, size ? work.data_ptr() : nullptr, size, stream); });
+        return y.give();
+    });
+}
+
 // ---------------------------------------------------------------- gradients and AdamW
 
 // Owned references to one map for each rank.
@@ -436,6 +541,6 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define RC_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
 PyMethodDef rows_binding::block_methods[] = {
-    RC_METHOD(rms_norm), RC_METHOD(rms_norm_grad), RC_METHOD(grad_norm), RC_METHOD(adamw_table), RC_METHOD(adamw_step),
+    RC_METHOD(rms_norm), RC_METHOD(rms_norm_grad), RC_METHOD(moe_layer), RC_METHOD(grad_norm), RC_METHOD(adamw_table), RC_METHOD(adamw_step),
     {nullptr, nullptr, 0, nullptr},
 };

@@ -45,6 +45,41 @@ Error check_norm(const char* what, int R, const rc_norm_desc* d, NormArgs* a) {
     return {};
 }
 
+// ---------------------------------------------------------------- experts
+
+int64_t any_element_size(int dtype) { return dtype == RC_E4M3 ? 1 : row_element_size(dtype); }
+
+Error check_moe(const char* what, int R, const rc_moe_desc* d, MoeArgs* a, int64_t* workspace) {
+    RC_TRY(check_desc(what, d, "rc_moe_desc"));
+    if (!any_element_size(d->dtype)) return bad(what, fmt("unknown dtype %lld", d->dtype));
+    if (d->weight_dtype != d->dtype && (d->weight_dtype != RC_E4M3 || d->dtype == RC_F32))
+        return bad(what, fmt("weight_dtype %lld for rows of dtype %lld", d->weight_dtype, d->dtype));
+    if (d->dtype == RC_E4M3 ? !row_element_size(d->out_dtype) : d->out_dtype != d->dtype)
+        return bad(what, fmt("out_dtype %lld for rows of dtype %lld", d->out_dtype, d->dtype));
+    if (d->num_experts < 1 || d->num_experts > RC_MAX_EXPERTS || d->num_experts % R)
+        return bad(what, fmt("num_experts %lld outside [1, 1024] or not divisible by the %lld ranks", d->num_experts, R));
+    if (d->top_k < 1 || d->top_k > RC_MAX_TOP_K) return bad(what, fmt("top_k %lld outside [1, 16]", d->top_k));
+    if (d->width < 1 || d->width > RC_MAX_MOE_WIDTH) return bad(what, fmt("width %lld outside [1, 65536]", d->width));
+    if (d->inner < 1 || d->inner > RC_MAX_MOE_WIDTH) return bad(what, fmt("inner %lld outside [1, 65536]", d->inner));
+    RC_TRY(spans_of(what, R, d->tokens, d->top_k, &a->entries));
+    const int64_t n = a->entries.total();
+    if (n > RC_MAX_MOE_ENTRIES)
+        return bad(what, fmt("%lld tokens times %lld choices: more than 2048 (a dispatch takes any number)", n / d->top_k, d->top_k));
+    a->num_experts = d->num_experts;
+    a->per_rank = d->num_experts / R;
+    a->top_k = d->top_k;
+    a->width = (int32_t)d->width;
+    a->inner = (int32_t)d->inner;
+    a->out_dtype = d->out_dtype;
+    a->hidden_row = (int32_t)((d->inner + 63) / 64 * 64);
+    a->hidden_plane = n * a->hidden_row * 2;
+    // parts enough to keep a workgroup's waves busy where few experts can be named, as far as their sums fit LDS
+    const int64_t experts = std::max<int64_t>(1, std::min<int64_t>(n, d->num_experts));
+    a->splits = (int32_t)std::max<int64_t>(1, std::min((32 + experts - 1) / experts, RC_MAX_MOE_ENTRIES / std::max<int64_t>(1, n)));
+    *workspace = n * a->hidden_row * 4;
+    return {};
+}
+
 // ---------------------------------------------------------------- gradients
 
 // One gradient's fields; *has: whether there is one.
@@ -254,6 +289,71 @@ int rc_rms_norm_grad(const rc_norm_desc* desc, const void* const* d_ys, const vo
         RC_TRY(b.check());
         if (validate_only) return {};
         return device_run([&] { return launch_rms_norm_grad(a, desc->dtype, desc->weight_dtype, stream); });
+    });
+}
+
+int rc_moe_layer_workspace(const rc_moe_desc* desc, int64_t* bytes) {
+    return whole_call([&](int R, bool) -> Error {
+        const char* what = "moe_layer_workspace";
+        MoeArgs a{};
+        int64_t ws = 0;
+        RC_TRY(check_moe(what, R, desc, &a, &ws));
+        RC_TRY(need(what, bytes, "bytes"));
+        *bytes = ws;
+        return {};
+    });
+}
+
+int rc_moe_layer(const rc_moe_desc* desc, const void* const* xs, const float* const* scales,
+                 const int32_t* const* experts, const float* const* weights, const void* const* gate_up,
+                 const float* const* gate_up_scales, const void* const* down, const float* const* down_scales,
+                 void* const* ys, void* workspace, int64_t workspace_bytes, void* stream) {
+    return whole_call([&](int R, bool validate_only) -> Error {
+        const char* what = "moe_layer";
+        MoeArgs a{};
+        int64_t ws = 0;
+        RC_TRY(check_moe(what, R, desc, &a, &ws));
+        RC_TRY(need(what, xs, "xs"));
+        RC_TRY(need(what, experts, "experts"));
+        RC_TRY(need(what, weights, "weights"));
+        RC_TRY(need(what, gate_up, "gate_up"));
+        RC_TRY(need(what, down, "down"));
+        RC_TRY(need(what, ys, "ys"));
+        const bool rows8 = desc->dtype == RC_E4M3, weights8 = desc->weight_dtype == RC_E4M3;
+        if (rows8 != (scales != nullptr)) return bad(what, "scales are given with 8-bit rows, and only then");
+        if (weights8 != (gate_up_scales != nullptr) || weights8 != (down_scales != nullptr))
+            return bad(what, "scales of the weights are given with 8-bit weights, and only then");
+        Buffers b(what);
+        RC_TRY(check_workspace(what, workspace, workspace_bytes, ws, &b));
+        const int64_t xe = any_element_size(desc->dtype), we = any_element_size(desc->weight_dtype);
+        const int64_t H = desc->width, I = desc->inner, per = a.per_rank, K = desc->top_k;
+        for (int r = 0; r < R; ++r) {
+            const int64_t n = desc->tokens[r];
+            b.read(xs[r], n * H, xe, "xs", r);
+            if (rows8) b.read(scales[r], n, 4, "scales", r);
+            b.read(experts[r], n * K, 4, "experts", r);
+            b.read(weights[r], n * K, 4, "weights", r);
+            if (a.entries.total()) {
+                b.read(gate_up[r], per * 2 * I * H, we, "gate_up", r);
+                b.read(down[r], per * H * I, we, "down", r);
+                if (weights8) b.read(gate_up_scales[r], per * 2 * I, 4, "gate_up_scales", r);
+                if (weights8) b.read(down_scales[r], per * H, 4, "down_scales", r);
+            }
+            b.write(ys[r], n * H, row_element_size(desc->out_dtype), "ys", r);
+            a.x[r] = xs[r];
+            a.x_scale[r] = rows8 ? scales[r] : nullptr;
+            a.experts[r] = experts[r];
+            a.weights[r] = weights[r];
+            a.gate_up[r] = gate_up[r];
+            a.gate_up_scale[r] = weights8 ? gate_up_scales[r] : nullptr;
+            a.down[r] = down[r];
+            a.down_scale[r] = weights8 ? down_scales[r] : nullptr;
+            a.y[r] = ys[r];
+        }
+        RC_TRY(b.check());
+        a.hidden = static_cast<uint8_t*>(workspace);
+        if (validate_only || !a.entries.total()) return {};
+        return device_run([&] { return launch_moe(a, desc->dtype, desc->weight_dtype, stream); });
     });
 }
 

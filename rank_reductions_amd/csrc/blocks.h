@@ -50,6 +50,32 @@ inline int launch_rms_norm_grad(const NormArgs& a, int dtype, int weight_dtype, 
 // Workgroups of each rank that sum its weights' gradient.
 RankSpans norm_parts(const RankSpans& tokens);
 
+// ---------------------------------------------------------------- experts
+struct MoeArgs {
+    const void* x[kMaxRanks];
+    const float* x_scale[kMaxRanks];
+    const int32_t* experts[kMaxRanks];
+    const float* weights[kMaxRanks];
+    const void* gate_up[kMaxRanks];
+    const float* gate_up_scale[kMaxRanks];
+    const void* down[kMaxRanks];
+    const float* down_scale[kMaxRanks];
+    void* y[kMaxRanks];
+    RankSpans entries;       // (token, k) of all ranks
+    uint8_t* hidden;         // silu(G x) * (U x) of every entry: [entries][hidden_row], float32, or bfloat16 twice
+    int64_t hidden_plane;    // bytes of all entries' first bfloat16 numbers
+    int32_t hidden_row;      // elements, a multiple of 64
+    int32_t num_experts;
+    int32_t per_rank;
+    int32_t top_k;
+    int32_t width;
+    int32_t inner;
+    int32_t out_dtype;
+    int32_t splits;          // parts of a sum over inner at most
+};
+static_assert(sizeof(MoeArgs) <= 4096, "kernel arguments");
+int launch_moe(const MoeArgs& a, int dtype, int weight_dtype, void* stream);
+
 // ---------------------------------------------------------------- gradient norms
 constexpr int64_t kNormChunk = 32768;  // elements of a workgroup
 constexpr int kNormList = 150;         // gradients of a launch: kernel arguments hold 4096 bytes

@@ -1,0 +1,211 @@
+"""The mixture-of-experts layer of a few tokens on the GPU against the oracle in
+64 bits.
+
+Error bound, with u = 2^-24: a sum of n products is off by at most (n / 4 + 16) * 2u
+of its terms' sizes (each lane group sums a part; the matrix instructions'
+sums are taken to be off by twice a float32 sum's), the exponential and the division by 4 u of
+h and g's own by its size; hidden values as two bfloat16 numbers by 2^-16, and a
+float16 weight's product without the two small parts by 2^-16: 3 * 2^-16 in all.
+oracle.moe_token adds the sizes up.  The output adds half a step.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import rank_reductions_amd as rr
+from gpu_util import session
+from oracle import blocks as orc
+from test_gpu_rows import DEV, HALF, TINY, TYPES, U, dev, f64, gen, near, normal, shifted
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+
+
+def inputs(counts, experts, top_k, width, inner, dtype, weights, seed, padding=0.0):
+    g = gen(seed)
+    R, E = len(counts), experts
+    eight = weights == "e4m3"
+    def w(*shape):
+        x = torch.randn(*shape, generator=g)
+        return (x * 100).clamp(-448, 448).to(E4M3) if eight else (x * shape[-1] ** -0.5).to(TYPES[weights])
+    if dtype == "e4m3":
+        xs = [(torch.randn(n, width, generator=g) * 100).clamp(-448, 448).to(E4M3) for n in counts]
+        scales = [0.005 + 0.01 * torch.rand(n, 1, generator=g) for n in counts]
+    else:
+        xs, scales = [normal(g, n, width, dtype=dtype) for n in counts], None
+    gu, dn = [w(E // R, 2 * inner, width) for _ in range(R)], [w(E // R, width, inner) for _ in range(R)]
+    gs = [(0.5 + torch.rand(E // R, 2 * inner, generator=g)) * 0.01 * width ** -0.5 for _ in range(R)] if eight else None
+    ds = [(0.5 + torch.rand(E // R, width, generator=g)) * 0.01 * inner ** -0.5 for _ in range(R)] if eight else None
+    ex, ws = [], []
+    for n in counts:
+        e = torch.argsort(torch.rand(n, E, generator=g), dim=1)[:, :top_k].to(torch.int32)
+        gone = torch.rand(n, top_k, generator=g) < padding
+        ex.append(torch.where(gone, -1, e).to(torch.int32).contiguous())
+        ws.append(torch.rand(n, top_k, generator=g))
+    return dict(xs=xs, weights=ws, experts=ex, gate_up=gu, down=dn, scales=scales, gate_up_scales=gs, down_scales=ds)
+
+
+def on_gpu(i):
+    return {k: dev(v) if v is not None else None for k, v in i.items()}
+
+
+def check(ys, i, out):
+    f = lambda ts: [t.float().double().numpy() for t in ts]  # noqa: E731
+    xs, gu, dn = f(i["xs"]), np.concatenate(f(i["gate_up"])), np.concatenate(f(i["down"]))
+    if i["scales"] is not None:
+        xs = [x * s for x, s in zip(xs, f(i["scales"]))]
+    if i["gate_up_scales"] is not None:
+        gu = gu * np.concatenate(f(i["gate_up_scales"]))[..., None]
+        dn = dn * np.concatenate(f(i["down_scales"]))[..., None]
+    H, I, K = dn.shape[1], dn.shape[2], i["experts"][0].shape[1]
+    wide = i["gate_up"][0].dtype == torch.float32
+    rel = 1.01 * 2 * U * (H / 4 + I / 4 + 32 + K + 8) + (0 if wide else 3 * 2.0 ** -16)
+    for r, x in enumerate(xs):
+        for t in range(x.shape[0]):
+            y, size = orc.moe_token(x[t], i["weights"][r][t].double().numpy(), i["experts"][r][t].numpy(), gu, dn)
+            near(ys[r][t].float().cpu().double().numpy(), y, rel * size + HALF[out] * np.abs(y) * 1.01 + TINY[out], f"rank {r}, token {t}")
+
+
+KINDS = [("f32", "f32", "f32"), ("f16", "f16", "f16"), ("bf16", "bf16", "bf16"), ("f16", "e4m3", "f16"), ("bf16", "e4m3", "bf16"),
+         ("e4m3", "e4m3", "bf16"), ("e4m3", "e4m3", "f16"), ("e4m3", "e4m3", "f32")]
+SHAPES = [
+    # tokens of each rank, experts, top_k, width, inner
+    ([1], 1, 1, 1, 1),
+    ([1], 8, 2, 64, 64),
+    ([1], 64, 8, 512, 192),
+    ([3, 0, 2], 12, 4, 100, 37),
+    ([5], 4, 3, 257, 130),
+    ([17, 1], 6, 2, 333, 65),   # more than one tile of entries to an expert
+    ([40], 3, 2, 96, 200),      # and more than two
+    ([200], 2, 1, 130, 48),     # and more than four
+    ([2, 2, 2, 2, 2, 2, 2, 2], 256, 8, 128, 64),
+    ([64, 64], 16, 16, 48, 33),  # 2048 entries
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("kind", KINDS, ids="-".join)
+def test_layer(shape, kind):
+    counts, experts, top_k, width, inner = shape
+    i = inputs(counts, experts, top_k, width, inner, kind[0], kind[1], 7, padding=0.2 if sum(counts) > 4 else 0.0)
+    with session(len(counts)):
+        ys = rr.moe_layer(**on_gpu(i), dtype=TYPES[kind[2]])
+        torch.cuda.synchronize()
+        assert all(y.dtype == TYPES[kind[2]] for y in ys)
+        check(ys, i, kind[2])
+
+
+@pytest.mark.parametrize("kind", KINDS[:6], ids="-".join)
+def test_rows_off_the_grid(kind):
+    i = inputs([3, 4], 4, 2, 333, 65, kind[0], kind[1], 3)
+    with session(2):
+        g = on_gpu(i)
+        for k in g:
+            if g[k] is not None:
+                g[k] = shifted(g[k], 3)
+        ys = rr.moe_layer(**g, out=shifted([torch.zeros(n, 333, dtype=TYPES[kind[2]], device=DEV) for n in (3, 4)], 1))
+        torch.cuda.synchronize()
+        check(ys, i, kind[2])
+
+
+def test_choices_that_repeat_or_name_none():
+    """One expert twice in a token, experts out of range, tokens without any, their rows not numbers."""
+    i = inputs([6], 4, 3, 128, 64, "bf16", "bf16", 5)
+    i["experts"] = [torch.tensor([[1, 1, 2], [-1, -1, -1], [4, 0, -7], [2**31 - 1, 3, 3], [-1, 2, -1], [0, 1, 2]], dtype=torch.int32)]
+    i["xs"][0][1] = float("nan")
+    i["weights"][0][2, 0] = float("nan")  # of expert 4, that is none
+    i["gate_up"][0][3, 5] = 0.0
+    with session(1):
+        ys = rr.moe_layer(**on_gpu(i))
+        torch.cuda.synchronize()
+    assert not ys[0][1].any()
+    i["xs"][0][1] = 0
+    i["weights"][0][2, 0] = 0
+    check(ys, i, "bf16")
+
+
+def test_a_row_that_is_not_finite_stays_alone():
+    i = inputs([8], 2, 1, 256, 128, "bf16", "bf16", 9)
+    i["experts"][0].zero_()
+    with session(1):
+        want = rr.moe_layer(**on_gpu(i))[0].clone()
+        i["xs"][0][3, 10] = float("inf")
+        i["xs"][0][5, 20] = float("nan")
+        got = rr.moe_layer(**on_gpu(i))[0]
+        torch.cuda.synchronize()
+        for t in range(8):
+            assert got[t].isnan().any() if t in (3, 5) else torch.equal(got[t], want[t]), t
+
+
+def test_values_beyond_float16():
+    """Hidden values past 65504, and far below its smallest, with float16 weights."""
+    i = inputs([2], 2, 1, 64, 64, "f16", "f16", 11)
+    i["experts"][0].copy_(torch.tensor([[0], [1]]))
+    i["gate_up"][0][0] *= 200
+    i["down"][0][0] *= 2.0 ** -12
+    i["gate_up"][0][1] *= 2.0 ** -7
+    with session(1):
+        ys = rr.moe_layer(**on_gpu(i))
+        torch.cuda.synchronize()
+        check(ys, i, "f16")
+
+
+def test_a_token_alone_and_among_others():
+    """Bit for bit: what a token gives does not hang on the others, or on the rank that holds it."""
+    for kind in (("bf16", "bf16"), ("e4m3", "e4m3")):
+        i = inputs([30], 8, 8, 192, 96, *kind, 13)
+        one = dict(i, **{k: [i[k][0][11:12]] for k in ("xs", "weights", "experts")})
+        if i["scales"] is not None:
+            one["scales"] = [i["scales"][0][11:12]]
+        with session(1):
+            a, b = rr.moe_layer(**on_gpu(i)), rr.moe_layer(**on_gpu(one))
+            torch.cuda.synchronize()
+            # the sums over inner are cut into as many parts as keep the waves busy, which hangs on the number of experts
+            # named: all eight here, both times
+            assert torch.equal(a[0][11], b[0][0])
+
+
+def test_graph_replays():
+    i = inputs([2, 3], 8, 2, 256, 128, "bf16", "bf16", 15)
+    with session(2):
+        g = on_gpu(i)
+        out = [torch.zeros(n, 256, dtype=torch.bfloat16, device=DEV) for n in (2, 3)]
+        rr.moe_layer(**g, out=out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            rr.moe_layer(**g, out=out)
+        for k in range(4):
+            for x, e in zip(g["xs"], g["experts"]):
+                x.mul_(-1.25)
+                e.copy_((e + 1) % 8)
+            want = rr.moe_layer(**g)
+            torch.cuda.synchronize()
+            for y in out:
+                y.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_against_dispatch_and_combine():
+    """The layer is what dispatch, the experts' products and combine give, float32."""
+    i = inputs([5, 9], 4, 2, 160, 96, "f32", "f32", 17, padding=0.1)
+    with session(2):
+        g = on_gpu(i)
+        got = rr.moe_layer(**g)
+        plan = rr.dispatch_plan(g["experts"], 4)
+        rows = rr.dispatch(g["xs"], plan)
+        results = []
+        for d in range(2):
+            y = torch.zeros_like(rows[d])
+            at = plan.offsets[d].tolist()
+            for e in range(2):
+                x = rows[d][at[e]:at[e + 1]]
+                a, b = (x @ g["gate_up"][d][e].t()).split(96, 1)
+                y[at[e]:at[e + 1]] = (torch.nn.functional.silu(a) * b) @ g["down"][d][e].t()
+            results.append(y)
+        want = rr.combine(results, plan, g["weights"])
+        for a, b in zip(got, want):
+            assert torch.allclose(a, b, rtol=1e-4, atol=1e-5)
