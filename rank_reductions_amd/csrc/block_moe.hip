@@ -1,13 +1,18 @@
-// A mixture-of-experts layer for a few tokens in two kernels.
+// A mixture-of-experts layer for a few tokens.
 //
-// The first computes silu(G x) * (U x) for every (token, expert) entry, the
-// second D times that and the weighted sum over a token's experts.  With few
-// tokens the time is that of reading the chosen experts' weights, so each weight
-// is read once, by one wave, straight into the registers that the matrix
-// instructions take: 16 rows of weights by 16 entries, sums over 16 bytes a lane
-// and row at a time.  Entries of an expert share its weights' pass; a lane's
-// column of the product is one entry, so an entry's result does not hang on which
-// others stand beside it.
+// The first kernel computes silu(G x) * (U x) for every (token, expert) entry, the
+// second D times that, the third the weighted sum over a token's experts.  With
+// few tokens the time is that of reading the chosen experts' weights, so each
+// weight is read once, by one wave, straight into the registers that the matrix
+// instructions take: 16 rows of weights by 16 entries, 64 bytes of each row at a
+// time.  Entries of an expert share its weights' pass; a lane's column of the
+// product is one entry, so an entry's result does not hang on which others stand
+// beside it.  One token of 4096 on 8 experts (302 MB of bfloat16 weights) takes 73
+// us, 4.1 TB/s; 64 tokens on 64 experts in 8 bits (1.2 GB) 279 us, 4.3 TB/s; 256
+// tokens, bfloat16 (2.4 GB), 545 us, 4.4 TB/s, where a kernel that only reads
+// reaches 5.9.  A kernel that holds every token's sum for its columns does without
+// the third, but reads the hidden values once for each 16 columns: 190 us in place
+// of 100 for 64 tokens.
 #include "blocks_impl.h"
 
 namespace rc {
@@ -18,6 +23,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4a1 __attribute__((ext_vector_type(4), aligned(1)));
 
 struct E4M3 {
@@ -25,23 +31,28 @@ struct E4M3 {
     static constexpr int n = 16;
 };
 
-// 16 bytes of a row from element k on; with Full all are there, else zeros
-// from element `count` on.
-template <class T, bool Full>
-__device__ __forceinline__ u32x4 load_row(const typename T::E* row, int k, int count) {
-    constexpr int n = 16 / sizeof(typename T::E), per = n / 4;
-    if (Full || k + n <= count) return *reinterpret_cast<const u32x4a1*>(row + k);
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-        if (k + i >= count) continue;
-        const typename T::E e = row[k + i];
-        uint32_t u;
-        if constexpr (sizeof(e) == 4) u = __builtin_bit_cast(uint32_t, e);
-        else if constexpr (sizeof(e) == 2) u = __builtin_bit_cast(uint16_t, e);
-        else u = e;
-        v[i / per] |= u << (8 * sizeof(e) * (i % per));
+__device__ __forceinline__ u32x4 load_bytes(const uint8_t* p) { return *reinterpret_cast<const u32x4a1*>(p); }
+
+// v moved down by `bytes` >= 0, zeros from above.
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int bytes) {
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    const int bits = 8 * (bytes & 7);
+    if (bytes >= 16) lo = hi = 0;
+    if (bytes >= 8) lo = hi, hi = 0;
+    lo = lo >> bits | (bits ? hi << (64 - bits) : 0);
+    hi >>= bits;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// 16 bytes of a row of `size` bytes from byte `at` on, zeros behind its end: those
+// at its end moved down, without a branch unless the row is shorter.
+__device__ __forceinline__ u32x4 load_end(const uint8_t* row, int at, int size) {
+    if (size >= 16) {
+        const int from = min(at, size - 16);
+        return shift_down(load_bytes(row + from), at - from);
     }
+    u32x4 v = {0, 0, 0, 0};
+    for (int i = 0; i < 16 && at + i < size; ++i) v[i / 4] |= (uint32_t)row[at + i] << (8 * (i % 4));
     return v;
 }
 
@@ -101,7 +112,11 @@ template <class X, class W>
 struct Up {
     static constexpr int kK = 64 / (int)sizeof(typename W::E);
     static constexpr int kX = kK / 4 * (int)sizeof(typename X::E) / 16;  // 16-byte vectors of x
-    __device__ __forceinline__ static f32x4 mma(u32x4 w, const u32x4* x, f32x4 c) {
+    struct Frag {
+        u32x4 x[kX];
+    };
+    __device__ __forceinline__ static f32x4 mma(u32x4 w, const Frag& f, f32x4 c) {
+        const u32x4* x = f.x;
         if constexpr (sizeof(typename W::E) == 4) {
             return mma_f32(w, x[0], c);
         } else if constexpr (sizeof(typename X::E) == 1) {
@@ -124,7 +139,11 @@ struct Down {
     static constexpr int kK = 64 / (int)sizeof(typename W::E);
     static constexpr bool kWide = sizeof(typename W::E) == 4;
     static constexpr int kH = kWide ? 1 : kK / 32;  // 16-byte vectors of one kind of hidden value
-    __device__ __forceinline__ static f32x4 mma(u32x4 w, const u32x4* hi, const u32x4* lo, f32x4 c) {
+    struct Frag {
+        u32x4 hi[kH], lo[kH];
+    };
+    __device__ __forceinline__ static f32x4 mma(u32x4 w, const Frag& f, f32x4 c) {
+        const u32x4 *hi = f.hi, *lo = f.lo;
         if constexpr (kWide) {
             return mma_f32(w, hi[0], c);
         } else if constexpr (sizeof(typename W::E) == 1) {
@@ -135,13 +154,13 @@ struct Down {
             }
             return c;
         } else if constexpr (__is_same(W, F16)) {
-            float f[8], l[8];
-            F16::unpack(w, f);
-            const u32x4 first = BF16::pack(f);
+            float e[8], l[8];
+            F16::unpack(w, e);
+            const u32x4 first = BF16::pack(e);
             float g[8];
             BF16::unpack(first, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) l[i] = __builtin_isfinite(g[i]) ? f[i] - g[i] : 0.0f;
+            for (int i = 0; i < 8; ++i) l[i] = __builtin_isfinite(g[i]) ? e[i] - g[i] : 0.0f;
             return mma_bf16(first, lo[0], mma_bf16(BF16::pack(l), hi[0], mma_bf16(first, hi[0], c)));
         } else {
             return mma_bf16(w, lo[0], mma_bf16(w, hi[0], c));
@@ -149,15 +168,25 @@ struct Down {
     }
 };
 
-constexpr int kTile = 16;   // rows of weights, and entries, of a product
-constexpr int kUpWaves = 4;
-constexpr int kDownWaves = 8;
+constexpr int kTile = 16;  // rows of weights, and entries, of a product
+constexpr int kWaves = 4;
+constexpr int kThreads = kWaves * kWave;
 constexpr int kMaxWords = RC_MAX_EXPERTS / 32;
+
+// An expert that entries name: its entries are list[first .. first + count).
+// The first kernel writes them for the second.
+struct Named {
+    int32_t expert, first, count, pad;
+};
+__device__ __forceinline__ Named* named_of(const MoeArgs& a) { return reinterpret_cast<Named*>(a.lists); }
+__device__ __forceinline__ uint16_t* list_of(const MoeArgs& a) {
+    return reinterpret_cast<uint16_t*>(a.lists + sizeof(Named) * min(a.num_experts, a.entries.total()));
+}
 
 // The expert of entry i, -1 for none.
 __device__ __forceinline__ int expert_of(const MoeArgs& a, int32_t i) {
     int32_t local;
-    const int rank = rank_of(a.entries, i, &local);
+    const int rank = rank_at(a.entries, i, &local);
     const int e = a.experts[rank][local];
     return e >= 0 && e < a.num_experts ? e : -1;
 }
@@ -182,99 +211,299 @@ __device__ __forceinline__ int nth_expert(const uint32_t* words, int num_words, 
     return __builtin_amdgcn_readlane(lane * 32 + __ffs((int)w) - 1, __builtin_amdgcn_readfirstlane(at));
 }
 
-// G x and U x for kTile rows of each and N tiles of entries, the sum cut over the
-// workgroup's waves; then the waves' parts added and the hidden values written.
+// This wave's part of a sum of `steps` steps: a quarter, in multiples of `ahead`.
+__device__ __forceinline__ void part_of(int steps, int ahead, int* s0, int* s1) {
+    const int each = ((steps + kWaves - 1) / kWaves + ahead - 1) / ahead * ahead;
+    *s0 = threadIdx.x / kWave * each;
+    *s1 = min(*s0 + each, steps);
+}
+
+// Sums over the steps [s0, s1) of Rows row tiles by N tiles of entries: c[row
+// tile][entry tile].  A step is 64 bytes of a row of weights, of which the four
+// lanes that share it take 16 each.  w: this lane's row of each row tile, of
+// `size` bytes; other(n, step, frag, full): the entries' side of a step;
+// zeros behind the sum's end where the step is not full.
+template <class M, int Rows, int N, int Ahead, class Other>
+__device__ __forceinline__ void sums_of(const uint8_t* const* w, int s0, int s1, int size, f32x4 (&c)[Rows][N], Other other) {
+    const int mine = lane_id() / kTile * 16, whole = min(s1, size / 64);
+    auto use = [&](const u32x4 (&v)[Rows], const typename M::Frag (&f)[N]) {
+#pragma unroll
+        for (int r = 0; r < Rows; ++r)
+#pragma unroll
+            for (int n = 0; n < N; ++n) c[r][n] = M::mma(v[r], f[n], c[r][n]);
+    };
+    for (int s = s0; s < whole; s += Ahead) {
+        u32x4 v[Ahead][Rows];
+        typename M::Frag f[Ahead][N];
+#pragma unroll
+        for (int j = 0; j < Ahead; ++j) {
+            const int at = min(s + j, whole - 1);  // what is read twice is used once
+#pragma unroll
+            for (int r = 0; r < Rows; ++r) v[j][r] = load_bytes(w[r] + at * 64 + mine);
+#pragma unroll
+            for (int n = 0; n < N; ++n) other(n, at, f[j][n], true);
+        }
+#pragma unroll
+        for (int j = 0; j < Ahead; ++j)
+            if (s + j < whole) use(v[j], f[j]);
+    }
+    if (whole < s1 && s0 < s1) {  // a step that the row fills in part
+        u32x4 v[Rows];
+        typename M::Frag f[N];
+#pragma unroll
+        for (int r = 0; r < Rows; ++r) v[r] = load_end(w[r], whole * 64 + mine, size);
+#pragma unroll
+        for (int n = 0; n < N; ++n) other(n, whole, f[n], false);
+        use(v, f);
+    }
+}
+
+// ---- the same sums where an expert has many entries: the entries' side is read
+// once by the workgroup, through LDS, and each of its waves has rows of its own.
+constexpr int kManyWaves = 8;
+constexpr int kManyThreads = kManyWaves * kWave;
+
+// Bytes a step takes of an entry, in kPlanes rows of their own.
+template <int Bytes, int Planes, int N>
+struct Stage {
+    static constexpr int kStage = Bytes * N > 512 ? 65536 : 32768;       // bytes of a part; two at a time
+    static constexpr int kSteps = kStage / (Bytes * N * kTile);          // of a part
+    static constexpr int kPlane = Bytes / Planes;                        // bytes of a step in a row
+    static constexpr int kRow = kSteps * kPlane + 16;                    // rows 16 bytes apart in the banks
+    static constexpr int kSize = kRow * Planes * N * kTile;              // of one of the two buffers
+    static constexpr int kUnits = kSteps * kPlane / 16;                  // 16-byte pieces of a row
+    static constexpr int kMine = kUnits * Planes * N * kTile / kManyThreads;
+    static constexpr int kAhead = N < 8 && kSteps >= 8 ? 4 : kSteps >= 4 ? 2 : 1;  // as registers allow
+    static_assert(kSteps >= 2 && kMine * kManyThreads == kUnits * Planes * N * kTile, "parts");
+};
+
+// A barrier that waits for LDS only: what is on its way from memory stays so.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// src: where this thread's pieces of the entries' rows begin, at byte `off[i]` of
+// rows of `row_size` bytes.  get(buffer, step of the part, n, frag): the entries'
+// side of a step out of LDS.
+template <class M, int Rows, int N, class S, class Get>
+__device__ __forceinline__ void staged_sums(const uint8_t* const* w, int size, const uint8_t* const* src, int row_size, uint8_t* lds,
+                                            f32x4 (&c)[Rows][N], Get get) {
+    constexpr int kAhead = S::kAhead;
+    const int mine = lane_id() / kTile * 16, whole = size / 64, steps = (size + 63) / 64;
+    auto load = [&](u32x4 (&v)[kAhead][Rows], int s) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int at = min(s + j, whole - 1);  // what is read twice is used once
+#pragma unroll
+            for (int r = 0; r < Rows; ++r) v[j][r] = load_bytes(w[r] + at * 64 + mine);
+        }
+    };
+    auto use_step = [&](const u32x4 (&v)[Rows], const uint8_t* from, int at) {
+        typename M::Frag f[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) get(from, at, n, f[n]);
+#pragma unroll
+        for (int r = 0; r < Rows; ++r)
+#pragma unroll
+            for (int n = 0; n < N; ++n) c[r][n] = M::mma(v[r], f[n], c[r][n]);
+    };
+    auto use = [&](const u32x4 (&v)[kAhead][Rows], const uint8_t* from, int at, int s) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (s + j < whole) use_step(v[j], from, at + j);
+    };
+    const int unit = threadIdx.x % S::kUnits * 16;
+    u32x4 held[S::kMine];
+    auto fetch = [&](int part) {
+        const int from = min(part * S::kUnits * 16 + unit, row_size - 16);
+#pragma unroll
+        for (int i = 0; i < S::kMine; ++i) held[i] = load_bytes(src[i] + from);
+    };
+    auto put = [&](uint8_t* to, int part) {
+        const int at = part * S::kUnits * 16 + unit, behind = at - min(at, row_size - 16);
+#pragma unroll
+        for (int i = 0; i < S::kMine; ++i)
+            *reinterpret_cast<u32x4*>(to + (threadIdx.x + i * kManyThreads) / S::kUnits * S::kRow + unit) = shift_down(held[i], behind);
+    };
+    u32x4 w0[kAhead][Rows], w1[kAhead][Rows];
+    const int parts = (steps + S::kSteps - 1) / S::kSteps;
+    fetch(0);
+    load(w0, 0);
+    __syncthreads();  // the buffers may still be read
+    put(lds, 0);
+    lds_barrier();
+    for (int p = 0; p < parts; ++p) {
+        const uint8_t* from = lds + (p & 1) * S::kSize;
+        fetch(min(p + 1, parts - 1));
+#pragma unroll
+        for (int at = 0; at < S::kSteps; at += 2 * kAhead) {
+            const int s = p * S::kSteps + at;
+            load(w1, s + kAhead);
+            use(w0, from, at, s);
+            load(w0, s + 2 * kAhead);
+            use(w1, from, at + kAhead, s + kAhead);
+        }
+        if (p + 1 < parts) put(lds + (~p & 1) * S::kSize, p + 1);
+        lds_barrier();
+    }
+    if (whole < steps) {  // a step that the row fills in part
+        u32x4 v[Rows];
+#pragma unroll
+        for (int r = 0; r < Rows; ++r) v[r] = load_end(w[r], whole * 64 + mine, size);
+        use_step(v, lds + ((parts - 1) & 1) * S::kSize, whole - (parts - 1) * S::kSteps);
+    }
+}
+
+// The hidden value of one entry and row from the two sums.
+template <class X, class W>
+__device__ __forceinline__ float hidden_of(const MoeArgs& a, int rank, int local, int row, float x_scale, float g, float u) {
+    if (row >= a.inner) return 0.0f;  // what the second product's sum ends on
+    if constexpr (sizeof(typename W::E) == 1) {
+        const float* f = a.gate_up_scale[rank] + (int64_t)local * 2 * a.inner + row;
+        g *= f[0];
+        u *= f[a.inner];
+    }
+    if constexpr (sizeof(typename X::E) == 1) {
+        g *= x_scale;
+        u *= x_scale;
+    }
+    return g / (1.0f + expf(-g)) * u;
+}
+template <class X>
+__device__ __forceinline__ float scale_of(const MoeArgs& a, int entry) {
+    if constexpr (sizeof(typename X::E) > 1) return 1.0f;
+    int32_t t;
+    const int rank = rank_at(a.entries, entry, &t);
+    return a.x_scale[rank][t / a.top_k];
+}
+
+// The hidden values of this lane's rows and entries, from the sums with G and with U.
 template <class X, class W, int N>
-__device__ __forceinline__ void up_tiles(const MoeArgs& a, int expert, const uint16_t* list, int first, int count, float* parts) {
-    using M = Up<X, W>;
-    constexpr int kAhead = N == 4 ? 2 : 4;
-    const int lane = lane_id(), wave = threadIdx.x / kWave, sub = lane / kTile;
-    const int rank = expert / a.per_rank, local = expert - rank * a.per_rank;
-    const int tile = blockIdx.x * kTile, row = min(tile + lane % kTile, a.inner - 1);
-    const int64_t K = a.width;
-    const typename W::E* gate = (const typename W::E*)a.gate_up[rank] + ((int64_t)local * 2 * a.inner + row) * K;
-    const typename W::E* up = gate + a.inner * K;
-    const typename X::E* x[N];
+__device__ __forceinline__ void write_hidden(const MoeArgs& a, int rank, int local, const uint16_t* list, int first, int count, int tile,
+                                             const f32x4 (&c)[2][N]) {
+    const int lane = lane_id(), row = tile + lane / kTile * 4;
+    if (row >= a.hidden_row) return;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const int i = first + n * kTile + lane % kTile;
-        int32_t at;  // columns behind the last entry repeat the first, and are dropped
-        const int r = rank_of(a.entries, list[i < count ? i : 0], &at);
-        x[n] = (const typename X::E*)a.x[r] + (int64_t)(at / a.top_k) * K;
-    }
-    f32x4 g[N] = {}, u[N] = {};
-    const int steps = ((int)K + M::kK - 1) / M::kK, whole = (int)K / M::kK, each = (steps + kUpWaves - 1) / kUpWaves;
-    const int s0 = wave * each, s1 = min(s0 + each, steps), full = min(s1, whole);
-    const int mine = sub * (M::kK / 4);
-    int s = s0;
-    for (; s + kAhead <= full; s += kAhead) {
-        u32x4 wg[kAhead], wu[kAhead], xv[kAhead][N][M::kX];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int k = (s + j) * M::kK + mine;
-            wg[j] = load_row<W, true>(gate, k, 0);
-            wu[j] = load_row<W, true>(up, k, 0);
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-#pragma unroll
-                for (int v = 0; v < M::kX; ++v) xv[j][n][v] = load_row<X, true>(x[n], k + v * 16 / (int)sizeof(typename X::E), 0);
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                g[n] = M::mma(wg[j], xv[j][n], g[n]);
-                u[n] = M::mma(wu[j], xv[j][n], u[n]);
-            }
-    }
-    for (; s < s1; ++s) {
-        const int k = s * M::kK + mine;
-        const u32x4 wg = load_row<W, false>(gate, k, (int)K), wu = load_row<W, false>(up, k, (int)K);
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            u32x4 xv[M::kX];
-#pragma unroll
-            for (int v = 0; v < M::kX; ++v) xv[v] = load_row<X, false>(x[n], k + v * 16 / (int)sizeof(typename X::E), (int)K);
-            g[n] = M::mma(wg, xv, g[n]);
-            u[n] = M::mma(wu, xv, u[n]);
-        }
-    }
-    // [wave][gate, up][entry][row]
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const int at = (n * kTile + lane % kTile) * kTile + sub * 4;
-        *reinterpret_cast<f32x4*>(parts + (2 * wave) * N * kTile * kTile + at) = g[n];
-        *reinterpret_cast<f32x4*>(parts + (2 * wave + 1) * N * kTile * kTile + at) = u[n];
-    }
-    __syncthreads();
-    for (int at = threadIdx.x; at < N * kTile * kTile; at += kUpWaves * kWave) {
-        const int i = first + at / kTile, r = tile + at % kTile;
         if (i >= count) continue;
-        float gs = 0.0f, us = 0.0f;
+        const int entry = list[i];
+        const float x_scale = scale_of<X>(a, entry);
+        f32x4 h;
 #pragma unroll
-        for (int w = 0; w < kUpWaves; ++w) {
-            gs += parts[(2 * w) * N * kTile * kTile + at];
-            us += parts[(2 * w + 1) * N * kTile * kTile + at];
+        for (int v = 0; v < 4; ++v) h[v] = hidden_of<X, W>(a, rank, local, row + v, x_scale, c[0][n][v], c[1][n][v]);
+        const int64_t to = (int64_t)entry * a.hidden_row + row;
+        if constexpr (sizeof(typename W::E) == 4) {
+            *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.hidden) + to) = h;
+        } else {
+            uint16_t hi[4], lo[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) two_bf16(h[v], hi + v, lo + v);
+            *reinterpret_cast<u16x4*>(reinterpret_cast<uint16_t*>(a.hidden) + to) = u16x4{hi[0], hi[1], hi[2], hi[3]};
+            *reinterpret_cast<u16x4*>(reinterpret_cast<uint16_t*>(a.hidden + a.hidden_plane) + to) = u16x4{lo[0], lo[1], lo[2], lo[3]};
+        }
+    }
+}
+
+// Where an entry's row of x begins.
+template <class X>
+__device__ __forceinline__ const uint8_t* row_of(const MoeArgs& a, int entry) {
+    int32_t at;
+    const int r = rank_at(a.entries, entry, &at);
+    return static_cast<const uint8_t*>(a.x[r]) + (int64_t)(at / a.top_k) * a.width * (int)sizeof(typename X::E);
+}
+// This lane's row of G and of U.
+template <class W>
+__device__ __forceinline__ void up_rows(const MoeArgs& a, int rank, int local, int tile, const uint8_t** w) {
+    const int64_t size = (int64_t)a.width * (int)sizeof(typename W::E), row = min(tile + lane_id() % kTile, a.inner - 1);
+    w[0] = static_cast<const uint8_t*>(a.gate_up[rank]) + ((int64_t)local * 2 * a.inner + row) * size;
+    w[1] = w[0] + a.inner * size;
+}
+// This lane's rows of D.
+template <class W, int Rows>
+__device__ __forceinline__ void down_rows(const MoeArgs& a, int rank, int local, int tile, const uint8_t** w) {
+    const int64_t size = (int64_t)a.inner * (int)sizeof(typename W::E);
+#pragma unroll
+    for (int r = 0; r < Rows; ++r)
+        w[r] = static_cast<const uint8_t*>(a.down[rank]) + ((int64_t)local * a.width + min(tile + r * kTile + lane_id() % kTile, a.width - 1)) * size;
+}
+
+// G x and U x of N tiles of entries through LDS, a tile of rows of each a wave.
+template <class X, class W, int N>
+__device__ __forceinline__ void up_many(const MoeArgs& a, int expert, const uint16_t* list, int first, int count, uint8_t* lds) {
+    using M = Up<X, W>;
+    using S = Stage<M::kX * 64, 1, N>;
+    constexpr int Rows = 2, kSize = sizeof(typename X::E);
+    const int lane = lane_id(), sub = lane / kTile;
+    const int rank = expert / a.per_rank, local = expert - rank * a.per_rank;
+    const int tile = (blockIdx.x * kManyWaves + threadIdx.x / kWave) * kTile;
+    const int size = a.width * (int)sizeof(typename W::E);
+    const uint8_t* w[Rows];
+    up_rows<W>(a, rank, local, tile, w);
+    const uint8_t* src[S::kMine];
+#pragma unroll
+    for (int i = 0; i < S::kMine; ++i) {
+        const int row = (threadIdx.x + i * kManyThreads) / S::kUnits;
+        src[i] = row_of<X>(a, list[first + row < count ? first + row : 0]);
+    }
+    f32x4 c[Rows][N] = {};
+    staged_sums<M, Rows, N, S>(w, size, src, a.width * kSize, lds, c, [&](const uint8_t* from, int step, int n, typename M::Frag& f) {
+#pragma unroll
+        for (int v = 0; v < M::kX; ++v)
+            f.x[v] = *reinterpret_cast<const u32x4*>(from + (n * kTile + lane % kTile) * S::kRow + step * S::kPlane + (sub * M::kX + v) * 16);
+    });
+    write_hidden<X, W, N>(a, rank, local, list, first, count, tile, c);
+}
+
+// G x and U x for a tile of rows of each and N tiles of entries, the sums cut over
+// the workgroup's waves, then the hidden values.
+template <class X, class W, int N>
+__device__ __forceinline__ void up_tiles(const MoeArgs& a, int expert, const uint16_t* list, int first, int count, float* parts) {
+    using M = Up<X, W>;
+    constexpr int Rows = 2, kAhead = N == 4 ? 2 : 4;
+    const int lane = lane_id(), wave = threadIdx.x / kWave, sub = lane / kTile;
+    const int rank = expert / a.per_rank, local = expert - rank * a.per_rank;
+    const int tile = blockIdx.x * kTile;
+    const int size = a.width * (int)sizeof(typename W::E), x_size = a.width * (int)sizeof(typename X::E);
+    const uint8_t* w[Rows];
+    up_rows<W>(a, rank, local, tile, w);
+    const uint8_t* x[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {  // columns behind the last entry repeat the first, and are dropped
+        const int i = first + n * kTile + lane % kTile;
+        x[n] = row_of<X>(a, list[i < count ? i : 0]);
+    }
+    f32x4 c[Rows][N] = {};
+    int s0, s1;
+    part_of((size + 63) / 64, kAhead, &s0, &s1);
+    sums_of<M, Rows, N, kAhead>(w, s0, s1, size, c, [&](int n, int step, typename M::Frag& f, bool full) {
+        const int at = (step * 4 + sub) * M::kX * 16;
+#pragma unroll
+        for (int v = 0; v < M::kX; ++v) f.x[v] = full ? load_bytes(x[n] + at + v * 16) : load_end(x[n], at + v * 16, x_size);
+    });
+    // [wave][gate, up][entry][row]
+    constexpr int kPart = N * kTile * kTile;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < Rows; ++r)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            *reinterpret_cast<f32x4*>(parts + (2 * wave + r) * kPart + (n * kTile + lane % kTile) * kTile + sub * 4) = c[r][n];
+    __syncthreads();
+    for (int at = threadIdx.x; at < kPart; at += kThreads) {
+        const int i = first + at / kTile, row = tile + at % kTile;
+        if (i >= count) continue;
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            g += parts[(2 * v) * kPart + at];
+            u += parts[(2 * v + 1) * kPart + at];
         }
         const int entry = list[i];
-        float h = 0.0f;  // behind the last row: what the second product's sum ends on
-        if (r < a.inner) {
-            if constexpr (sizeof(typename W::E) == 1) {
-                const float* f = a.gate_up_scale[rank] + (int64_t)local * 2 * a.inner + r;
-                gs *= f[0];
-                us *= f[a.inner];
-            }
-            if constexpr (sizeof(typename X::E) == 1) {
-                int32_t t;
-                const int xr = rank_of(a.entries, entry, &t);
-                const float f = a.x_scale[xr][t / a.top_k];
-                gs *= f;
-                us *= f;
-            }
-            h = gs / (1.0f + expf(-gs)) * us;
-        }
-        const int64_t to = (int64_t)entry * a.hidden_row + r;
+        const float h = hidden_of<X, W>(a, rank, local, row, scale_of<X>(a, entry), g, u);
+        const int64_t to = (int64_t)entry * a.hidden_row + row;
         if constexpr (sizeof(typename W::E) == 4) {
             reinterpret_cast<float*>(a.hidden)[to] = h;
         } else {
@@ -283,34 +512,57 @@ __device__ __forceinline__ void up_tiles(const MoeArgs& a, int expert, const uin
     }
 }
 
-// blockIdx.x: kTile rows of the hidden layer; blockIdx.y: the n-th expert named.
-template <class X, class W>
-__global__ __launch_bounds__(kUpWaves * kWave) void moe_up_kernel(MoeArgs a) {
+// The blockIdx.y-th expert that entries name and its entries, in any order; -1 if
+// there are no more.  The first workgroup of each writes them for the second
+// kernel.  The whole workgroup of Threads calls.
+template <int Threads>
+__device__ __forceinline__ int find_expert(const MoeArgs& a, uint16_t* list, int* count) {
     __shared__ uint32_t words[kMaxWords];
-    __shared__ uint16_t list[RC_MAX_MOE_ENTRIES];
-    __shared__ int count;
-    __shared__ float parts[kUpWaves * 2 * 4 * kTile * kTile];
-    constexpr int kThreads = kUpWaves * kWave, kMost = RC_MAX_MOE_ENTRIES / kThreads;
+    __shared__ int many, before;
+    constexpr int kMost = RC_MAX_MOE_ENTRIES / Threads;
     const int32_t total = a.entries.total();
-    const int num_words = (a.num_experts + 31) / 32;
     if (threadIdx.x < kMaxWords) words[threadIdx.x] = 0;
-    if (threadIdx.x == 0) count = 0;
+    if (threadIdx.x == 0) many = before = 0;
     __syncthreads();
     int e[kMost];
 #pragma unroll
     for (int j = 0; j < kMost; ++j) {
-        const int32_t i = threadIdx.x + j * kThreads;
-        e[j] = i < total ? expert_of(a, i) : -1;
+        const int32_t i = threadIdx.x + j * Threads;
+        e[j] = -1;
+        if (j * Threads >= total) continue;
+        if (i < total) e[j] = expert_of(a, i);
         if (e[j] >= 0) atomicOr(&words[e[j] / 32], 1u << (e[j] % 32));
     }
     __syncthreads();
-    const int expert = nth_expert(words, num_words, blockIdx.y);
-    if (expert < 0) return;
+    const int expert = nth_expert(words, (a.num_experts + 31) / 32, blockIdx.y);
+    if (expert < 0) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) named_of(a)[blockIdx.y] = Named{-1, 0, 0, 0};
+        return -1;
+    }
 #pragma unroll
-    for (int j = 0; j < kMost; ++j)  // in any order
-        if (e[j] == expert) list[atomicAdd(&count, 1)] = (uint16_t)(threadIdx.x + j * kThreads);
+    for (int j = 0; j < kMost; ++j) {
+        if (j * Threads >= total) continue;
+        if (e[j] == expert) list[atomicAdd(&many, 1)] = (uint16_t)(threadIdx.x + j * Threads);
+        if (blockIdx.x == 0 && e[j] >= 0 && e[j] < expert) atomicAdd(&before, 1);
+    }
     __syncthreads();
-    const int n = __builtin_amdgcn_readfirstlane(count);
+    const int n = __builtin_amdgcn_readfirstlane(many);
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) named_of(a)[blockIdx.y] = Named{expert, before, n, 0};
+        for (int i = threadIdx.x; i < n; i += Threads) list_of(a)[before + i] = list[i];
+    }
+    *count = n;
+    return expert;
+}
+
+// blockIdx.x: a tile of rows of the hidden layer; blockIdx.y: the n-th expert named.
+template <class X, class W>
+__global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
+    __shared__ uint16_t list[RC_MAX_MOE_ENTRIES];
+    __shared__ __align__(16) float parts[kWaves * 2 * 4 * kTile * kTile];
+    int n;
+    const int expert = find_expert<kThreads>(a, list, &n);
+    if (expert < 0) return;
     if (n <= kTile) {
         up_tiles<X, W, 1>(a, expert, list, 0, n, parts);
     } else if (n <= 2 * kTile) {
@@ -320,173 +572,228 @@ __global__ __launch_bounds__(kUpWaves * kWave) void moe_up_kernel(MoeArgs a) {
     }
 }
 
-// One part of D times the hidden values of N tiles of an expert's entries, into
-// `sums` ([entry][row]).
+// Tiles of entries at most that a wave has registers for.
+template <class W>
+constexpr int kDownMost = Down<W>::kH == 2 ? 4 : 8;
+
+// blockIdx.x: kManyWaves tiles of rows.
+template <class X, class W>
+__global__ __launch_bounds__(kManyThreads) void moe_up_many_kernel(MoeArgs a) {
+    using M = Up<X, W>;
+    __shared__ uint16_t list[RC_MAX_MOE_ENTRIES];
+    __shared__ __align__(16) uint8_t lds[2 * Stage<M::kX * 64, 1, 8>::kSize];
+    int n;
+    const int expert = find_expert<kManyThreads>(a, list, &n);
+    if (expert < 0) return;
+    if (n <= kTile) {
+        up_many<X, W, 1>(a, expert, list, 0, n, lds);
+    } else if (n <= 2 * kTile) {
+        up_many<X, W, 2>(a, expert, list, 0, n, lds);
+    } else if (n <= 4 * kTile) {
+        up_many<X, W, 4>(a, expert, list, 0, n, lds);
+    } else {
+        for (int first = 0; first < n; first += 8 * kTile) up_many<X, W, 8>(a, expert, list, first, n, lds);
+    }
+}
+
+// This lane's rows of D times the hidden values of its entries.
+template <class W, int Rows, int N>
+__device__ __forceinline__ void write_products(const MoeArgs& a, int rank, int local, int tile, const int (&entry)[N], f32x4 (&c)[Rows][N]) {
+    const int sub = lane_id() / kTile;
+#pragma unroll
+    for (int r = 0; r < Rows; ++r) {
+        const int at = tile + r * kTile + sub * 4;
+        if (at >= a.width) continue;
+        if constexpr (sizeof(typename W::E) == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float scale = a.down_scale[rank][(int64_t)local * a.width + min(at + i, a.width - 1)];
+#pragma unroll
+                for (int n = 0; n < N; ++n) c[r][n][i] *= scale;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n)  // a row of products has room for whole tiles
+            if (entry[n] >= 0) *reinterpret_cast<f32x4*>(a.products + (int64_t)entry[n] * a.product_row + at) = c[r][n];
+    }
+}
+
+// D times the hidden values of N tiles of an expert's entries, for two tiles of
+// rows, the sums cut over the workgroup's waves.
 template <class W, int N>
-__device__ __forceinline__ void down_tiles(const MoeArgs& a, int expert, const uint16_t* list, int first, int count, int s0, int s1,
-                                           float* sums) {
+__device__ __forceinline__ void down_tiles(const MoeArgs& a, const Named& e, int first, float* parts) {
     using M = Down<W>;
-    constexpr int kAhead = N == 4 ? 2 : N == 2 ? 4 : 8;
+    constexpr int Rows = 2, kAhead = M::kH == 2 ? 4 / N : N == 4 ? 2 : 4;
     const int lane = lane_id(), sub = lane / kTile;
-    const int rank = expert / a.per_rank, local = expert - rank * a.per_rank;
-    const int tile = blockIdx.x * kTile, row = min(tile + lane % kTile, a.width - 1);
-    const int64_t K = a.inner;
-    const typename W::E* down = (const typename W::E*)a.down[rank] + ((int64_t)local * a.width + row) * K;
+    const int rank = e.expert / a.per_rank, local = e.expert - rank * a.per_rank;
+    const int wave = threadIdx.x / kWave, tile = blockIdx.x * Rows * kTile;
+    const int size = a.inner * (int)sizeof(typename W::E);
+    const uint8_t* w[Rows];
+    down_rows<W, Rows>(a, rank, local, tile, w);
+    const uint16_t* list = list_of(a) + e.first;
     const uint8_t* h[N];
     int entry[N];
     constexpr int kSize = M::kWide ? 4 : 2;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const int i = first + n * kTile + lane % kTile;
-        entry[n] = i < count ? list[i] : -1;
-        h[n] = a.hidden + ((int64_t)list[i < count ? i : 0] * a.hidden_row + sub * (M::kK / 4)) * kSize;
+        entry[n] = i < e.count ? list[i] : -1;
+        h[n] = a.hidden + ((int64_t)list[i < e.count ? i : 0] * a.hidden_row + sub * (M::kK / 4)) * kSize;
     }
-    f32x4 c[N] = {};
-    const int full = min(s1, (int)K / M::kK), mine = sub * (M::kK / 4);
-    int s = s0;
-    auto hidden = [&](int n, int step, u32x4* hi, u32x4* lo) {
+    f32x4 c[Rows][N] = {};
+    int s0, s1;
+    part_of((size + 63) / 64, kAhead, &s0, &s1);
+    sums_of<M, Rows, N, kAhead>(w, s0, s1, size, c, [&](int n, int step, typename M::Frag& f, bool) {
 #pragma unroll
         for (int v = 0; v < M::kH; ++v) {
-            const uint8_t* p = h[n] + (int64_t)step * M::kK * kSize + v * 16;
-            hi[v] = *reinterpret_cast<const u32x4*>(p);
-            if constexpr (!M::kWide) lo[v] = *reinterpret_cast<const u32x4*>(p + a.hidden_plane);
+            const uint8_t* p = h[n] + step * M::kK * kSize + v * 16;
+            f.hi[v] = *reinterpret_cast<const u32x4*>(p);
+            if constexpr (!M::kWide) f.lo[v] = *reinterpret_cast<const u32x4*>(p + a.hidden_plane);
         }
-    };
-    for (; s + kAhead <= full; s += kAhead) {
-        u32x4 w[kAhead], hi[kAhead][N][M::kH], lo[kAhead][N][M::kH];
+    });
+    constexpr int kPart = Rows * N * kTile * kTile;
+    __syncthreads();
+    if (wave > 0) {
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) w[j] = load_row<W, true>(down, (s + j) * M::kK + mine, 0);
+        for (int r = 0; r < Rows; ++r)
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-            for (int n = 0; n < N; ++n) hidden(n, s + j, hi[j][n], lo[j][n]);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-            for (int n = 0; n < N; ++n) c[n] = M::mma(w[j], hi[j][n], lo[j][n], c[n]);
+            for (int n = 0; n < N; ++n)
+                *reinterpret_cast<f32x4*>(parts + (wave - 1) * kPart + ((r * N + n) * kWave + lane) * 4) = c[r][n];
     }
-    for (; s < s1; ++s) {
-        const u32x4 w = load_row<W, false>(down, s * M::kK + mine, (int)K);
+    __syncthreads();
+    if (wave > 0) return;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            u32x4 hi[M::kH], lo[M::kH];
-            hidden(n, s, hi, lo);
-            c[n] = M::mma(w, hi, lo, c[n]);
-        }
-    }
-    f32x4 scale = {1, 1, 1, 1};
-    if constexpr (sizeof(typename W::E) == 1) {
+    for (int r = 0; r < Rows; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) scale[i] = a.down_scale[rank][(int64_t)local * a.width + min(tile + sub * 4 + i, a.width - 1)];
-    }
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-        if (entry[n] >= 0) *reinterpret_cast<f32x4*>(sums + entry[n] * kTile + sub * 4) = c[n] * scale;
+            for (int v = 0; v < kWaves - 1; ++v) c[r][n] += *reinterpret_cast<f32x4*>(parts + v * kPart + ((r * N + n) * kWave + lane) * 4);
+    write_products<W, Rows, N>(a, rank, local, tile, entry, c);
 }
 
-// blockIdx.x: kTile columns of the output, for all tokens.
-template <class W>
-__global__ __launch_bounds__(kDownWaves * kWave) void moe_down_kernel(MoeArgs a) {
-    extern __shared__ float sums[];  // [part][entry][column]
-    __shared__ int start[RC_MAX_EXPERTS];
-    __shared__ int many[RC_MAX_EXPERTS];
-    __shared__ uint16_t list[RC_MAX_MOE_ENTRIES], named[RC_MAX_EXPERTS];
-    __shared__ int carry[2][kDownWaves];
-    constexpr int kThreads = kDownWaves * kWave, kMost = RC_MAX_MOE_ENTRIES / kThreads, kEach = RC_MAX_EXPERTS / kThreads;
-    const int32_t total = a.entries.total();
-    const int lane = lane_id(), wave = threadIdx.x / kWave;
-    // a counting sort of the entries by their expert
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) many[threadIdx.x + j * kThreads] = 0;
-    __syncthreads();
-    int e[kMost];
-#pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-        const int32_t i = threadIdx.x + j * kThreads;
-        e[j] = i < total ? expert_of(a, i) : -1;
-        if (e[j] >= 0) atomicAdd(&many[e[j]], 1);
-    }
-    __syncthreads();
-    int own[kEach], sum = 0, some = 0;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-        own[j] = many[threadIdx.x * kEach + j];
-        sum += own[j];
-        some += own[j] > 0;
-    }
-    int before = sum, first = some;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const int v = __shfl_up(before, d), w = __shfl_up(first, d);
-        if (lane >= d) before += v, first += w;
-    }
-    if (lane == kWave - 1) carry[0][wave] = before, carry[1][wave] = first;
-    __syncthreads();
-    int experts = 0;
-#pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) {
-        if (w < wave) before += carry[0][w], first += carry[1][w];
-        experts += carry[1][w];
-    }
-    before -= sum;
-    first -= some;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-        start[threadIdx.x * kEach + j] = before;
-        before += own[j];
-        if (own[j]) named[first++] = (uint16_t)(threadIdx.x * kEach + j);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kMost; ++j)  // within an expert in any order; start ends as each expert's end
-        if (e[j] >= 0) list[atomicAdd(&start[e[j]], 1)] = (uint16_t)(threadIdx.x + j * kThreads);
-    __syncthreads();
-    // experts, or parts of their sums where they are few, to the waves in turn
+// The same through LDS, two tiles of rows a wave.
+template <class W, int N>
+__device__ __forceinline__ void down_many(const MoeArgs& a, const Named& e, int first, uint8_t* lds) {
     using M = Down<W>;
-    const int steps = (a.inner + M::kK - 1) / M::kK;
-    const int splits = experts ? max(1, min(min(a.splits, steps), (4 * kDownWaves + experts - 1) / experts)) : 1;
-    const int each = (steps + splits - 1) / splits;
-    for (int item = wave; item < experts * splits; item += kDownWaves) {
-        const int expert = __builtin_amdgcn_readfirstlane(named[item / splits]), part = item % splits;
-        const int n = __builtin_amdgcn_readfirstlane(many[expert]), s0 = part * each, s1 = min(s0 + each, steps);
-        const uint16_t* mine = list + start[expert] - n;
-        float* to = sums + part * total * kTile;
-        if (n <= kTile) {
-            down_tiles<W, 1>(a, expert, mine, 0, n, s0, s1, to);
-        } else if (n <= 2 * kTile) {
-            down_tiles<W, 2>(a, expert, mine, 0, n, s0, s1, to);
-        } else {
-            for (int f = 0; f < n; f += 4 * kTile) down_tiles<W, 4>(a, expert, mine, f, n, s0, s1, to);
-        }
+    constexpr int Rows = 2, kPlanes = M::kWide ? 1 : 2, kSize = M::kWide ? 4 : 2;
+    using S = Stage<64 * M::kH * kPlanes, kPlanes, N>;
+    const int lane = lane_id(), sub = lane / kTile;
+    const int rank = e.expert / a.per_rank, local = e.expert - rank * a.per_rank;
+    const int tile = (blockIdx.x * kManyWaves + threadIdx.x / kWave) * Rows * kTile;
+    const int size = a.inner * (int)sizeof(typename W::E);
+    const uint8_t* w[Rows];
+    down_rows<W, Rows>(a, rank, local, tile, w);
+    const uint16_t* list = list_of(a) + e.first;
+    int entry[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int i = first + n * kTile + lane % kTile;
+        entry[n] = i < e.count ? list[i] : -1;
     }
-    __syncthreads();
-    const int tokens = total / a.top_k;
-    for (int at = threadIdx.x; at < tokens * kTile; at += kThreads) {
-        const int token = at / kTile, column = blockIdx.x * kTile + at % kTile;
-        if (column >= a.width) continue;
-        int32_t local;
-        const int rank = rank_of(a.entries, token * a.top_k, &local);
-        float y = 0.0f;
-        for (int k = 0; k < a.top_k; ++k) {
-            const int x = a.experts[rank][local + k];
-            if (x < 0 || x >= a.num_experts) continue;
-            float v = 0.0f;
-            for (int p = 0; p < splits; ++p) v += sums[(p * total + token * a.top_k + k) * kTile + at % kTile];
-            y = __builtin_fmaf(a.weights[rank][local + k], v, y);
+    const uint8_t* src[S::kMine];
+#pragma unroll
+    for (int k = 0; k < S::kMine; ++k) {
+        const int row = (threadIdx.x + k * kManyThreads) / S::kUnits, i = first + row % (N * kTile);
+        src[k] = a.hidden + row / (N * kTile) * a.hidden_plane + (int64_t)list[i < e.count ? i : 0] * a.hidden_row * kSize;
+    }
+    f32x4 c[Rows][N] = {};
+    staged_sums<M, Rows, N, S>(w, size, src, a.hidden_row * kSize, lds, c, [&](const uint8_t* from, int step, int n, typename M::Frag& f) {
+#pragma unroll
+        for (int v = 0; v < M::kH; ++v) {
+            const uint8_t* p = from + (n * kTile + lane % kTile) * S::kRow + step * S::kPlane + (sub * M::kH + v) * 16;
+            f.hi[v] = *reinterpret_cast<const u32x4*>(p);
+            if constexpr (!M::kWide) f.lo[v] = *reinterpret_cast<const u32x4*>(p + N * kTile * S::kRow);
         }
-        const int64_t to = (int64_t)(local / a.top_k) * a.width + column;
-        if (a.out_dtype == RC_F32) static_cast<float*>(a.y[rank])[to] = y;
-        else if (a.out_dtype == RC_F16) static_cast<F16::E*>(a.y[rank])[to] = F16::store(y);
-        else static_cast<BF16::E*>(a.y[rank])[to] = BF16::store(y);
+    });
+    write_products<W, Rows, N>(a, rank, local, tile, entry, c);
+}
+
+// blockIdx.x: two tiles of output columns; blockIdx.y: the n-th expert named.
+template <class W>
+__global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
+    __shared__ __align__(16) float parts[(kWaves - 1) * 2 * 4 * kTile * kTile];
+    const Named e = named_of(a)[blockIdx.y];
+    if (e.expert < 0) return;
+    if (e.count <= kTile) {
+        down_tiles<W, 1>(a, e, 0, parts);
+    } else if (e.count <= 2 * kTile) {
+        down_tiles<W, 2>(a, e, 0, parts);
+    } else {
+        for (int first = 0; first < e.count; first += 4 * kTile) down_tiles<W, 4>(a, e, first, parts);
     }
 }
 
+// blockIdx.x: kManyWaves times two tiles of output columns.
+template <class W>
+__global__ __launch_bounds__(kManyThreads) void moe_down_many_kernel(MoeArgs a) {
+    using M = Down<W>;
+    constexpr int kMost = kDownMost<W>;
+    __shared__ __align__(16) uint8_t lds[2 * Stage<64 * M::kH * (M::kWide ? 1 : 2), M::kWide ? 1 : 2, kMost>::kSize];
+    const Named e = named_of(a)[blockIdx.y];
+    if (e.expert < 0) return;
+    if (e.count <= kTile) {
+        down_many<W, 1>(a, e, 0, lds);
+    } else if (e.count <= 2 * kTile) {
+        down_many<W, 2>(a, e, 0, lds);
+    } else if (e.count <= 4 * kTile) {
+        down_many<W, 4>(a, e, 0, lds);
+    } else {
+        for (int first = 0; first < e.count; first += kMost * kTile) down_many<W, kMost>(a, e, first, lds);
+    }
+}
+
+// Four columns of a token: the weighted sum of its experts' products, in order.
+__global__ __launch_bounds__(kThreads) void moe_join_kernel(MoeArgs a) {
+    const int token = blockIdx.y, column = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (column >= a.width) return;
+    int32_t local;
+    const int rank = rank_at(a.entries, token * a.top_k, &local);
+    f32x4 y = {0, 0, 0, 0};
+    constexpr int kAhead = 8;
+    for (int k0 = 0; k0 < a.top_k; k0 += kAhead) {
+        bool named[kAhead];
+        float f[kAhead];
+        f32x4 v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int k = min(k0 + j, a.top_k - 1), x = a.experts[rank][local + k];
+            named[j] = k0 + j < a.top_k && x >= 0 && x < a.num_experts;
+            f[j] = a.weights[rank][local + k];
+            // there whether an expert is named or not
+            v[j] = *reinterpret_cast<const f32x4*>(a.products + (int64_t)(token * a.top_k + k) * a.product_row + column);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = named[j] ? __builtin_fmaf(f[j], v[j][i], y[i]) : y[i];
+    }
+    const int64_t to = (int64_t)(local / a.top_k) * a.width + column;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (column + i >= a.width) continue;
+        if (a.out_dtype == RC_F32) static_cast<float*>(a.y[rank])[to + i] = y[i];
+        else if (a.out_dtype == RC_F16) static_cast<F16::E*>(a.y[rank])[to + i] = F16::store(y[i]);
+        else static_cast<BF16::E*>(a.y[rank])[to + i] = BF16::store(y[i]);
+    }
+}
+
+unsigned groups(int64_t n, int of) { return (unsigned)((n + of - 1) / of); }
+
+// Through LDS where an expert has two entries or more on the average: waves that
+// share their entries then read them once (64 tokens on 8 of 64 experts each, 8-bit
+// weights: 279 us, and 352 without; 256 tokens, bfloat16: 545 and 892), but wait for
+// each other (one token: 118 us, and 73 without).  Rows have to hold one step.
 template <class X, class W>
 int run(const MoeArgs& a, hipStream_t s) {
-    const int experts = a.num_experts < a.entries.total() ? a.num_experts : a.entries.total();
-    moe_up_kernel<X, W><<<dim3(a.hidden_row / kTile, experts), kUpWaves * kWave, 0, s>>>(a);
-    const size_t lds = (size_t)a.splits * a.entries.total() * kTile * sizeof(float);
-    moe_down_kernel<W><<<(a.width + kTile - 1) / kTile, kDownWaves * kWave, lds, s>>>(a);
+    const int total = a.entries.total(), experts = min(a.num_experts, total);
+    if (total >= 2 * experts && a.width >= 64 && a.inner >= 64) {
+        moe_up_many_kernel<X, W><<<dim3(groups(a.hidden_row, kManyWaves * kTile), experts), kManyThreads, 0, s>>>(a);
+        moe_down_many_kernel<W><<<dim3(groups(a.width, kManyWaves * 2 * kTile), experts), kManyThreads, 0, s>>>(a);
+    } else {
+        moe_up_kernel<X, W><<<dim3(a.hidden_row / kTile, experts), kThreads, 0, s>>>(a);
+        moe_down_kernel<W><<<dim3(groups(a.width, 2 * kTile), experts), kThreads, 0, s>>>(a);
+    }
+    moe_join_kernel<<<dim3(groups(a.width, 4 * kThreads), total / a.top_k), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 

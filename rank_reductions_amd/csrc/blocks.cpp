@@ -73,10 +73,10 @@ Error check_moe(const char* what, int R, const rc_moe_desc* d, MoeArgs* a, int64
     a->out_dtype = d->out_dtype;
     a->hidden_row = (int32_t)((d->inner + 63) / 64 * 64);
     a->hidden_plane = n * a->hidden_row * 2;
-    // parts enough to keep a workgroup's waves busy where few experts can be named, as far as their sums fit LDS
-    const int64_t experts = std::max<int64_t>(1, std::min<int64_t>(n, d->num_experts));
-    a->splits = (int32_t)std::max<int64_t>(1, std::min((32 + experts - 1) / experts, RC_MAX_MOE_ENTRIES / std::max<int64_t>(1, n)));
-    *workspace = n * a->hidden_row * 4;
+    a->product_row = (int32_t)((d->width + 15) / 16 * 16);
+    // the hidden values, the products, the lists
+    const int64_t experts = std::min<int64_t>(n, d->num_experts);
+    *workspace = n * (a->hidden_row + a->product_row) * 4 + experts * 16 + (n * 2 + 15) / 16 * 16;
     return {};
 }
 
@@ -351,7 +351,10 @@ int rc_moe_layer(const rc_moe_desc* desc, const void* const* xs, const float* co
             a.y[r] = ys[r];
         }
         RC_TRY(b.check());
+        const int64_t n = a.entries.total();
         a.hidden = static_cast<uint8_t*>(workspace);
+        a.products = reinterpret_cast<float*>(a.hidden + n * a.hidden_row * 4);
+        a.lists = reinterpret_cast<uint8_t*>(a.products + n * a.product_row);
         if (validate_only || !a.entries.total()) return {};
         return device_run([&] { return launch_moe(a, desc->dtype, desc->weight_dtype, stream); });
     });

@@ -64,14 +64,16 @@ struct MoeArgs {
     RankSpans entries;       // (token, k) of all ranks
     uint8_t* hidden;         // silu(G x) * (U x) of every entry: [entries][hidden_row], float32, or bfloat16 twice
     int64_t hidden_plane;    // bytes of all entries' first bfloat16 numbers
+    float* products;         // D times the hidden values: [entries][product_row]
+    uint8_t* lists;          // the experts named, and their entries
     int32_t hidden_row;      // elements, a multiple of 64
+    int32_t product_row;     // elements, a multiple of 16
     int32_t num_experts;
     int32_t per_rank;
     int32_t top_k;
     int32_t width;
     int32_t inner;
     int32_t out_dtype;
-    int32_t splits;          // parts of a sum over inner at most
 };
 static_assert(sizeof(MoeArgs) <= 4096, "kernel arguments");
 int launch_moe(const MoeArgs& a, int dtype, int weight_dtype, void* stream);

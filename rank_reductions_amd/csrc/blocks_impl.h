@@ -50,6 +50,20 @@ __device__ __forceinline__ float wave_max(float v) {
     return fmaxf(fmaxf(of_lane(v, 0), of_lane(v, 16)), fmaxf(of_lane(v, 32), of_lane(v, 48)));
 }
 
+// rank_of without a loop: spans past the last rank begin at the total.
+__device__ __forceinline__ int rank_at(const RankSpans& s, int32_t i, int32_t* local) {
+    int r = 0;
+    int32_t base = 0;
+#pragma unroll
+    for (int k = 1; k < kMaxRanks; ++k) {
+        const bool past = i >= s.first[k];
+        r = past ? k : r;
+        base = past ? s.first[k] : base;
+    }
+    *local = i - base;
+    return r;
+}
+
 // Four values as e4m3, to nearest even.
 __device__ __forceinline__ uint32_t e4m3_of(float a, float b, float c, float d) {
     int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);

@@ -151,19 +151,30 @@ def test_values_beyond_float16():
         check(ys, i, "f16")
 
 
-def test_a_token_alone_and_among_others():
-    """Bit for bit: what a token gives does not hang on the others, or on the rank that holds it."""
+@pytest.mark.parametrize("shape", [([60, 3], 3, 2, 130, 96), ([150], 2, 1, 200, 70), ([301], 2, 1, 65, 129), ([90, 90, 90], 3, 3, 1000, 67)], ids=str)
+@pytest.mark.parametrize("kind", KINDS, ids="-".join)
+def test_experts_with_many_entries(shape, kind):
+    """Tens and hundreds of entries to an expert: four and eight tiles of them, and more than one pass."""
+    counts, experts, top_k, width, inner = shape
+    i = inputs(counts, experts, top_k, width, inner, kind[0], kind[1], 19, padding=0.1)
+    with session(len(counts)):
+        ys = rr.moe_layer(**on_gpu(i), dtype=TYPES[kind[2]])
+        torch.cuda.synchronize()
+        check(ys, i, kind[2])
+
+
+def test_a_token_among_others():
+    """Bit for bit: what a token gives does not hang on which others there are, where there are enough for experts
+    to have two entries on the average."""
     for kind in (("bf16", "bf16"), ("e4m3", "e4m3")):
-        i = inputs([30], 8, 8, 192, 96, *kind, 13)
-        one = dict(i, **{k: [i[k][0][11:12]] for k in ("xs", "weights", "experts")})
+        i = inputs([60], 8, 8, 192, 96, *kind, 13)
+        some = dict(i, **{k: [i[k][0][11:14].contiguous()] for k in ("xs", "weights", "experts")})
         if i["scales"] is not None:
-            one["scales"] = [i["scales"][0][11:12]]
+            some["scales"] = [i["scales"][0][11:14].contiguous()]
         with session(1):
-            a, b = rr.moe_layer(**on_gpu(i)), rr.moe_layer(**on_gpu(one))
+            a, b = rr.moe_layer(**on_gpu(i)), rr.moe_layer(**on_gpu(some))
             torch.cuda.synchronize()
-            # the sums over inner are cut into as many parts as keep the waves busy, which hangs on the number of experts
-            # named: all eight here, both times
-            assert torch.equal(a[0][11], b[0][0])
+            assert torch.equal(a[0][11:14], b[0])
 
 
 def test_graph_replays():
