@@ -89,10 +89,10 @@ __global__ __launch_bounds__(Waves == 1 ? 256 : Waves * kWave) void rms_norm_ker
     __shared__ float joined[2][Waves];
     constexpr int kThreads = Waves * kWave, N = T::n;
     const int at = Waves == 1 ? lane_id() : threadIdx.x;
-    const int64_t row = Waves == 1 ? group_index() * (256 / kWave) + threadIdx.x / kWave : group_index();
+    const int64_t row = Waves == 1 ? group_index() * (256 / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) : group_index();
     if (row >= a.tokens.total()) return;
     int32_t t;
-    const int rank = rank_of(a.tokens, (int32_t)row, &t);
+    const int rank = rank_at(a.tokens, (int32_t)row, &t);
     const int64_t width = a.width, from = t * width;
     u32x4 raw[V], more[V];
 #pragma unroll
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(Waves == 1 ? 256 : Waves * kWave) void rms_norm_gra
     __shared__ float rows[kRows == 1 ? 1 : 3 * kWave * V * N];
     const int at = Waves == 1 ? lane_id() : threadIdx.x, wave = threadIdx.x / kWave;
     int32_t part;
-    const int rank = rank_of(a.parts, (int32_t)blockIdx.x, &part);
+    const int rank = rank_at(a.parts, (int32_t)blockIdx.x, &part);
     const int32_t parts = a.parts.first[rank + 1] - a.parts.first[rank];
     const int32_t tokens = a.tokens.first[rank + 1] - a.tokens.first[rank];
     const int64_t width = a.width;
@@ -275,17 +275,21 @@ int run_norm(const NormArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// One wave holds up to 4096 16-bit elements (2048 of 32 bits), four or sixteen
-// waves longer rows.
+// Short rows take a wave each, longer ones four to sixteen waves with a few
+// vectors a lane (16384 rows of 4096 bf16: 84 us with four waves of two vectors,
+// 105 with one of eight; 64 rows: 4.4 and 7.6 us), in steps that leave few lanes idle.
 template <class T, class W>
 int norm_of(const NormArgs& a, hipStream_t s) {
     const int64_t vectors = (a.width + T::n - 1) / T::n;
     if (vectors <= 64) return run_norm<T, W, 1, 1>(a, s);
     if (vectors <= 128) return run_norm<T, W, 1, 2>(a, s);
-    if (vectors <= 256) return run_norm<T, W, 1, 4>(a, s);
-    if (vectors <= 512) return run_norm<T, W, 1, 8>(a, s);
+    if (vectors <= 256) return run_norm<T, W, 4, 1>(a, s);
+    if (vectors <= 512) return run_norm<T, W, 4, 2>(a, s);
+    if (vectors <= 768) return run_norm<T, W, 4, 3>(a, s);
     if (vectors <= 1024) return run_norm<T, W, 4, 4>(a, s);
-    if (vectors <= 2048) return run_norm<T, W, 4, 8>(a, s);
+    if (vectors <= 1536) return run_norm<T, W, 8, 3>(a, s);
+    if (vectors <= 2048) return run_norm<T, W, 8, 4>(a, s);
+    if (vectors <= 3072) return run_norm<T, W, 16, 3>(a, s);
     if constexpr (T::n == 4)
         if (vectors > 4096) return run_norm<T, W, 16, 8>(a, s);
     return run_norm<T, W, 16, 4>(a, s);
@@ -305,7 +309,8 @@ int grad_of(const NormArgs& a, hipStream_t s) {
     const int64_t vectors = (a.width + T::n - 1) / T::n;
     if (vectors <= 64) return run_grad<T, W, 1, 1>(a, s);
     if (vectors <= 128) return run_grad<T, W, 1, 2>(a, s);
-    if (vectors <= 512) return run_grad<T, W, 4, 2>(a, s);
+    if (vectors <= 256) return run_grad<T, W, 4, 1>(a, s);
+    if (vectors <= 512) return run_grad<T, W, 8, 1>(a, s);
     if (vectors <= 1024) return run_grad<T, W, 8, 2>(a, s);
     if (vectors <= 2048) return run_grad<T, W, 16, 2>(a, s);
     if constexpr (T::n == 4)
