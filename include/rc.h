@@ -570,8 +570,8 @@ int rc_rms_norm_grad(const rc_norm_desc* desc, const void* const* d_ys, const vo
                      void* workspace, int64_t workspace_bytes, void* stream);
 
 /* A mixture-of-experts layer for a few tokens: what a dispatch, the experts'
- * products and a combine give, in two kernels that read the chosen experts'
- * weights once, where they lie.  struct_size = sizeof(rc_moe_desc).
+ * products and a combine give, by kernels that read the chosen experts'
+ * weights where they lie, once for every 64 to 128 entries of an expert.  struct_size = sizeof(rc_moe_desc).
  *   dtype         of the rows xs: RC_F32, RC_F16, RC_BF16 or RC_E4M3
  *   weight_dtype  dtype, or RC_E4M3 (not with RC_F32)
  *   out_dtype     of ys: dtype; with RC_E4M3 rows RC_F32, RC_F16 or RC_BF16
@@ -607,8 +607,9 @@ typedef struct rc_moe_desc {
  *               [E/R, 2 * inner] float32 with RC_E4M3 weights, a factor of each
  *               row, else NULL
  *   down[d]     [E/R, width, inner]; down_scales[d] [E/R, width] likewise
- * Sums are float32.  silu(G x) * (U x) is held in float32, or as two bfloat16
- * numbers whose sum is within 2^-16 of it; ys are rounded once. */
+ * Sums are float32, in an order that depends on the sizes (tokens, top_k,
+ * num_experts, width, inner) alone.  silu(G x) * (U x) is held in float32, or as
+ * two bfloat16 numbers whose sum is within 2^-16 of it; ys are rounded once. */
 int rc_moe_layer_workspace(const rc_moe_desc* desc, int64_t* bytes);
 int rc_moe_layer(const rc_moe_desc* desc, const void* const* xs, const float* const* scales,
                  const int32_t* const* experts, const float* const* weights, const void* const* gate_up,

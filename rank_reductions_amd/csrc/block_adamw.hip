@@ -78,6 +78,9 @@ __device__ __forceinline__ void values_of(uint32_t c, float scale, float* f) {
     f[3] = hi[1] * scale;
 }
 
+__device__ __forceinline__ const void* address_of(uint64_t tagged) { return reinterpret_cast<const void*>(tagged & 0xffffffffffffffull); }
+__device__ __forceinline__ int type_of(uint64_t tagged) { return (int)(tagged >> 56); }
+
 // ---------------------------------------------------------------- gradient norms
 
 constexpr int kThreads = 256;
@@ -124,9 +127,10 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(GradNormArgs a) {
         if (a.first[mid] <= chunk) lo = mid;
         else hi = mid - 1;
     }
-    const int64_t from = (int64_t)(chunk - a.first[lo]) * kNormChunk, to = min(a.count[lo], from + kNormChunk);
-    double sum = a.dtype[lo] == RC_F32 ? squares<F32>(a.grad[lo], from, to)
-               : a.dtype[lo] == RC_F16 ? squares<F16>(a.grad[lo], from, to) : squares<BF16>(a.grad[lo], from, to);
+    const int64_t from = (int64_t)(chunk - a.first[lo]) * kNormChunk, to = min((int64_t)a.count[lo], from + kNormChunk);
+    const void* grad = address_of(a.grad[lo]);
+    const int type = type_of(a.grad[lo]);
+    double sum = type == RC_F32 ? squares<F32>(grad, from, to) : type == RC_F16 ? squares<F16>(grad, from, to) : squares<BF16>(grad, from, to);
     sum = join_sum(sum);
     if (threadIdx.x == 0) a.partial[chunk] = sum;
 }
@@ -135,7 +139,15 @@ __global__ __launch_bounds__(kThreads) void grad_norm_join_kernel(GradNormJoin a
     const int rank = blockIdx.x;
     const int64_t from = a.over_all ? 0 : a.first[rank], to = a.over_all ? a.first[a.nranks] : a.first[rank + 1];
     double sum = 0.0;
-    for (int64_t i = from + threadIdx.x; i < to; i += kThreads) sum += a.partial[i];
+    int64_t i = from + threadIdx.x;
+    for (; i + 7 * kThreads < to; i += 8 * kThreads) {
+        double v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = a.partial[i + j * kThreads];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += v[j];
+    }
+    for (; i < to; i += kThreads) sum += a.partial[i];
     sum = join_sum(sum);
     if (threadIdx.x == 0) a.norms[rank] = (float)sqrt(sum);
 }
@@ -189,6 +201,7 @@ template <class P, class G, int Bits, bool Full>
 __device__ __forceinline__ void step_chunk(const AdamwArgs& a, const AdamwEntry& e, const AdamwEntry& o, const void* grad,
                                            const AdamwFactors& c, int64_t from, int64_t to) {
     constexpr int kAhead = 2, kRound = 4 * kThreads;
+    static_assert(kAdamwLeast % (kAhead * kRound) == 0, "whole rounds");
     for (int64_t base = from; base < to; base += kRound * kAhead) {
         float p[kAhead][4], g[kAhead][4], m[kAhead][4], v[kAhead][4];
         uint32_t mc[kAhead], vc[kAhead];
@@ -275,7 +288,7 @@ __device__ __forceinline__ void copy_chunk(const void* src, void* dst, int64_t f
 template <class P, class G, int Bits>
 __device__ __forceinline__ void step_any(const AdamwArgs& a, const AdamwEntry& e, const AdamwEntry& o, const void* grad,
                                          const AdamwFactors& c, int64_t from) {
-    if (from + kAdamwChunk <= e.count) step_chunk<P, G, Bits, true>(a, e, o, grad, c, from, from + kAdamwChunk);
+    if (from + a.chunk <= e.count) step_chunk<P, G, Bits, true>(a, e, o, grad, c, from, from + a.chunk);
     else step_chunk<P, G, Bits, false>(a, e, o, grad, c, from, e.count);
 }
 
@@ -288,13 +301,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs a) {
     const AdamwEntry& e = reinterpret_cast<const AdamwEntry*>(table + a.entries_at)[t];
     const AdamwEntry& o = reinterpret_cast<const AdamwEntry*>(reinterpret_cast<const uint8_t*>(a.out) + a.entries_at)[t];
     const AdamwFactors c = a.table->factors[e.rank];
-    const int64_t from = (a.first_chunk + chunk - e.first_chunk) * kAdamwChunk;
-    const uint64_t tagged = a.grad[t - a.first];
-    const void* grad = reinterpret_cast<const void*>(tagged & 0xffffffffffffffull);
-    const int type = (int)(tagged >> 56);
+    const int64_t from = (a.first_chunk + chunk - e.first_chunk) * a.chunk;
+    const void* grad = address_of(a.grad[t - a.first]);
+    const int type = type_of(a.grad[t - a.first]);
     if (c.skip || !grad) {
         if (a.out == a.table) return;
-        const int64_t to = min(e.count, from + kAdamwChunk);
+        const int64_t to = min(e.count, from + a.chunk);
         copy_chunk(e.param, o.param, from, to, e.dtype == RC_F32 ? 4 : 2);
         if (e.dtype != RC_F32) copy_chunk(e.master, o.master, from, to, 4);
         copy_chunk(e.m, o.m, from, to, Bits / 8);

@@ -92,6 +92,7 @@ Error check_grad(const char* what, const rc_grad& g, int rank, int i, bool* has)
     const int64_t es = row_element_size(g.dtype);
     if (!es) return wrong(fmt("unknown dtype %lld", g.dtype));
     if (reinterpret_cast<uintptr_t>(g.grad) % (uintptr_t)es) return wrong("misaligned");
+    if (reinterpret_cast<uintptr_t>(g.grad) >> 56) return wrong("no address of a GPU buffer");  // the byte holds the type
     return {};
 }
 
@@ -402,14 +403,15 @@ int rc_grad_norm(const rc_grad_norm_desc* desc, const int* num_grads, const rc_g
                 for (int i = 0; i < num_grads[r]; ++i) {
                     const rc_grad& g = grads[r][i];
                     if (!g.grad || !g.count) continue;
-                    const int64_t chunks = pieces(g.count, kNormChunk);
-                    if (a.n == kNormList || a.chunks + chunks > kMaxNormChunks)
-                        if (const int e = flush()) return e;
-                    a.grad[a.n] = g.grad;
-                    a.count[a.n] = g.count;
-                    a.dtype[a.n] = (uint8_t)g.dtype;
-                    a.first[a.n++] = a.chunks;
-                    a.chunks += (int32_t)chunks;
+                    for (int64_t at = 0; at < g.count; at += kNormPiece) {
+                        const int64_t count = std::min(g.count - at, kNormPiece), chunks = pieces(count, kNormChunk);
+                        if (a.n == kNormList || a.chunks + chunks > kMaxNormChunks)
+                            if (const int e = flush()) return e;
+                        a.grad[a.n] = (reinterpret_cast<uint64_t>(g.grad) + (uint64_t)(at * row_element_size(g.dtype))) | (uint64_t)g.dtype << 56;
+                        a.count[a.n] = (int32_t)count;
+                        a.first[a.n++] = a.chunks;
+                        a.chunks += (int32_t)chunks;
+                    }
                 }
             if (const int e = flush()) return e;
             return launch_grad_norm_join(join, stream);
@@ -433,6 +435,12 @@ int rc_adamw_table(const rc_adamw_table_desc* desc, const int* num_params, const
         std::vector<AdamwEntry> entries;
         std::vector<AdamwSpan> spans;
         Buffers b(what);
+        int64_t elements = 0;
+        for (int r = 0; r < R; ++r)
+            for (int i = 0; i < num_params[r]; ++i)
+                elements += std::min(std::max<int64_t>(0, params[r][i].count), kMaxElements);
+        h.chunk = kAdamwMost;
+        while (h.chunk > kAdamwLeast && elements / h.chunk < 2048) h.chunk /= 2;
         for (int r = 0; r < R; ++r) {
             h.first[r] = (int32_t)entries.size();
             for (int i = 0; i < num_params[r]; ++i) {
@@ -455,7 +463,7 @@ int rc_adamw_table(const rc_adamw_table_desc* desc, const int* num_params, const
                     add(p.v_scale, blocks, 4, "v_scale");
                 }
                 entries.push_back({p.param, p.master, p.m, p.v, p.m_scale, p.v_scale, p.count, h.chunks, p.dtype, r});
-                h.chunks += pieces(p.count, kAdamwChunk);
+                h.chunks += pieces(p.count, h.chunk);
                 if (h.chunks > kMaxItems) return bad(what, "too many elements for one table");
             }
         }
@@ -483,7 +491,7 @@ int rc_adamw_table(const rc_adamw_table_desc* desc, const int* num_params, const
         std::memcpy(at, &h, sizeof h);
         if (!entries.empty()) std::memcpy(at + h.entries_at, entries.data(), entries.size() * sizeof(AdamwEntry));
         auto* map = reinterpret_cast<int32_t*>(at + h.chunks_at);
-        for (size_t i = 0; i < entries.size(); ++i) map = std::fill_n(map, pieces(entries[i].count, kAdamwChunk), (int32_t)i);
+        for (size_t i = 0; i < entries.size(); ++i) map = std::fill_n(map, pieces(entries[i].count, h.chunk), (int32_t)i);
         std::fill(reinterpret_cast<uint8_t*>(map), at + h.spans_at, uint8_t(0));
         if (kept) std::memcpy(at + h.spans_at, spans.data(), kept * sizeof(AdamwSpan));
         return {};
@@ -532,7 +540,6 @@ int rc_adamw_step(const rc_adamw_desc* desc, const void* table, void* table_on_g
                 if (g.count != e.count) return wrong(fmt("%lld elements, the parameter has %lld", g.count, e.count));
                 if (g.dtype != RC_F32 && g.dtype != e.dtype) return wrong(fmt("dtype %lld is neither RC_F32 nor the parameter's", g.dtype));
                 const auto lo = reinterpret_cast<uintptr_t>(g.grad);
-                if (lo >> 56) return wrong("no address of a GPU buffer");
                 if (in_spans(to, lo, lo + (uint64_t)(g.count * row_element_size(g.dtype)))) return wrong("overlaps a parameter's buffers");
             }
         }
@@ -547,6 +554,7 @@ int rc_adamw_step(const rc_adamw_desc* desc, const void* table, void* table_on_g
             a.out = static_cast<const AdamwHeader*>(out_table_on_gpu);
             a.entries_at = from->entries_at;
             a.chunks_at = from->chunks_at;
+            a.chunk = from->chunk;
             a.beta1 = (float)desc->beta1;
             a.rest1 = (float)(1.0 - desc->beta1);
             a.beta2 = (float)desc->beta2;

@@ -80,13 +80,13 @@ int launch_moe(const MoeArgs& a, int dtype, int weight_dtype, void* stream);
 
 // ---------------------------------------------------------------- gradient norms
 constexpr int64_t kNormChunk = 32768;  // elements of a workgroup
-constexpr int kNormList = 150;         // gradients of a launch: kernel arguments hold 4096 bytes
+constexpr int kNormList = 250;         // pieces of a launch: kernel arguments hold 4096 bytes
+constexpr int64_t kNormPiece = int64_t(1) << 30;  // elements of a piece at most: whole chunks
 
 struct GradNormArgs {
-    const void* grad[kNormList];
-    int64_t count[kNormList];
-    int32_t first[kNormList];  // the gradient's first chunk within the launch
-    uint8_t dtype[kNormList];
+    uint64_t grad[kNormList];  // addresses; the top byte is the type
+    int32_t count[kNormList];
+    int32_t first[kNormList];  // the piece's first chunk within the launch
     int32_t n;
     int32_t chunks;
     double* partial;           // the launch's first chunk
@@ -102,7 +102,8 @@ int launch_grad_norm(const GradNormArgs& a, void* stream);
 int launch_grad_norm_join(const GradNormJoin& a, void* stream);
 
 // ---------------------------------------------------------------- AdamW
-constexpr int64_t kAdamwChunk = 8192;  // elements of a workgroup, a multiple of RC_ADAMW_BLOCK
+// Elements of a workgroup: the most that still give 2048 workgroups, or the least.
+constexpr int64_t kAdamwLeast = 2048, kAdamwMost = 8192;
 constexpr int kAdamwList = 440;        // parameters of a launch
 
 struct AdamwEntry {
@@ -137,6 +138,7 @@ struct AdamwHeader {
     int32_t first[kMaxRanks + 1];  // parameters of each rank
     int32_t spans;
     int64_t chunks;
+    int64_t chunk;  // elements
     int64_t entries_at, chunks_at, spans_at;  // byte offsets
     AdamwFactors factors[kMaxRanks];
 };
@@ -162,7 +164,7 @@ struct AdamwArgs {
     int64_t entries_at, chunks_at;
     int32_t first;              // the launch's first parameter
     int32_t pad;
-    int64_t first_chunk, chunks;
+    int64_t first_chunk, chunks, chunk;
     float beta1, rest1, beta2, rest2, eps;
 };
 static_assert(sizeof(GradNormArgs) <= 4096 && sizeof(AdamwArgs) <= 4096, "kernel arguments");
