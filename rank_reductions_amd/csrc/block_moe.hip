@@ -512,17 +512,19 @@ __device__ __forceinline__ void up_tiles(const MoeArgs& a, int expert, const uin
     }
 }
 
-// The blockIdx.y-th expert that entries name and its entries, in any order; -1 if
-// there are no more.  The first workgroup of each writes them for the second
-// kernel.  The whole workgroup of Threads calls.
+// The blockIdx.y-th expert that entries name and its entries, in order (workgroups
+// that share an expert's entries go by the same list); -1 if there are no more.  The
+// first workgroup of each writes them for the second kernel.  The whole workgroup
+// of Threads calls.
 template <int Threads>
 __device__ __forceinline__ int find_expert(const MoeArgs& a, uint16_t* list, int* count) {
+    constexpr int kMost = RC_MAX_MOE_ENTRIES / Threads, kStrips = RC_MAX_MOE_ENTRIES / kWave;
     __shared__ uint32_t words[kMaxWords];
-    __shared__ int many, before;
-    constexpr int kMost = RC_MAX_MOE_ENTRIES / Threads;
+    __shared__ int many[kStrips], before;  // of each 64 entries
     const int32_t total = a.entries.total();
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
     if (threadIdx.x < kMaxWords) words[threadIdx.x] = 0;
-    if (threadIdx.x == 0) many = before = 0;
+    if (threadIdx.x == 0) before = 0;
     __syncthreads();
     int e[kMost];
 #pragma unroll
@@ -535,19 +537,39 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, uint16_t* list, int
     }
     __syncthreads();
     const int expert = nth_expert(words, (a.num_experts + 31) / 32, blockIdx.y);
+    const bool writes = blockIdx.x == 0 && blockIdx.z == 0;
     if (expert < 0) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) named_of(a)[blockIdx.y] = Named{-1, 0, 0, 0};
+        if (writes && threadIdx.x == 0) named_of(a)[blockIdx.y] = Named{-1, 0, 0, 0};
         return -1;
     }
 #pragma unroll
     for (int j = 0; j < kMost; ++j) {
         if (j * Threads >= total) continue;
-        if (e[j] == expert) list[atomicAdd(&many, 1)] = (uint16_t)(threadIdx.x + j * Threads);
-        if (blockIdx.x == 0 && e[j] >= 0 && e[j] < expert) atomicAdd(&before, 1);
+        const uint64_t here = __ballot(e[j] == expert), less = __ballot(e[j] >= 0 && e[j] < expert);
+        if (lane == 0) {
+            many[j * (Threads / kWave) + wave] = __popcll(here);
+            if (writes) atomicAdd(&before, __popcll(less));
+        }
     }
     __syncthreads();
-    const int n = __builtin_amdgcn_readfirstlane(many);
-    if (blockIdx.x == 0) {
+    const int strips = (total + Threads - 1) / Threads * (Threads / kWave);  // those that were counted
+    int own = lane < strips ? many[lane] : 0, upto = own;
+#pragma unroll
+    for (int d = 1; d < kStrips; d *= 2) {
+        const int v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
+    }
+    const int n = __builtin_amdgcn_readlane(upto, kStrips - 1);
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        if (j * Threads >= total) continue;
+        const int strip = __builtin_amdgcn_readfirstlane(j * (Threads / kWave) + wave);
+        const int first = __builtin_amdgcn_readlane(upto - own, strip);
+        const uint64_t here = __ballot(e[j] == expert);
+        if (e[j] == expert) list[first + __popcll(here & ((1ull << lane) - 1))] = (uint16_t)(threadIdx.x + j * Threads);
+    }
+    __syncthreads();
+    if (writes) {
         if (threadIdx.x == 0) named_of(a)[blockIdx.y] = Named{expert, before, n, 0};
         for (int i = threadIdx.x; i < n; i += Threads) list_of(a)[before + i] = list[i];
     }
@@ -555,7 +577,8 @@ __device__ __forceinline__ int find_expert(const MoeArgs& a, uint16_t* list, int
     return expert;
 }
 
-// blockIdx.x: a tile of rows of the hidden layer; blockIdx.y: the n-th expert named.
+// blockIdx.x: a tile of rows of the hidden layer; blockIdx.y: the n-th expert
+// named; blockIdx.z: every gridDim.z-th 64 of many entries.
 template <class X, class W>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
     __shared__ uint16_t list[RC_MAX_MOE_ENTRIES];
@@ -563,12 +586,13 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
     int n;
     const int expert = find_expert<kThreads>(a, list, &n);
     if (expert < 0) return;
+    if (n <= 2 * kTile && blockIdx.z) return;
     if (n <= kTile) {
         up_tiles<X, W, 1>(a, expert, list, 0, n, parts);
     } else if (n <= 2 * kTile) {
         up_tiles<X, W, 2>(a, expert, list, 0, n, parts);
     } else {
-        for (int first = 0; first < n; first += 4 * kTile) up_tiles<X, W, 4>(a, expert, list, first, n, parts);
+        for (int first = blockIdx.z * 4 * kTile; first < n; first += gridDim.z * 4 * kTile) up_tiles<X, W, 4>(a, expert, list, first, n, parts);
     }
 }
 
@@ -713,13 +737,13 @@ template <class W>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
     __shared__ __align__(16) float parts[(kWaves - 1) * 2 * 4 * kTile * kTile];
     const Named e = named_of(a)[blockIdx.y];
-    if (e.expert < 0) return;
+    if (e.expert < 0 || (e.count <= 2 * kTile && blockIdx.z)) return;
     if (e.count <= kTile) {
         down_tiles<W, 1>(a, e, 0, parts);
     } else if (e.count <= 2 * kTile) {
         down_tiles<W, 2>(a, e, 0, parts);
     } else {
-        for (int first = 0; first < e.count; first += 4 * kTile) down_tiles<W, 4>(a, e, first, parts);
+        for (int first = blockIdx.z * 4 * kTile; first < e.count; first += gridDim.z * 4 * kTile) down_tiles<W, 4>(a, e, first, parts);
     }
 }
 
@@ -779,19 +803,24 @@ __global__ __launch_bounds__(kThreads) void moe_join_kernel(MoeArgs a) {
 
 unsigned groups(int64_t n, int of) { return (unsigned)((n + of - 1) / of); }
 
-// Through LDS where an expert has two entries or more on the average: waves that
-// share their entries then read them once (64 tokens on 8 of 64 experts each, 8-bit
-// weights: 279 us, and 352 without; 256 tokens, bfloat16: 545 and 892), but wait for
-// each other (one token: 118 us, and 73 without).  Rows have to hold one step.
+// Through LDS where an expert has four entries or more on the average and there
+// are workgroups for half of the CUs: waves that share their entries then read
+// them once (64 tokens on 8 of 64 experts each, 8-bit weights: 279 us, and 352
+// without; 256 tokens, bfloat16: 543 and 892; 32 on 4 of 16: 140 and 152), but wait
+// for each other and are fewer (16 on 8 of 64: 383 and 362; 16 on 2 of 8: 117 and
+// 74).  Without, entries past 64 to an expert go to workgroups of their own (1024
+// tokens on two experts).  Rows have to hold one step.
 template <class X, class W>
 int run(const MoeArgs& a, hipStream_t s) {
     const int total = a.entries.total(), experts = min(a.num_experts, total);
-    if (total >= 2 * experts && a.width >= 64 && a.inner >= 64) {
-        moe_up_many_kernel<X, W><<<dim3(groups(a.hidden_row, kManyWaves * kTile), experts), kManyThreads, 0, s>>>(a);
-        moe_down_many_kernel<W><<<dim3(groups(a.width, kManyWaves * 2 * kTile), experts), kManyThreads, 0, s>>>(a);
+    const dim3 up(groups(a.hidden_row, kManyWaves * kTile), experts), down(groups(a.width, kManyWaves * 2 * kTile), experts);
+    if (total >= 4 * experts && (int)up.x * experts >= 128 && a.width >= 64 && a.inner >= 64) {
+        moe_up_many_kernel<X, W><<<up, kManyThreads, 0, s>>>(a);
+        moe_down_many_kernel<W><<<down, kManyThreads, 0, s>>>(a);
     } else {
-        moe_up_kernel<X, W><<<dim3(a.hidden_row / kTile, experts), kThreads, 0, s>>>(a);
-        moe_down_kernel<W><<<dim3(groups(a.width, 2 * kTile), experts), kThreads, 0, s>>>(a);
+        const unsigned z = groups(total, experts * 4 * kTile);
+        moe_up_kernel<X, W><<<dim3(a.hidden_row / kTile, experts, z), kThreads, 0, s>>>(a);
+        moe_down_kernel<W><<<dim3(groups(a.width, 2 * kTile), experts, z), kThreads, 0, s>>>(a);
     }
     moe_join_kernel<<<dim3(groups(a.width, 4 * kThreads), total / a.top_k), kThreads, 0, s>>>(a);
     return hipGetLastError();

@@ -151,12 +151,18 @@ def test_values_beyond_float16():
         check(ys, i, "f16")
 
 
-@pytest.mark.parametrize("shape", [([60, 3], 3, 2, 130, 96), ([150], 2, 1, 200, 70), ([301], 2, 1, 65, 129), ([90, 90, 90], 3, 3, 1000, 67)], ids=str)
+@pytest.mark.parametrize("shape", [([60, 3], 4, 2, 130, 96), ([150], 2, 1, 200, 70), ([301], 2, 1, 65, 129), ([90, 90, 90], 3, 3, 1000, 67),
+                                   ([700], 1, 1, 64, 64), ([40, 30], 32, 8, 129, 519), ([200], 16, 10, 70, 1030), ([300], 16, 1, 257, 1025),
+                                   ([900, 100], 16, 2, 65, 1100), ([64], 64, 4, 64, 200)], ids=str)
 @pytest.mark.parametrize("kind", KINDS, ids="-".join)
 def test_experts_with_many_entries(shape, kind):
-    """Tens and hundreds of entries to an expert: four and eight tiles of them, and more than one pass."""
+    """Tens and hundreds of entries to an expert: four and eight tiles of them, and more than one pass; with enough
+    experts and rows for the way through LDS, and without."""
     counts, experts, top_k, width, inner = shape
     i = inputs(counts, experts, top_k, width, inner, kind[0], kind[1], 19, padding=0.1)
+    if experts >= 16:  # popular experts, and some that nobody names
+        for e in i["experts"]:
+            e[:, 0] = torch.where(e[:, 0] >= 0, e[:, 0] % (experts // 8), -1)
     with session(len(counts)):
         ys = rr.moe_layer(**on_gpu(i), dtype=TYPES[kind[2]])
         torch.cuda.synchronize()
@@ -164,17 +170,21 @@ def test_experts_with_many_entries(shape, kind):
 
 
 def test_a_token_among_others():
-    """Bit for bit: what a token gives does not hang on which others there are, where there are enough for experts
-    to have two entries on the average."""
+    """Bit for bit: what a token gives does not hang on which others there are, by either way of the sums."""
     for kind in (("bf16", "bf16"), ("e4m3", "e4m3")):
-        i = inputs([60], 8, 8, 192, 96, *kind, 13)
-        some = dict(i, **{k: [i[k][0][11:14].contiguous()] for k in ("xs", "weights", "experts")})
-        if i["scales"] is not None:
-            some["scales"] = [i["scales"][0][11:14].contiguous()]
-        with session(1):
-            a, b = rr.moe_layer(**on_gpu(i)), rr.moe_layer(**on_gpu(some))
-            torch.cuda.synchronize()
-            assert torch.equal(a[0][11:14], b[0])
+        for experts, n in ((8, 60), (64, 64)):
+            i = inputs([n], experts, 8, 192, 260, *kind, 13)
+            other = dict(i, xs=[i["xs"][0].flip(0)], experts=[i["experts"][0].clone()], weights=[i["weights"][0].flip(0)])
+            other["experts"][0][:] = (other["experts"][0] + 1) % experts
+            for k in ("xs", "weights", "experts"):
+                other[k][0][11:14] = i[k][0][11:14]
+            if i["scales"] is not None:
+                other["scales"] = [i["scales"][0].flip(0)]
+                other["scales"][0][11:14] = i["scales"][0][11:14]
+            with session(1):
+                a, b = rr.moe_layer(**on_gpu(i)), rr.moe_layer(**on_gpu(other))
+                torch.cuda.synchronize()
+                assert torch.equal(a[0][11:14], b[0][11:14]) and not torch.equal(a[0], b[0])
 
 
 def test_graph_replays():
