@@ -532,7 +532,7 @@ enum { RC_QUANTIZE_NONE = 0, RC_QUANTIZE_E4M3 = 1 };
  *   group         elements that share a scale: 32, 64, 128 or 256 consecutive
  *                 ones (a row's last group may hold fewer), or 0 for a row
  *   width         elements of a row, in [1, RC_MAX_NORM_WIDTH]
- *   eps           >= 0
+ *   eps           >= 0 (with 0, rows of zeros give NaN)
  *   tokens        [R] rows of each rank */
 typedef struct rc_norm_desc {
     uint32_t struct_size;
@@ -670,7 +670,7 @@ typedef struct rc_adamw_table_desc {
 
 /* A table of all ranks' parameters, num_params[r] of rank r, which steps go by.
  * With `table` NULL *bytes receives its size; else *bytes >= that size, and the
- * table is written to host memory.  The caller copies it to the GPU (16-byte
+ * table is written to host memory, aligned to 8 bytes.  The caller copies it to the GPU (16-byte
  * aligned) and keeps both as long as it makes steps by them; the step writes to
  * the GPU's copy, so steps by one table run one after the other.  The buffers
  * must not overlap. */

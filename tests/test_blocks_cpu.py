@@ -458,3 +458,26 @@ def test_binding_refuses_steps(two):
     code(rr.grad_norm, [{}, {}])
     code(rr.grad_norm, [{0: 1.0}, {}])
     code(rr.grad_norm, [[z(3)], {}])
+
+
+def test_struct_layouts_match_a_c_compiler(tmp_path):
+    import subprocess
+    from pathlib import Path
+
+    structs = {"rc_norm_desc": blocks.RcNormDesc, "rc_moe_desc": blocks.RcMoeDesc, "rc_grad": blocks.RcGrad,
+               "rc_grad_norm_desc": blocks.RcGradNormDesc, "rc_adamw_table_desc": blocks.RcAdamwTableDesc,
+               "rc_adamw_param": blocks.RcAdamwParam, "rc_adamw_desc": blocks.RcAdamwDesc}
+    lines, want = [], []
+    for name, cls in structs.items():
+        lines.append(f'printf("%zu\\n", sizeof({name}));')
+        want.append(ctypes.sizeof(cls))
+        for field, _ in cls._fields_:
+            lines.append(f'printf("%zu\\n", offsetof({name}, {field}));')
+            want.append(getattr(cls, field).offset)
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "rc.h"\nint main(void){' + "".join(lines) + "return 0;}\n")
+    exe = tmp_path / "layout"
+    include = Path(__file__).resolve().parent.parent / "include"
+    subprocess.run(["gcc", f"-I{include}", str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+    assert [int(x) for x in out.split()] == want
