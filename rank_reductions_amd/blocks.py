@@ -212,8 +212,9 @@ class AdamWState:
                       with float32 scales of 256 elements each in m_scale, v_scale;
       step            int32, one number for each rank: the steps made.
     The tensors are updated in place by adamw_step, which goes by their addresses
-    from here: it refuses a state whose tensors have been given other memory.
-    One made from saved tensors goes on where they were saved."""
+    from here: copy into them to change them (others put into the maps are not
+    seen); it refuses a state whose tensors have been given other memory.  A state
+    made from saved tensors goes on where they were saved."""
 
     __slots__ = ("bits", "params", "m", "v", "step", "master", "m_scale", "v_scale", "_table")
 
