@@ -686,8 +686,9 @@ int rc_adamw_table(const rc_adamw_table_desc* desc, const int* num_params, const
  *               |grad_scale|) is larger are scaled down to it
  *   grad_scale  factor of the gradients
  *   seed        of the roundings of 8-bit states
- *   steps, steps_out  [R] int32 on the GPU: the steps made before and after;
- *               may be the same */
+ *   steps, steps_out  [R] int32 on the GPU, >= 0: the steps made before and after;
+ *               may be the same.  A rank's count goes on with each step that it
+ *               makes, whichever of its parameters have gradients */
 typedef struct rc_adamw_desc {
     uint32_t struct_size;
     uint32_t seed;

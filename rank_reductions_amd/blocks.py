@@ -210,7 +210,8 @@ class AdamWState:
       m, v            means of the gradients and of their squares: float32, or
                       with bits=8 float8_e4m3fn codes of m and of the root of v
                       with float32 scales of 256 elements each in m_scale, v_scale;
-      step            int32, one number for each rank: the steps made.
+      step            int32, one number for each rank: the steps made, whichever
+                      parameters had gradients in them.
     The tensors are updated in place by adamw_step, which goes by their addresses
     from here: copy into them to change them (others put into the maps are not
     seen); it refuses a state whose tensors have been given other memory.  A state

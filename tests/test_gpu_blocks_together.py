@@ -199,3 +199,63 @@ def test_tensors_past_2_31_elements():
         torch.cuda.synchronize()
         silu = 1 / (1 + np.exp(-1.0))
         assert abs(float(y[0][0, -1]) - 2 * silu) < 2.0 ** -7 and not y[0][0, :-1].any()
+
+
+def test_nothing_to_do():
+    """Ranks without tokens, parameters without elements or gradients."""
+    with session(2):
+        e = torch.zeros(0, 64, dtype=torch.bfloat16, device=DEV)
+        w = torch.ones(64, dtype=torch.bfloat16, device=DEV)
+        y, s = rr.rms_norm([e, e], [w, w], residuals=[e, e])
+        assert [t.shape for t in y + s] == [(0, 64)] * 4
+        dx, dw = rr.rms_norm_grad([e, e], [e, e], [w, w])
+        torch.cuda.synchronize()
+        assert dx[0].shape == (0, 64) and not dw[0].any() and not dw[1].any()
+        i = moe_inputs([0, 0], 4, 2, 64, 32, "bf16", "bf16", 1)
+        y = rr.moe_layer(**{k: dev(t) if t is not None else None for k, t in i.items()})
+        assert [t.shape for t in y] == [(0, 64)] * 2
+        out = torch.ones(2, device=DEV)
+        assert rr.grad_norm([{}, {}], out=out).tolist() == [0.0, 0.0]
+        for bits in (32, 8):
+            params = [{0: torch.zeros(0, device=DEV), 1: torch.ones(5, device=DEV)}, {}]
+            state = rr.adamw_state(params, bits=bits)
+            rr.adamw_step(state, [{0: torch.zeros(0, device=DEV)}, {}])
+            rr.adamw_step(state, [{1: torch.ones(5, device=DEV)}, {}], lr=0.5, weight_decay=0.0, eps=0.0, betas=(0.0, 0.5))
+            torch.cuda.synchronize()
+            # counted at both calls: v = 0.5 of 1 - 0.5^2
+            want = 1 - 0.5 / (0.5 / 0.75) ** 0.5
+            assert state.step.tolist() == [2, 2] and torch.allclose(params[0][1], torch.full((5,), want, device=DEV), rtol=1e-6)
+
+
+@pytest.mark.parametrize("where", ["the first call", "every call"])
+def test_a_step_and_its_sync_in_one_graph(where):
+    """grad_norm, adamw_step and a norm of the stepped weights captured together, replayed beside eager work."""
+    with session(2):
+        g = gen(11)
+        make = lambda: [{0: torch.ones(512, device=DEV)} for _ in range(2)]  # noqa: E731
+        eager, graphed = rr.adamw_state(make()), rr.adamw_state(make())
+        grads = [{0: normal(g, 512).to(DEV)} for _ in range(2)]
+        x = [normal(g, 7, 512).to(DEV) for _ in range(2)]
+        norms = torch.zeros(2, device=DEV)
+        out = [torch.zeros(7, 512, device=DEV) for _ in range(2)]
+
+        def work(state, out):
+            rr.grad_norm(grads, out=norms)
+            rr.adamw_step(state, grads, lr=0.1, norms=norms, max_norm=1.0)
+            rr.rms_norm(x, [m[0] for m in state.params], out=out)
+
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            work(graphed, out)
+        want = [torch.zeros(7, 512, device=DEV) for _ in range(2)]
+        for k in range(3):
+            if k == 0 or where == "every call":
+                for m in grads:
+                    m[0].mul_(-0.7)
+            work(eager, want)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(out + [m[0] for m in graphed.params], want + [m[0] for m in eager.params]):
+                assert torch.equal(a, b)
