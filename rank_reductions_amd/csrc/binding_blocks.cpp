@@ -357,7 +357,7 @@ struct Table {
     at::Device dev{at::kCPU};
     std::vector<PyObject*> keys, tensors;  // owned
     std::vector<const void*> addresses;
-    std::vector<int64_t> counts;           // of the parameters
+    std::vector<PyObject*> params;         // those of `tensors` that are parameters
     int num[RC_MAX_RANKS] = {};
     std::vector<uint64_t> host;
     Tensor gpu;
@@ -427,6 +427,7 @@ PyObject* adamw_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 e.count = p.numel();
                 e.dtype = row_type(p, what);
                 e.param = t.hold(params.map[r], key, p.scalar_type(), e.count, what, "param");
+                t.params.push_back(t.tensors.back());
                 if (e.dtype != RC_F32) {
                     if (!maps[0].n) raise(RC_ERR_INVALID_ARGUMENT, what, "16-bit parameters without master copies");
                     e.master = static_cast<float*>(t.hold(maps[0].map[r], key, ScalarType::Float, e.count, what, "master"));
@@ -438,7 +439,6 @@ PyObject* adamw_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     e.m_scale = static_cast<float*>(t.hold(maps[3].map[r], key, ScalarType::Float, blocks, what, "m_scale"));
                     e.v_scale = static_cast<float*>(t.hold(maps[4].map[r], key, ScalarType::Float, blocks, what, "v_scale"));
                 }
-                t.counts.push_back(e.count);
                 all.push_back(e);
                 ++t.num[r];
             }
@@ -504,9 +504,9 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 if (g == Py_None) continue;
                 if (!THPVariable_Check(g)) raise(RC_ERR_INVALID_ARGUMENT, what, "rank %d: a gradient is not a tensor", r);
                 held.push_back(THPVariable_Unpack(g));
-                if (held.back().numel() != t.counts[i])
-                    raise(RC_ERR_SHAPE_MISMATCH, what, "rank %d: a gradient has %lld elements, its parameter %lld", r,
-                          (long long)held.back().numel(), (long long)t.counts[i]);
+                if (held.back().sizes() != THPVariable_Unpack(t.params[i]).sizes())
+                    raise(RC_ERR_SHAPE_MISMATCH, what, "rank %d: a gradient of %lld elements has another shape than its parameter", r,
+                          (long long)held.back().numel());
                 all[i] = grad_of(held.back(), t.dev, what, r);
             }
             if (found != PyDict_GET_SIZE(grads.map[r])) raise(RC_ERR_PARAM_MISMATCH, what, "rank %d: gradients of parameters that the state does not hold", r);

@@ -345,3 +345,29 @@ def test_state_whose_tensors_moved_is_refused():
         p.data = torch.randn(100, device=DEV)
         with pytest.raises(rr.CollectiveError, match="other memory"):
             rr.adamw_step(state, [{0: torch.randn(100, device=DEV)}])
+
+
+def test_gradients_that_do_not_fit_are_refused():
+    """Another shape, type, device or layout, and gradients of parameters that are not there: nothing is changed."""
+    with session(1):
+        p = torch.randn(4, 6, device=DEV)
+        state = rr.adamw_state([{0: p, 1: torch.ones(3, device=DEV).half()}])
+        keep = p.clone()
+        good = torch.randn(4, 6, device=DEV)
+        for grads in ([{0: good.t().contiguous()}], [{0: good.view(-1)}], [{0: good[:2]}], [{0: good.t().contiguous().t()}], [{0: good.bfloat16()}],
+                      [{0: good.double()}], [{0: good.cpu()}], [{2: good}], [{0: 1.0}], [good], [], [{0: p}], [{1: torch.ones(3, device=DEV).bfloat16()}]):
+            with pytest.raises((rr.CollectiveError, TypeError)):
+                rr.adamw_step(state, grads)
+        for kw in (dict(lr=-1.0), dict(lr=torch.ones(2, device=DEV)), dict(lr=torch.ones(1)), dict(lr=torch.ones(1, device=DEV).double()),
+                   dict(norms=torch.ones(2, device=DEV)), dict(max_norm=1.0), dict(seed=-1), dict(seed=2**32), dict(betas=(0.9, 1.0)),
+                   dict(out=rr.adamw_state([{0: torch.zeros(4, 6, device=DEV)}])), dict(out=rr.adamw_state([{0: p, 1: torch.ones(3, device=DEV).half()}])),
+                   dict(out=rr.adamw_state([{0: torch.zeros(4, 6, device=DEV), 1: torch.ones(3, device=DEV).half()}], bits=8))):
+            with pytest.raises((rr.CollectiveError, TypeError)):
+                rr.adamw_step(state, [{0: good}], **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(p, keep) and state.step.tolist() == [0]
+        rr.adamw_step(state, [{0: good}])
+        assert not torch.equal(p, keep)
+    with session(2):
+        with pytest.raises(rr.CollectiveError, match="ranks"):
+            rr.adamw_step(state, [{}, {}])
