@@ -284,8 +284,7 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// src: where this thread's pieces of the entries' rows begin, at byte `off[i]` of
-// rows of `row_size` bytes.  get(buffer, step of the part, n, frag): the entries'
+// src: the entries' rows, of `row_size` bytes, that this thread brings pieces of.  get(buffer, step of the part, n, frag): the entries'
 // side of a step out of LDS.
 template <class M, int Rows, int N, class S, class Get>
 __device__ __forceinline__ void staged_sums(const uint8_t* const* w, int size, const uint8_t* const* src, int row_size, uint8_t* lds,

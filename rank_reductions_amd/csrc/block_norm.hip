@@ -8,6 +8,9 @@
 // dx = (dn - n * mean(dn * n)) / sqrt(...) + d_sum; dw = the sum over rows of
 // dy * n, held in registers by a workgroup over the rows it takes, then added
 // up over the workgroups in order.
+// Both stream: 16384 rows of 4096 bf16 with a residual take 85 us forward (537 MB,
+// some from the last-level cache, at 6.2 TB/s) and 119 back (4.5 TB/s: a row waits
+// for its two sums); 6404 rows of 5003 float16 to 8 bits 58 us (3.9 TB/s).
 #include "blocks_impl.h"
 
 #ifndef RC_ROW_TYPE
@@ -164,6 +167,10 @@ __global__ __launch_bounds__(Waves == 1 ? 256 : Waves * kWave) void rms_norm_ker
     }
 }
 
+// A workgroup keeps its part of dw in registers, so few workgroups, 512 in all,
+// keep the parts' memory small (8 MB of 546 at 4096 columns); with eight waves of
+// one vector 120 us in place of 126 with four of two.
+//
 // The gradient for the rows t = part, part + parts, ... of a rank (a workgroup
 // is four waves with a row each, or `Waves` on one row).
 template <class T, class W, int Waves, int V>
