@@ -211,9 +211,11 @@ __device__ __forceinline__ int nth_expert(const uint32_t* words, int num_words, 
     return __builtin_amdgcn_readlane(lane * 32 + __ffs((int)w) - 1, __builtin_amdgcn_readfirstlane(at));
 }
 
-// This wave's part of a sum of `steps` steps: a quarter, in multiples of `ahead`.
-__device__ __forceinline__ void part_of(int steps, int ahead, int* s0, int* s1) {
-    const int each = ((steps + kWaves - 1) / kWaves + ahead - 1) / ahead * ahead;
+// This wave's part of a sum of `steps` steps: a quarter, in multiples of `whole`.  That
+// is the steps in flight of one tile of entries, also with more tiles: an entry's sum
+// is cut alike however many others stand beside it.
+__device__ __forceinline__ void part_of(int steps, int whole, int* s0, int* s1) {
+    const int each = ((steps + kWaves - 1) / kWaves + whole - 1) / whole * whole;
     *s0 = threadIdx.x / kWave * each;
     *s1 = min(*s0 + each, steps);
 }
@@ -461,7 +463,7 @@ __device__ __forceinline__ void up_many(const MoeArgs& a, int expert, const uint
 template <class X, class W, int N>
 __device__ __forceinline__ void up_tiles(const MoeArgs& a, int expert, const uint16_t* list, int first, int count, float* parts) {
     using M = Up<X, W>;
-    constexpr int Rows = 2, kAhead = N == 4 ? 2 : N == 1 ? 6 : 4;  // as registers allow; four: 6% slower for 16 tokens on 4 of 32
+    constexpr int Rows = 2, kFirst = 6, kAhead = N == 4 ? 2 : N == 1 ? kFirst : 4;  // as registers allow; four: 6% slower for 16 tokens on 4 of 32
     const int lane = lane_id(), wave = threadIdx.x / kWave, sub = lane / kTile;
     const int rank = expert / a.per_rank, local = expert - rank * a.per_rank;
     const int tile = blockIdx.x * kTile;
@@ -476,7 +478,7 @@ __device__ __forceinline__ void up_tiles(const MoeArgs& a, int expert, const uin
     }
     f32x4 c[Rows][N] = {};
     int s0, s1;
-    part_of((size + 63) / 64, kAhead, &s0, &s1);
+    part_of((size + 63) / 64, kFirst, &s0, &s1);
     sums_of<M, Rows, N, kAhead>(w, s0, s1, size, c, [&](int n, int step, typename M::Frag& f, bool full) {
         const int at = (step * 4 + sub) * M::kX * 16;
 #pragma unroll
@@ -646,7 +648,8 @@ __device__ __forceinline__ void write_products(const MoeArgs& a, int rank, int l
 template <class W, int N>
 __device__ __forceinline__ void down_tiles(const MoeArgs& a, const Named& e, int first, float* parts) {
     using M = Down<W>;
-    constexpr int Rows = 2, kAhead = M::kH == 2 ? 4 / N : N == 4 ? 2 : N > 1 ? 4 : __is_same(W, F16) ? 6 : 12;  // as registers allow
+    constexpr int Rows = 2, kFirst = M::kH == 2 ? 4 : __is_same(W, F16) ? 6 : 12;  // as registers allow
+    constexpr int kAhead = N == 1 ? kFirst : M::kH == 2 ? 4 / N : N == 4 ? 2 : 4;
     const int lane = lane_id(), sub = lane / kTile;
     const int rank = e.expert / a.per_rank, local = e.expert - rank * a.per_rank;
     const int wave = threadIdx.x / kWave, tile = blockIdx.x * Rows * kTile;
@@ -665,7 +668,7 @@ __device__ __forceinline__ void down_tiles(const MoeArgs& a, const Named& e, int
     }
     f32x4 c[Rows][N] = {};
     int s0, s1;
-    part_of((size + 63) / 64, kAhead, &s0, &s1);
+    part_of((size + 63) / 64, kFirst, &s0, &s1);
     sums_of<M, Rows, N, kAhead>(w, s0, s1, size, c, [&](int n, int step, typename M::Frag& f, bool) {
 #pragma unroll
         for (int v = 0; v < M::kH; ++v) {

@@ -187,6 +187,31 @@ def test_a_token_among_others():
                 assert torch.equal(a[0][11:14], b[0][11:14]) and not torch.equal(a[0], b[0])
 
 
+@pytest.mark.parametrize("kind", KINDS, ids="-".join)
+@pytest.mark.parametrize("experts,width,inner", [(2, 192, 192), (2, 640, 448), (3, 645, 453), (2, 2048, 768), (16, 192, 1100)])
+def test_a_token_in_a_growing_crowd(experts, width, inner, kind):
+    """Bit for bit the same, whether its expert has one entry or several tiles of them, with the same sizes: the last
+    shape through LDS, the others without."""
+    n, token = 66, 5
+    i = inputs([n], experts, 1, width, inner, *kind[:2], 23)
+    with session(1):
+        want = None
+        for top in (1, 2, 16, 17, 32, 33, 48, 64, 65, 66):
+            # expert 0's entries: this token and the last ones, so that its place among them changes too
+            e = 1 + torch.arange(n, dtype=torch.int32) % (experts - 1)
+            e[n - top:] = 0
+            if n - top > token:
+                e[n - top], e[token] = 1, 0
+            assert int((e == 0).sum()) == top
+            i["experts"] = [e.view(n, 1)]
+            y = rr.moe_layer(**on_gpu(i), dtype=TYPES[kind[2]])[0]
+            torch.cuda.synchronize()
+            if want is None:
+                want = y[token].clone()
+                check([y], i, kind[2])
+            assert torch.equal(y[token], want), top
+
+
 def test_graph_replays():
     i = inputs([2, 3], 8, 2, 256, 128, "bf16", "bf16", 15)
     with session(2):
