@@ -215,7 +215,10 @@ class AdamWState:
     The tensors are updated in place by adamw_step, which goes by their addresses
     from here: copy into them to change them (others put into the maps are not
     seen); it refuses a state whose tensors have been given other memory.  A state
-    made from saved tensors goes on where they were saved."""
+    made from saved tensors goes on where they were saved.  It has to live until a
+    step on a stream that is not torch's own (a number, an ExternalStream) is done,
+    and as long as a graph that holds a step is replayed; with torch's streams the
+    tensors alone do."""
 
     __slots__ = ("bits", "params", "m", "v", "step", "master", "m_scale", "v_scale", "_table")
 

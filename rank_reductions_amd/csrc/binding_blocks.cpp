@@ -2,6 +2,8 @@
 // holds the public functions).
 #include "binding_blocks.h"
 
+#include <c10/hip/HIPCachingAllocator.h>
+
 #include <cstring>
 #include <memory>
 
@@ -384,6 +386,15 @@ struct Table {
             if (THPVariable_Unpack(tensors[i]).data_ptr() != addresses[i])
                 raise(RC_ERR_INVALID_ARGUMENT, what, "a tensor of the state has been given other memory since the state was made: make it anew");
     }
+    // Keeps the table's memory, should the state go, from being given out again
+    // before what the current stream holds by now is done: the table is not the
+    // caller's to record.  A stream that is not torch's own, whose number is its
+    // handle, may be gone by the time the memory is asked for, and stays out.
+    void hold_for_stream() const {
+        const auto s = c10::hip::getCurrentHIPStream(dev.index());
+        if (s.stream() && s.id() == reinterpret_cast<intptr_t>(s.stream())) return;
+        c10::hip::HIPCachingAllocator::recordStream(gpu.storage().data_ptr(), s);
+    }
 };
 
 constexpr const char* kTableName = "rank_reductions_amd.AdamWTable";
@@ -532,6 +543,8 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         d.steps = static_cast<const int32_t*>(data_of(a[1], ScalarType::Int, s.ranks, t.dev, what, "step"));
         d.steps_out = static_cast<int32_t*>(data_of(a[3], ScalarType::Int, s.ranks, t.dev, what, "step of out"));
         void* stream = stream_on(s, t.dev, what);
+        t.hold_for_stream();
+        if (&o != &t) o.hold_for_stream();
         call([&] { return rc_adamw_step(&d, t.host.data(), t.gpu.data_ptr(), o.host.data(), o.gpu.data_ptr(), lists, stream); });
         Py_RETURN_NONE;
     });

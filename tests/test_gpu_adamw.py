@@ -338,6 +338,61 @@ def test_steps_captured_into_a_graph():
         assert eager.step.tolist() == [11, 9]
 
 
+def awaiting_free():
+    """Addresses of blocks that are freed, but wait for a stream."""
+    return {b["address"] for seg in torch.cuda.memory_snapshot() for b in seg["blocks"] if b["state"] not in ("active_allocated", "inactive")}
+
+
+@pytest.mark.parametrize("other", [False, True])
+def test_state_dropped_under_a_step_on_another_stream(other):
+    """What the step goes by stays until the stream is done with it, though the state that held it is gone."""
+    sizes = [300, 8193, 70000]
+    with session(2):
+        _, gs, want = make(sizes, 2, "bf16", "bf16", 8, 41)
+        rr.adamw_step(want, gs, seed=6)
+        _, _, state = make(sizes, 2, "bf16", "bf16", 8, 41)
+        _, _, out = make(sizes, 2, "bf16", "bf16", 8, 42)
+        a = torch.randn(4096, 4096, device=DEV)
+        keep = [getattr(x, k) for x in (state, out) for k in ("params", "m", "v", "step", "master", "m_scale", "v_scale")]
+        got = out if other else state
+        got = {k: getattr(got, k) for k in ("bits", "params", "m", "v", "step", "master", "m_scale", "v_scale")}
+        torch.cuda.synchronize()
+        before = awaiting_free()
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            b = a
+            for _ in range(60):
+                b = a @ b * 1e-2
+            rr.adamw_step(state, gs, seed=6, out=out if other else None)
+        del state, out
+        waiting = awaiting_free() - before
+        done = s.query()  # if the stream had been done by then, nothing would have to wait
+        junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device=DEV) for n in range(512, 1 << 16, 512)]
+        s.synchronize()
+        assert done or len(waiting) == (2 if other else 1)
+        torch.empty(1, device=DEV)  # takes note of what is done
+        assert not waiting & awaiting_free()
+        del junk, keep
+        states_equal(rr.AdamWState(**got), want)
+
+
+def test_a_step_on_a_stream_of_the_callers():
+    """A stream that torch does not know is not asked for once the step is done: it may be gone."""
+    with session(1):
+        _, gs, want = make([5000], 1, "f32", "f32", 32, 43)
+        rr.adamw_step(want, gs)
+        _, _, state = make([5000], 1, "f32", "f32", 32, 43)
+        s = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        before = awaiting_free()
+        rr.adamw_step(state, gs, stream=s.cuda_stream)
+        s.synchronize()
+        states_equal(state, want)
+        keep = state.params, state.m, state.v
+        del state
+        assert awaiting_free() <= before and keep
+
+
 def test_state_whose_tensors_moved_is_refused():
     with session(1):
         p = torch.randn(100, device=DEV)
