@@ -608,8 +608,9 @@ typedef struct rc_moe_desc {
  *               row, else NULL
  *   down[d]     [E/R, width, inner]; down_scales[d] [E/R, width] likewise
  * Sums are float32, in an order that depends on the sizes (tokens, top_k,
- * num_experts, width, inner) alone.  silu(G x) * (U x) is held in float32, or as
- * two bfloat16 numbers whose sum is within 2^-16 of it; ys are rounded once. */
+ * num_experts, width, inner) alone.  silu(G x) * (U x) is held in float32 (with
+ * RC_E4M3 rows as three bfloat16 numbers), or where ys are of 16 bits as two
+ * bfloat16 numbers whose sum is within 2^-16 of it; ys are rounded once. */
 int rc_moe_layer_workspace(const rc_moe_desc* desc, int64_t* bytes);
 int rc_moe_layer(const rc_moe_desc* desc, const void* const* xs, const float* const* scales,
                  const int32_t* const* experts, const float* const* weights, const void* const* gate_up,

@@ -97,13 +97,17 @@ __device__ __forceinline__ u32x4 as_f16(u32x4 v, int half) {
     return o;
 }
 
-// The two bfloat16 numbers whose sum is nearest to v (within 2^-16 of it); the
-// second is zero where the first is not finite.
-__device__ __forceinline__ void two_bf16(float v, uint16_t* hi, uint16_t* lo) {
-    const __bf16 h = (__bf16)v;
-    const float f = (float)h;
-    *hi = __builtin_bit_cast(uint16_t, h);
-    *lo = __builtin_bit_cast(uint16_t, (__bf16)(__builtin_isfinite(f) ? v - f : 0.0f));
+// Parts bfloat16 numbers whose sum is nearest to v: two within 2^-16 of it, three
+// at v itself.  Those after the first are zero where it is not finite.
+template <int Parts>
+__device__ __forceinline__ void as_bf16_parts(float v, uint16_t* part) {
+#pragma unroll
+    for (int i = 0; i < Parts; ++i) {
+        const __bf16 h = (__bf16)v;
+        const float f = (float)h;
+        part[i] = __builtin_bit_cast(uint16_t, h);
+        v = __builtin_isfinite(f) ? v - f : 0.0f;
+    }
 }
 
 // The first product's step: kK elements of a row's sum, of which each of the
@@ -132,25 +136,28 @@ struct Up {
     }
 };
 
-// The second product's: the hidden values are float32, or two bfloat16 each,
-// and the weights taken as bfloat16 (float16 ones, of 11 bits, as the sum of two).
-template <class W>
+// The second product's: the hidden values are float32, or Parts bfloat16 each (two,
+// an eighth of a float16's half step and less of a bfloat16's; three for float32
+// outputs), and the weights taken as bfloat16 (float16 ones, of 11 bits, as the sum
+// of two: hidden values may pass float16's range).
+template <class W, int Parts>
 struct Down {
     static constexpr int kK = 64 / (int)sizeof(typename W::E);
     static constexpr bool kWide = sizeof(typename W::E) == 4;
+    static constexpr int kParts = kWide ? 1 : Parts;
     static constexpr int kH = kWide ? 1 : kK / 32;  // 16-byte vectors of one kind of hidden value
     struct Frag {
-        u32x4 hi[kH], lo[kH];
+        u32x4 h[kParts][kH];
     };
     __device__ __forceinline__ static f32x4 mma(u32x4 w, const Frag& f, f32x4 c) {
-        const u32x4 *hi = f.hi, *lo = f.lo;
         if constexpr (kWide) {
-            return mma_f32(w, hi[0], c);
+            return mma_f32(w, f.h[0][0], c);
         } else if constexpr (sizeof(typename W::E) == 1) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const u32x4 v = as_bf16(w, h);
-                c = mma_bf16(v, lo[h], mma_bf16(v, hi[h], c));
+            for (int i = 0; i < 2; ++i) {
+                const u32x4 v = as_bf16(w, i);
+#pragma unroll
+                for (int p = 0; p < Parts; ++p) c = mma_bf16(v, f.h[p][i], c);
             }
             return c;
         } else if constexpr (__is_same(W, F16)) {
@@ -161,9 +168,9 @@ struct Down {
             BF16::unpack(first, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) l[i] = __builtin_isfinite(g[i]) ? e[i] - g[i] : 0.0f;
-            return mma_bf16(first, lo[0], mma_bf16(BF16::pack(l), hi[0], mma_bf16(first, hi[0], c)));
+            return mma_bf16(first, f.h[1][0], mma_bf16(BF16::pack(l), f.h[0][0], mma_bf16(first, f.h[0][0], c)));
         } else {
-            return mma_bf16(w, lo[0], mma_bf16(w, hi[0], c));
+            return mma_bf16(w, f.h[1][0], mma_bf16(w, f.h[0][0], c));
         }
     }
 };
@@ -269,7 +276,8 @@ constexpr int kManyThreads = kManyWaves * kWave;
 template <int Bytes, int Planes, int N>
 struct Stage {
     static constexpr int kStage = Bytes * N > 512 ? 65536 : 32768;       // bytes of a part; two at a time
-    static constexpr int kSteps = kStage / (Bytes * N * kTile);          // of a part
+    static constexpr int kFit = kStage / (Bytes * N * kTile);
+    static constexpr int kSteps = kFit >= 16 ? 16 : kFit >= 8 ? 8 : kFit >= 4 ? 4 : kFit;  // of a part
     static constexpr int kPlane = Bytes / Planes;                        // bytes of a step in a row
     static constexpr int kRow = kSteps * kPlane + 16;                    // rows 16 bytes apart in the banks
     static constexpr int kSize = kRow * Planes * N * kTile;              // of one of the two buffers
@@ -380,6 +388,11 @@ __device__ __forceinline__ float scale_of(const MoeArgs& a, int entry) {
     return a.x_scale[rank][t / a.top_k];
 }
 
+// The p-th bfloat16 numbers of the hidden values; float32 outputs of 8-bit rows have a third.
+template <class X>
+constexpr int kMostParts = sizeof(typename X::E) == 1 ? 3 : 2;
+__device__ __forceinline__ uint16_t* hidden_part(const MoeArgs& a, int p) { return reinterpret_cast<uint16_t*>(a.hidden + p * a.hidden_plane); }
+
 // The hidden values of this lane's rows and entries, from the sums with G and with U.
 template <class X, class W, int N>
 __device__ __forceinline__ void write_hidden(const MoeArgs& a, int rank, int local, const uint16_t* list, int first, int count, int tile,
@@ -399,11 +412,13 @@ __device__ __forceinline__ void write_hidden(const MoeArgs& a, int rank, int loc
         if constexpr (sizeof(typename W::E) == 4) {
             *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.hidden) + to) = h;
         } else {
-            uint16_t hi[4], lo[4];
+            uint16_t part[4][kMostParts<X>];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) two_bf16(h[v], hi + v, lo + v);
-            *reinterpret_cast<u16x4*>(reinterpret_cast<uint16_t*>(a.hidden) + to) = u16x4{hi[0], hi[1], hi[2], hi[3]};
-            *reinterpret_cast<u16x4*>(reinterpret_cast<uint16_t*>(a.hidden + a.hidden_plane) + to) = u16x4{lo[0], lo[1], lo[2], lo[3]};
+            for (int v = 0; v < 4; ++v) as_bf16_parts<kMostParts<X>>(h[v], part[v]);
+#pragma unroll
+            for (int p = 0; p < kMostParts<X>; ++p)
+                if (p < 2 || a.out_dtype == RC_F32)
+                    *reinterpret_cast<u16x4*>(hidden_part(a, p) + to) = u16x4{part[0][p], part[1][p], part[2][p], part[3][p]};
         }
     }
 }
@@ -508,7 +523,11 @@ __device__ __forceinline__ void up_tiles(const MoeArgs& a, int expert, const uin
         if constexpr (sizeof(typename W::E) == 4) {
             reinterpret_cast<float*>(a.hidden)[to] = h;
         } else {
-            two_bf16(h, reinterpret_cast<uint16_t*>(a.hidden) + to, reinterpret_cast<uint16_t*>(a.hidden + a.hidden_plane) + to);
+            uint16_t part[kMostParts<X>];
+            as_bf16_parts<kMostParts<X>>(h, part);
+#pragma unroll
+            for (int p = 0; p < kMostParts<X>; ++p)
+                if (p < 2 || a.out_dtype == RC_F32) hidden_part(a, p)[to] = part[p];
         }
     }
 }
@@ -599,7 +618,7 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
 
 // Tiles of entries at most that a wave has registers for.
 template <class W>
-constexpr int kDownMost = Down<W>::kH == 2 ? 4 : 8;
+constexpr int kDownMost = Down<W, 2>::kH == 2 ? 4 : 8;
 
 // blockIdx.x: kManyWaves tiles of rows.
 template <class X, class W>
@@ -645,9 +664,9 @@ __device__ __forceinline__ void write_products(const MoeArgs& a, int rank, int l
 
 // D times the hidden values of N tiles of an expert's entries, for two tiles of
 // rows, the sums cut over the workgroup's waves.
-template <class W, int N>
+template <class W, int Parts, int N>
 __device__ __forceinline__ void down_tiles(const MoeArgs& a, const Named& e, int first, float* parts) {
-    using M = Down<W>;
+    using M = Down<W, Parts>;
     constexpr int Rows = 2, kFirst = M::kH == 2 ? 4 : __is_same(W, F16) ? 6 : 12;  // as registers allow
     constexpr int kAhead = N == 1 ? kFirst : M::kH == 2 ? 4 / N : N == 4 ? 2 : 4;
     const int lane = lane_id(), sub = lane / kTile;
@@ -672,9 +691,9 @@ __device__ __forceinline__ void down_tiles(const MoeArgs& a, const Named& e, int
     sums_of<M, Rows, N, kAhead>(w, s0, s1, size, c, [&](int n, int step, typename M::Frag& f, bool) {
 #pragma unroll
         for (int v = 0; v < M::kH; ++v) {
-            const uint8_t* p = h[n] + step * M::kK * kSize + v * 16;
-            f.hi[v] = *reinterpret_cast<const u32x4*>(p);
-            if constexpr (!M::kWide) f.lo[v] = *reinterpret_cast<const u32x4*>(p + a.hidden_plane);
+            const uint8_t* at = h[n] + step * M::kK * kSize + v * 16;
+#pragma unroll
+            for (int p = 0; p < M::kParts; ++p) f.h[p][v] = *reinterpret_cast<const u32x4*>(at + p * a.hidden_plane);
         }
     });
     constexpr int kPart = Rows * N * kTile * kTile;
@@ -698,11 +717,11 @@ __device__ __forceinline__ void down_tiles(const MoeArgs& a, const Named& e, int
 }
 
 // The same through LDS, two tiles of rows a wave.
-template <class W, int N>
+template <class W, int Parts, int N>
 __device__ __forceinline__ void down_many(const MoeArgs& a, const Named& e, int first, uint8_t* lds) {
-    using M = Down<W>;
-    constexpr int Rows = 2, kPlanes = M::kWide ? 1 : 2, kSize = M::kWide ? 4 : 2;
-    using S = Stage<64 * M::kH * kPlanes, kPlanes, N>;
+    using M = Down<W, Parts>;
+    constexpr int Rows = 2, kSize = M::kWide ? 4 : 2;
+    using S = Stage<64 * M::kH * M::kParts, M::kParts, N>;
     const int lane = lane_id(), sub = lane / kTile;
     const int rank = e.expert / a.per_rank, local = e.expert - rank * a.per_rank;
     const int tile = (blockIdx.x * kManyWaves + threadIdx.x / kWave) * Rows * kTile;
@@ -726,45 +745,45 @@ __device__ __forceinline__ void down_many(const MoeArgs& a, const Named& e, int 
     staged_sums<M, Rows, N, S>(w, size, src, a.hidden_row * kSize, lds, c, [&](const uint8_t* from, int step, int n, typename M::Frag& f) {
 #pragma unroll
         for (int v = 0; v < M::kH; ++v) {
-            const uint8_t* p = from + (n * kTile + lane % kTile) * S::kRow + step * S::kPlane + (sub * M::kH + v) * 16;
-            f.hi[v] = *reinterpret_cast<const u32x4*>(p);
-            if constexpr (!M::kWide) f.lo[v] = *reinterpret_cast<const u32x4*>(p + N * kTile * S::kRow);
+            const uint8_t* at = from + (n * kTile + lane % kTile) * S::kRow + step * S::kPlane + (sub * M::kH + v) * 16;
+#pragma unroll
+            for (int p = 0; p < M::kParts; ++p) f.h[p][v] = *reinterpret_cast<const u32x4*>(at + p * N * kTile * S::kRow);
         }
     });
     write_products<W, Rows, N>(a, rank, local, tile, entry, c);
 }
 
 // blockIdx.x: two tiles of output columns; blockIdx.y: the n-th expert named.
-template <class W>
+template <class W, int Parts>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
     __shared__ __align__(16) float parts[(kWaves - 1) * 2 * 4 * kTile * kTile];
     const Named e = named_of(a)[blockIdx.y];
     if (e.expert < 0 || (e.count <= 2 * kTile && blockIdx.z)) return;
     if (e.count <= kTile) {
-        down_tiles<W, 1>(a, e, 0, parts);
+        down_tiles<W, Parts, 1>(a, e, 0, parts);
     } else if (e.count <= 2 * kTile) {
-        down_tiles<W, 2>(a, e, 0, parts);
+        down_tiles<W, Parts, 2>(a, e, 0, parts);
     } else {
-        for (int first = blockIdx.z * 4 * kTile; first < e.count; first += gridDim.z * 4 * kTile) down_tiles<W, 4>(a, e, first, parts);
+        for (int first = blockIdx.z * 4 * kTile; first < e.count; first += gridDim.z * 4 * kTile) down_tiles<W, Parts, 4>(a, e, first, parts);
     }
 }
 
 // blockIdx.x: kManyWaves times two tiles of output columns.
-template <class W>
+template <class W, int Parts>
 __global__ __launch_bounds__(kManyThreads) void moe_down_many_kernel(MoeArgs a) {
-    using M = Down<W>;
+    using M = Down<W, Parts>;
     constexpr int kMost = kDownMost<W>;
-    __shared__ __align__(16) uint8_t lds[2 * Stage<64 * M::kH * (M::kWide ? 1 : 2), M::kWide ? 1 : 2, kMost>::kSize];
+    __shared__ __align__(16) uint8_t lds[2 * Stage<64 * M::kH * M::kParts, M::kParts, kMost>::kSize];
     const Named e = named_of(a)[blockIdx.y];
     if (e.expert < 0) return;
     if (e.count <= kTile) {
-        down_many<W, 1>(a, e, 0, lds);
+        down_many<W, Parts, 1>(a, e, 0, lds);
     } else if (e.count <= 2 * kTile) {
-        down_many<W, 2>(a, e, 0, lds);
+        down_many<W, Parts, 2>(a, e, 0, lds);
     } else if (e.count <= 4 * kTile) {
-        down_many<W, 4>(a, e, 0, lds);
+        down_many<W, Parts, 4>(a, e, 0, lds);
     } else {
-        for (int first = 0; first < e.count; first += kMost * kTile) down_many<W, kMost>(a, e, first, lds);
+        for (int first = 0; first < e.count; first += kMost * kTile) down_many<W, Parts, kMost>(a, e, first, lds);
     }
 }
 
@@ -812,17 +831,17 @@ unsigned groups(int64_t n, int of) { return (unsigned)((n + of - 1) / of); }
 // for each other and are fewer (16 on 8 of 64: 383 and 362; 16 on 2 of 8: 117 and
 // 74).  Without, entries past 64 to an expert go to workgroups of their own (1024
 // tokens on two experts).  Rows have to hold one step.
-template <class X, class W>
+template <class X, class W, int Parts = 2>
 int run(const MoeArgs& a, hipStream_t s) {
     const int total = a.entries.total(), experts = min(a.num_experts, total);
     const dim3 up(groups(a.hidden_row, kManyWaves * kTile), experts), down(groups(a.width, kManyWaves * 2 * kTile), experts);
     if (total >= 4 * experts && (int)up.x * experts >= 128 && a.width >= 64 && a.inner >= 64) {
         moe_up_many_kernel<X, W><<<up, kManyThreads, 0, s>>>(a);
-        moe_down_many_kernel<W><<<down, kManyThreads, 0, s>>>(a);
+        moe_down_many_kernel<W, Parts><<<down, kManyThreads, 0, s>>>(a);
     } else {
         const unsigned z = groups(total, experts * 4 * kTile);
         moe_up_kernel<X, W><<<dim3(a.hidden_row / kTile, experts, z), kThreads, 0, s>>>(a);
-        moe_down_kernel<W><<<dim3(groups(a.width, 2 * kTile), experts, z), kThreads, 0, s>>>(a);
+        moe_down_kernel<W, Parts><<<dim3(groups(a.width, 2 * kTile), experts, z), kThreads, 0, s>>>(a);
     }
     moe_join_kernel<<<dim3(groups(a.width, 4 * kThreads), total / a.top_k), kThreads, 0, s>>>(a);
     return hipGetLastError();
@@ -833,7 +852,7 @@ int run(const MoeArgs& a, hipStream_t s) {
 int launch_moe(const MoeArgs& a, int dtype, int weight_dtype, void* stream) {
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (dtype == RC_F32) return run<F32, F32>(a, s);
-    if (dtype == RC_E4M3) return run<E4M3, E4M3>(a, s);
+    if (dtype == RC_E4M3) return a.out_dtype == RC_F32 ? run<E4M3, E4M3, 3>(a, s) : run<E4M3, E4M3>(a, s);
     if (weight_dtype == RC_E4M3) return dtype == RC_F16 ? run<F16, E4M3>(a, s) : run<BF16, E4M3>(a, s);
     return dtype == RC_F16 ? run<F16, F16>(a, s) : run<BF16, BF16>(a, s);
 }

@@ -73,10 +73,12 @@ Error check_moe(const char* what, int R, const rc_moe_desc* d, MoeArgs* a, int64
     a->out_dtype = d->out_dtype;
     a->hidden_row = (int32_t)((d->inner + 63) / 64 * 64);
     a->hidden_plane = n * a->hidden_row * 2;
+    // float32 outputs of 8-bit rows: three bfloat16 numbers to a hidden value
+    a->hidden_bytes = a->hidden_plane * (d->dtype == RC_E4M3 && d->out_dtype == RC_F32 ? 3 : 2);
     a->product_row = (int32_t)((d->width + 15) / 16 * 16);
     // the hidden values, the products, the lists
     const int64_t experts = std::min<int64_t>(n, d->num_experts);
-    *workspace = n * (a->hidden_row + a->product_row) * 4 + experts * 16 + (n * 2 + 15) / 16 * 16;
+    *workspace = a->hidden_bytes + n * a->product_row * 4 + experts * 16 + (n * 2 + 15) / 16 * 16;
     return {};
 }
 
@@ -354,7 +356,7 @@ int rc_moe_layer(const rc_moe_desc* desc, const void* const* xs, const float* co
         RC_TRY(b.check());
         const int64_t n = a.entries.total();
         a.hidden = static_cast<uint8_t*>(workspace);
-        a.products = reinterpret_cast<float*>(a.hidden + n * a.hidden_row * 4);
+        a.products = reinterpret_cast<float*>(a.hidden + a.hidden_bytes);
         a.lists = reinterpret_cast<uint8_t*>(a.products + n * a.product_row);
         if (validate_only || !a.entries.total()) return {};
         return device_run([&] { return launch_moe(a, desc->dtype, desc->weight_dtype, stream); });

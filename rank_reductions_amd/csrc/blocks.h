@@ -62,8 +62,9 @@ struct MoeArgs {
     const float* down_scale[kMaxRanks];
     void* y[kMaxRanks];
     RankSpans entries;       // (token, k) of all ranks
-    uint8_t* hidden;         // silu(G x) * (U x) of every entry: [entries][hidden_row], float32, or bfloat16 twice
+    uint8_t* hidden;         // silu(G x) * (U x) of every entry: [entries][hidden_row], float32, or bfloat16 two or three times
     int64_t hidden_plane;    // bytes of all entries' first bfloat16 numbers
+    int64_t hidden_bytes;    // of all
     float* products;         // D times the hidden values: [entries][product_row]
     uint8_t* lists;          // the experts named, and their entries
     int32_t hidden_row;      // elements, a multiple of 64

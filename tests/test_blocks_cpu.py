@@ -212,6 +212,18 @@ def test_moe_workspace(lib):  # noqa: F811
     assert size.value == 24 * (128 + 112) * 4 + 8 * 16 + 48
 
 
+@pytest.mark.parametrize("out,each", [(F32, 6), (BF16, 4), (F16, 4)])
+def test_moe_workspace_of_8bit_rows(lib, out, each):  # noqa: F811
+    """Float32 outputs need a third number for each hidden value; one byte less is refused."""
+    args, (d, *keep) = moe_args(width=100, inner=65, dtype=E4M3, weight_dtype=E4M3, out_dtype=out)
+    size = ctypes.c_int64()
+    assert lib.rc_moe_layer_workspace(args[0], ctypes.byref(size)) == OK
+    assert size.value == 24 * (128 * each + 112 * 4) + 8 * 16 + 48
+    for less, code in ((0, OK), (1, INVAL)):
+        args[-2] = size.value - less
+        assert lib.rc_moe_layer(*args) == code, lib.rc_last_error()
+
+
 # ---------------------------------------------------------------- gradients and steps
 
 def grads_of(sp, counts, dtype=F32):

@@ -212,6 +212,45 @@ def test_a_token_in_a_growing_crowd(experts, width, inner, kind):
             assert torch.equal(y[token], want), top
 
 
+def lone_products(n, experts, inner, dtype, weights, gate, up, down, seed):
+    """Inputs of n tokens with one choice each, whose gates are large (silu(z) = z in float32 from 40 on) and whose rows
+    have one element: the hidden value j of an entry is gate[e, j] * up[e, j] * x, and the output D times them."""
+    x = torch.zeros(n, 64)
+    x[:, 0] = 1.0
+    gu = torch.zeros(experts, 2 * inner, 64)
+    gu[:, :inner, 0], gu[:, inner:, 0] = gate, up
+    t = dict(TYPES, e4m3=E4M3)
+    g = gen(seed)
+    return dict(xs=[x.to(t[dtype])], weights=[torch.ones(n, 1)], experts=[torch.randint(0, experts, (n, 1), generator=g, dtype=torch.int32)],
+                gate_up=[gu.to(t[weights])], down=[down.to(t[weights])], scales=None, gate_up_scales=None, down_scales=None)
+
+
+# entries of two experts without the way through LDS, and of 128 with it
+CROWDS = [(1, 2), (30, 2), (60, 2), (200, 2), (512, 128), (1800, 128)]
+
+
+@pytest.mark.parametrize("n,experts", CROWDS)
+def test_float32_outputs_of_8bit_rows(n, experts):
+    """Outputs that are the hidden values themselves, as of float32: g and u have two roundings each and their product
+    one, the three numbers that hold it add up in the matrix instructions with two more of twice that: 9 u."""
+    inner, g = 64, gen(29)
+    code = torch.arange(1, inner + 1).float()  # 8-bit numbers up to 16, every one of four bits after
+    down = torch.eye(inner).repeat(experts, 1, 1)
+    i = lone_products(n, experts, inner, "e4m3", "e4m3", (code % 15 + 1)[None], (code % 13 - 6.5)[None], down, 31)
+    i["scales"] = [1.0 + torch.rand(n, 1, generator=g)]
+    i["gate_up_scales"] = [40.0 + 10 * torch.rand(experts, 2 * inner, generator=g)]
+    i["down_scales"] = [torch.ones(experts, inner)]
+    with session(1):
+        y = rr.moe_layer(**on_gpu(i), dtype=torch.float32)[0]
+        torch.cuda.synchronize()
+    e = i["experts"][0][:, 0].long()
+    w = i["gate_up"][0].double()[:, :, 0] * i["gate_up_scales"][0].double()
+    gate, up = (w[e] * i["scales"][0].double()).split(inner, 1)
+    want = gate * up
+    assert gate.min() >= 40
+    near(y.cpu().double().numpy(), want.numpy(), 9.1 * U * want.abs().numpy(), "hidden values")
+
+
 def test_graph_replays():
     i = inputs([2, 3], 8, 2, 256, 128, "bf16", "bf16", 15)
     with session(2):
