@@ -168,7 +168,9 @@ struct Down {
             BF16::unpack(first, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) l[i] = __builtin_isfinite(g[i]) ? e[i] - g[i] : 0.0f;
-            return mma_bf16(first, f.h[1][0], mma_bf16(BF16::pack(l), f.h[0][0], mma_bf16(first, f.h[0][0], c)));
+            const u32x4 second = BF16::pack(l);
+            c = mma_bf16(second, f.h[0][0], mma_bf16(first, f.h[0][0], c));
+            return mma_bf16(second, f.h[1][0], mma_bf16(first, f.h[1][0], c));
         } else {
             return mma_bf16(w, f.h[1][0], mma_bf16(w, f.h[0][0], c));
         }

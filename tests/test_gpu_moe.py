@@ -251,6 +251,31 @@ def test_float32_outputs_of_8bit_rows(n, experts):
     near(y.cpu().double().numpy(), want.numpy(), 9.1 * U * want.abs().numpy(), "hidden values")
 
 
+@pytest.mark.parametrize("n,experts", CROWDS)
+def test_float16_weights_less_their_first_eight_bits(n, experts):
+    """Outputs (f + l) h - f h with f of eight bits and h of thirteen: l h, to which the smaller halves of the weight and
+    of the hidden value add up to 2^-9 by themselves.  Sums of six terms up to f h, each off by 2 u at most, and half a
+    step."""
+    inner = 64
+    j = torch.arange(inner // 2)
+    weight = 1 + (37 * j % 1024).float() * 2.0 ** -10
+    first = weight.to(torch.bfloat16).float()
+    down = torch.zeros(experts, 64, inner)
+    down[:, j, 2 * j], down[:, j, 2 * j + 1] = weight, -first
+    up = (1 + ((torch.arange(experts)[:, None] * 91 + 53 * j + 5) % 1024).float() * 2.0 ** -10).repeat_interleave(2, 1)
+    i = lone_products(n, experts, inner, "f16", "f16", torch.tensor(48.0), up, down, 33)
+    with session(1):
+        y = rr.moe_layer(**on_gpu(i))[0]
+        torch.cuda.synchronize()
+    e = i["experts"][0][:, 0].long()
+    h = 48 * up.double()[e][:, ::2]
+    want = torch.zeros(n, 64, dtype=torch.float64)
+    want[:, :inner // 2] = (weight - first).double() * h
+    bound = HALF["f16"] * want.abs() + TINY["f16"]
+    bound[:, :inner // 2] += 12 * U * first.double() * h
+    near(y.cpu().double().numpy(), want.numpy(), bound.numpy(), "small halves")
+
+
 def test_graph_replays():
     i = inputs([2, 3], 8, 2, 256, 128, "bf16", "bf16", 15)
     with session(2):
