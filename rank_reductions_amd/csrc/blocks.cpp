@@ -528,6 +528,19 @@ int rc_adamw_step(const rc_adamw_desc* desc, const void* table, void* table_on_g
         b.write(table_on_gpu, from->bytes, 1, "table", 0);
         if (!in_place) b.read(out_table_on_gpu, to->bytes, 1, "out_table", 0);
         RC_TRY(b.check());
+        // neither of the tables may be stepped over, nor a gradient written before it is read
+        struct Small {
+            uintptr_t lo, hi;
+            const char* name;
+        };
+        const auto at = [](const void* p, int64_t bytes, const char* name) {
+            return Small{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes, name};
+        };
+        const Small smalls[] = {at(table_on_gpu, from->bytes, "the table"), at(out_table_on_gpu, to->bytes, "the out_table"),
+                                at(desc->steps_out, (int64_t)R * 4, "steps_out")};
+        for (const Small& s : smalls)
+            if (in_spans(to, s.lo, s.hi) || in_spans(from, s.lo, s.hi))
+                return bad(what, std::string(s.name) + " overlaps a parameter's buffers");
         const AdamwEntry* entries = part<AdamwEntry>(from, from->entries_at);
         for (int r = 0; r < R; ++r) {
             const int n = from->first[r + 1] - from->first[r];
@@ -541,8 +554,10 @@ int rc_adamw_step(const rc_adamw_desc* desc, const void* table, void* table_on_g
                 auto wrong = [&](const std::string& how) { return bad(what, fmt("rank %lld, gradient %lld: ", r, i) + how); };
                 if (g.count != e.count) return wrong(fmt("%lld elements, the parameter has %lld", g.count, e.count));
                 if (g.dtype != RC_F32 && g.dtype != e.dtype) return wrong(fmt("dtype %lld is neither RC_F32 nor the parameter's", g.dtype));
-                const auto lo = reinterpret_cast<uintptr_t>(g.grad);
-                if (in_spans(to, lo, lo + (uint64_t)(g.count * row_element_size(g.dtype)))) return wrong("overlaps a parameter's buffers");
+                const auto lo = reinterpret_cast<uintptr_t>(g.grad), hi = lo + (uintptr_t)(g.count * row_element_size(g.dtype));
+                if (in_spans(to, lo, hi)) return wrong("overlaps a parameter's buffers");
+                for (const Small& s : smalls)
+                    if (lo < s.hi && s.lo < hi) return wrong(std::string("overlaps ") + s.name);
             }
         }
         if (validate_only) return {};

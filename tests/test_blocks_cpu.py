@@ -402,6 +402,29 @@ def test_table_refuses(lib):  # noqa: F811
     assert s.table() == OK
 
 
+@pytest.mark.parametrize("out", [0, 1])
+def test_step_refuses_tables_among_its_buffers(lib, out):  # noqa: F811
+    """A table on the GPU that lies in a parameter's buffer would be stepped over while kernels go by it; gradients that
+    the step writes before it reads them."""
+    for which in range(out + 1):
+        for k in ("param", "master", "m", "v"):
+            s = Steps(lib)
+            assert s.table(0) == OK and s.table(1) == OK
+            s.gpu[which] = getattr(s.params[which][1][2], k) + 64 & ~15
+            assert s.step(out=out, steps_out=s.out_steps) == INVAL, (which, k)
+            assert b"overlap" in lib.rc_last_error()
+        s = Steps(lib)
+        s.gpu[0] = s.params[which][0][0].v & ~15
+        assert s.table(0) == OK and s.table(1) == OK
+        assert s.step(out=out, steps_out=s.out_steps) == INVAL
+    for at in ("gpu", "out_steps"):
+        s = Steps(lib)
+        assert s.table(0) == OK and s.table(1) == OK
+        s.grads[1][2].grad = s.gpu[0] + 512 if at == "gpu" else s.out_steps + 4
+        assert s.step(out=out, steps_out=s.out_steps) == INVAL, at
+        assert b"gradient 2: overlaps" in lib.rc_last_error()
+
+
 def test_step_refuses(lib):  # noqa: F811
     s = Steps(lib)
     assert s.table(0) == OK and s.table(1) == OK
