@@ -284,7 +284,9 @@ int run_norm(const NormArgs& a, hipStream_t s) {
 
 // Short rows take a wave each, longer ones four to sixteen waves with a few
 // vectors a lane (16384 rows of 4096 bf16: 84 us with four waves of two vectors,
-// 105 with one of eight; 64 rows: 4.4 and 7.6 us), in steps that leave few lanes idle.
+// 105 with one of eight; 64 rows: 4.4 and 7.6 us), in steps that leave few lanes idle
+// (4096 rows of 17000: 118 us with three vectors a lane, 127 with four; of 24576: 153
+// and 159).
 template <class T, class W>
 int norm_of(const NormArgs& a, hipStream_t s) {
     const int64_t vectors = (a.width + T::n - 1) / T::n;
@@ -296,6 +298,7 @@ int norm_of(const NormArgs& a, hipStream_t s) {
     if (vectors <= 1024) return run_norm<T, W, 4, 4>(a, s);
     if (vectors <= 1536) return run_norm<T, W, 8, 3>(a, s);
     if (vectors <= 2048) return run_norm<T, W, 8, 4>(a, s);
+    if (vectors <= 3072) return run_norm<T, W, 16, 3>(a, s);
     if constexpr (T::n == 4)
         if (vectors > 4096) return run_norm<T, W, 16, 8>(a, s);
     return run_norm<T, W, 16, 4>(a, s);
