@@ -719,10 +719,7 @@ typedef struct rc_adamw_desc {
  * rounded to nearest even.  sqrt(v) is rounded up or down by chance, in
  * proportion to the distance (rounding to nearest would never let go of a value
  * that changes by a thousandth each step), and to no less than the smallest
- * code unless it is zero.  Where m was one of the seven smallest codes and is rounded
- * back to it, p takes no step by m / (...) (it would be held for ever, and divided by
- * a root that decays).  A steady gradient's m comes no nearer to it than half a code /
- * (1 - beta1): 0.62 of it in the worst case with beta1 = 0.9.  The chance of element i, u / 2^16 <= the part above the
+ * code unless it is zero.  The chance of element i, u / 2^16 <= the part above the
  * code below, is a function of seed, t and i alone, so ranks that hold the same
  * parameters keep them alike.  A gradient that is not finite spoils its element,
  * or block of an 8-bit state; give norms to leave such a step out.

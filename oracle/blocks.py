@@ -72,33 +72,6 @@ def adamw(p, g, m, v, t, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-
     return p - lr * weight_decay * p - lr * update, m, v
 
 
-def e4m3(x):
-    """x to the nearest e4m3 value (ties to even), 448 at most."""
-    x = np.asarray(x, np.float64)
-    a = np.minimum(np.abs(x), E4M3_MOST)
-    step = 2.0 ** (np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3)
-    return np.sign(x) * np.minimum(np.rint(a / step) * step, E4M3_MOST)
-
-
-def held(code, scale, m):
-    """Whether m, the mean after a step of one that was code * scale, is held by its rounding among the smallest codes."""
-    return (code != 0) & (np.abs(code) < 2.0 ** -6) & (e4m3(m / np.where(scale > 0, scale, 1.0)) == code)
-
-
-def adamw8(p, g, m_code, m_scale, v_code, v_scale, t, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, seed=0):
-    """One block of a parameter with 8-bit states after step t: (p, m_code, m_scale, v_code, v_scale), codes as values."""
-    stepped, m, v = adamw(p, g, m_code * m_scale, (v_code * v_scale) ** 2, t, lr, betas, eps, weight_decay)
-    p = np.where(held(m_code, m_scale, m), p * (1 - lr * weight_decay), stepped)
-    r = np.sqrt(v)
-    most = np.abs(m).max(), r.max()
-    m_scale, v_scale = (0.0 if x < LEAST else x / E4M3_MOST for x in most)
-    m_code = e4m3(m / m_scale) if m_scale else np.zeros_like(m)
-    x = np.minimum(r / v_scale, E4M3_MOST) if v_scale else np.zeros_like(r)
-    step = 2.0 ** (np.floor(np.log2(np.maximum(x, 2.0 ** -6))) - 3)
-    v_code = np.minimum(np.floor(x / step + chances(x.size, t, seed)) * step, E4M3_MOST)
-    return p, m_code, m_scale, np.where(x > 0, np.maximum(v_code, 2.0 ** -9), 0.0), v_scale
-
-
 # ---------------------------------------------------------------- experts
 
 def moe_token(x, weights, experts, gate_up, down):

@@ -200,21 +200,6 @@ __device__ __forceinline__ float by_chance(float x, uint32_t u) {
     return x > 0.0f && c < 0x1p-9f ? 0x1p-9f : c;
 }
 
-// The codes c of four means that held values of less than 2^-6 of their scale, where
-// the means m after the step round back to them: bytes of them, zeros for the others.
-// Rounding to nearest would keep such a mean for ever without a gradient (0.9 of one
-// to four of the smallest codes rounds to as many), while the root that divides it
-// decays, and the parameter would go on by as much as the rate in every step.  It is
-// below 2^-15 of the block's largest: without a step for it, nothing is lost.
-__device__ __forceinline__ uint32_t held_codes(uint32_t c, float scale, const float* m) {
-    const float per = 1.0f / scale;
-    uint32_t held = 0;
-    const uint32_t moved = (e4m3_of(m[0] * per, m[1] * per, m[2] * per, m[3] * per) ^ c) | (c & 0x78787878u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) held |= moved >> (8 * i) & 0xff ? 0 : c & 7u << (8 * i);
-    return held;
-}
-
 // One step of the chunk [from, to) of a parameter with a gradient: four elements a
 // lane, so that a wave holds a block of 256, and two blocks ahead, which leaves
 // registers for eight waves a SIMD.
@@ -258,13 +243,7 @@ __device__ __forceinline__ void step_chunk(const AdamwArgs& a, const AdamwEntry&
                 m[k][i] = a.beta1 * m[k][i] + a.rest1 * x;
                 v[k][i] = a.beta2 * v[k][i] + a.rest2 * (x * x);
                 r[i] = sqrtf(v[k][i]);
-            }
-            uint32_t held = 0;
-            if constexpr (Bits == 8) held = held_codes(mc[k], ms[k], m[k]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float step = c.rate * m[k][i] / (r[i] * c.root + a.eps);
-                p[k][i] = p[k][i] * c.keep - (held >> (8 * i) & 0xff ? 0.0f : step);
+                p[k][i] = p[k][i] * c.keep - c.rate * m[k][i] / (r[i] * c.root + a.eps);
             }
             if constexpr (P::n == 4) {
                 store4<F32, Full>(o.param, at, to, p[k]);

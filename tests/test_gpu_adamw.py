@@ -306,61 +306,6 @@ def test_chances_are_even():
     assert abs(np.corrcoef(c[:-1], c[1:])[0, 1]) < 0.01 and abs(np.corrcoef(c, orc.chances(1 << 18, 6, 1))[0, 1]) < 0.01
 
 
-def test_smallest_codes_that_a_step_holds():
-    """Means of the smallest codes, with gradients that move them by parts of a code, or far: only those that are rounded
-    back, up to seven codes, leave their parameter alone but for the decay."""
-    with session(1):
-        n, unit, rest = 256 * 60, 2.0 ** -9 / 448, 0.1
-        j = torch.arange(n)
-        code = (1 + j % 15).float() * 2.0 ** -9 * torch.where(j // 15 % 2 == 0, 1.0, -1.0)
-        code[::256] = 448.0  # the block's scale
-        move = torch.tensor([0.0, 0.2, -0.2, 0.7, -1.3, 3.1, 40.0])[j // 30 % 7] * unit
-        move[::256] = 0.1
-        g = (move / rest).to(DEV)
-        p = torch.randn(n, generator=gen(3)).to(DEV)
-        state = rr.adamw_state([{0: p}], bits=8)
-        state.step += 50
-        state.m[0][0].copy_(code.to(torch.float8_e4m3fn))
-        state.m_scale[0][0].fill_(1 / 448)
-        state.v[0][0].copy_(torch.full((n,), 64 * 2.0 ** -9).to(torch.float8_e4m3fn))
-        state.v_scale[0][0].fill_(1 / 448)
-        before = read(state, 0, 0)
-        rr.adamw_step(state, [{0: g}], lr=0.01)
-        torch.cuda.synchronize()
-        want, m, v = orc.adamw(before[0], d64(g), before[1], before[2], 51, 0.01)
-        c, scale = code.double().numpy(), float(np.float32(1 / 448))
-        held = orc.held(c, scale, m)
-        part = np.abs(m / scale) * 512 % 1
-        sure = (np.abs(part - 0.5) > 1e-3) | (np.abs(c) >= 2.0 ** -6)
-        assert 0.05 < (held & sure).mean() < 0.5 and sure.mean() > 0.9 and set(np.abs(c[held & sure]) * 512) == {1, 2, 3, 4, 5, 6, 7}
-        am = np.abs(0.9 * before[1]) + np.abs(rest * d64(g))
-        denom = np.sqrt(v / (1 - 0.999 ** 51)) + 1e-8
-        bound = 1.01 * U * (24 * 0.01 / (1 - 0.9 ** 51) * am / denom + 4 * np.abs(before[0]))
-        want = np.where(held, before[0] * (1 - 0.01 * 1e-2), want)
-        near(d64(p)[sure], want[sure], bound[sure], "p")
-
-
-def test_means_without_a_gradient_come_to_rest():
-    """As on the CPU: half of each block loses its gradient, one element holds its scale; from step 400 on the idle
-    parameters do not move by a bit."""
-    with session(1):
-        n = 256 * 8
-        g = gen(6)
-        p = torch.zeros(n, device=DEV)
-        state = rr.adamw_state([{0: p}], bits=8)
-        idle = torch.arange(n, device=DEV) % 2 == 1
-        noise = torch.randn(64, n, generator=g).to(DEV)
-        noise[:, ::256] = 8.0
-        quiet = torch.where(idle, 0.0, noise)
-        for t in range(3000):
-            rr.adamw_step(state, [{0: (noise if t < 20 else quiet)[t % 64]}], lr=0.01, weight_decay=0.0)
-            if t == 400:
-                rest = p.clone()
-        torch.cuda.synchronize()
-        assert torch.equal(p[idle], rest[idle]) and p[idle].all() and not torch.equal(p, rest)
-        assert state.m[0][0].float()[idle].ne(0).float().mean() > 0.9
-
-
 def test_steps_captured_into_a_graph():
     """Replays go on counting; lr from the GPU; each replay bit for bit the eager step."""
     with session(2):
