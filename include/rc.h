@@ -715,12 +715,16 @@ typedef struct rc_adamw_desc {
  *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * in float32, p being the master copy where there is one and the parameter then
  * p to nearest even.  8-bit states: a block's scale is its largest absolute
- * value over 448 (0, and all zeros, where that value is below 2^-117); m is
- * rounded to nearest even.  sqrt(v) is rounded up or down by chance, in
+ * value over 448 (0, and all zeros, where that value is below 2^-117).  m is
+ * rounded to nearest even, but without a gradient (|g| below 2^-6 of the block's
+ * scale before) by chance, as sqrt(v) and to zero too, where (1 - beta1) of it is less
+ * than half the distance of codes: to nearest it would stay for ever.  (With a
+ * gradient it comes as near to a steady one as half a code / (1 - beta1), 0.62 of
+ * it in the worst case with beta1 = 0.9; noise evens that out.)  sqrt(v) is rounded up or down by chance, in
  * proportion to the distance (rounding to nearest would never let go of a value
  * that changes by a thousandth each step), and to no less than the smallest
  * code unless it is zero.  The chance of element i, u / 2^16 <= the part above the
- * code below, is a function of seed, t and i alone, so ranks that hold the same
+ * code below, is a function of seed, t and i alone (another one for m), so ranks that hold the same
  * parameters keep them alike.  A gradient that is not finite spoils its element,
  * or block of an 8-bit state; give norms to leave such a step out.
  * The states are read from `table` and written to `out_table`, another

@@ -47,9 +47,11 @@ def mix(x):
     return x ^ (x >> 16)
 
 
-def chances(n, step, seed):
-    """The chance of each of n elements at a step, in [0, 1)."""
+def chances(n, step, seed, of_means=False):
+    """The chance of each of n elements at a step, in [0, 1): for the root of v, or for m."""
     key = mix(int(mix(step)) + seed)
+    if of_means:
+        key = key ^ np.uint64(0x6A09E667)
     pair = np.arange((n + 1) // 2, dtype=np.uint64)
     h = mix(key + pair + 0xBB67AE85 * (pair >> 32))
     return np.stack([h & 0xFFFF, h >> 16], axis=1).reshape(-1)[:n] / 65536.0
@@ -70,6 +72,44 @@ def adamw(p, g, m, v, t, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-
     v = betas[1] * v + (1 - betas[1]) * g * g
     update = m / (1 - betas[0] ** t) / (np.sqrt(v / (1 - betas[1] ** t)) + eps)
     return p - lr * weight_decay * p - lr * update, m, v
+
+
+def distance(x):
+    """From an e4m3 value x >= 0 to the next."""
+    return 2.0 ** (np.floor(np.log2(np.maximum(x, 2.0 ** -6))) - 3)
+
+
+def e4m3(x):
+    """x to the nearest e4m3 value (ties to even), 448 at most."""
+    x = np.asarray(x, np.float64)
+    a = np.minimum(np.abs(x), E4M3_MOST)
+    return np.sign(x) * np.minimum(np.rint(a / distance(a)) * distance(a), E4M3_MOST)
+
+
+def by_chance(x, chance):
+    """x >= 0 to the e4m3 value below, or where the part above and the chance reach a step to the one above."""
+    x = np.minimum(x, E4M3_MOST)
+    return np.minimum(np.floor(x / distance(x) + chance) * distance(x), E4M3_MOST)
+
+
+def mean_codes(y, g, scale_before, beta1, chance):
+    """Means in units of their new scale, y, as e4m3: to nearest, those that it would hold without a gradient by chance."""
+    a = np.abs(y)
+    held = (np.abs(g) < 2.0 ** -6 * scale_before) & ((1 - beta1) * a < distance(a) / 2)
+    return np.where(held, np.sign(y) * by_chance(a, chance), e4m3(y)), held
+
+
+def adamw8(p, g, m_code, m_scale, v_code, v_scale, t, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, seed=0):
+    """One block of a parameter with 8-bit states after step t: (p, m_code, m_scale, v_code, v_scale), codes as values."""
+    p, m, v = adamw(p, g, m_code * m_scale, (v_code * v_scale) ** 2, t, lr, betas, eps, weight_decay)
+    r, before = np.sqrt(v), m_scale
+    m_scale, v_scale = (0.0 if x < LEAST else x / E4M3_MOST for x in (np.abs(m).max(), r.max()))
+    m_code, v_code = np.zeros_like(m), np.zeros_like(r)
+    if m_scale:
+        m_code = mean_codes(m / m_scale, g, before, betas[0], chances(m.size, t, seed, True))[0]
+    if v_scale:
+        v_code = np.where(r > 0, np.maximum(by_chance(r / v_scale, chances(r.size, t, seed)), 2.0 ** -9), 0.0)
+    return p, m_code, m_scale, v_code, v_scale
 
 
 # ---------------------------------------------------------------- experts

@@ -167,6 +167,8 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
     return x ^ (x >> 16);
 }
 
+constexpr uint32_t kOfMeans = 0x6A09E667u;  // sets the chances of m apart from those of the root of v
+
 // One lane for each rank: its factors, its step counted.
 __global__ __launch_bounds__(kWave) void adamw_begin_kernel(AdamwBegin a) {
     const int r = threadIdx.x;
@@ -189,20 +191,46 @@ __global__ __launch_bounds__(kWave) void adamw_begin_kernel(AdamwBegin a) {
     a.steps_out[r] = t;
 }
 
+// The exponent's bits of x >= 0 among e4m3 values, whose distance is 2^-3 of theirs:
+// values below 2^-6 lie as far apart as those above.
+__device__ __forceinline__ uint32_t octave(float x) { return max(__builtin_bit_cast(uint32_t, x) >> 23, 127u - 6); }
+
 // Values in [0, 448] as e4m3, each rounded up with the chance `u` / 2^16 <= its
-// distance from the value below, zero to zero and others to no less than 2^-9.
+// distance from the value below.
 __device__ __forceinline__ float by_chance(float x, uint32_t u) {
     x = x > kE4M3Most ? kE4M3Most : x;
-    const uint32_t e = max(__builtin_bit_cast(uint32_t, x) >> 23, 127u - 6);  // values below 2^-6 lie as far apart as those above
+    const uint32_t e = octave(x);
     const float step = __builtin_bit_cast(float, (e - 3) << 23), per = __builtin_bit_cast(float, (257 - e) << 23);
     const float q = floorf(__builtin_fmaf(x, per, (float)u * 0x1p-16f)) * step;
-    const float c = q > kE4M3Most ? kE4M3Most : q;
+    return q > kE4M3Most ? kE4M3Most : q;
+}
+// The same, zero to zero and others to no less than 2^-9.
+__device__ __forceinline__ float root_by_chance(float x, uint32_t u) {
+    const float c = by_chance(x, u);
     return x > 0.0f && c < 0x1p-9f ? 0x1p-9f : c;
+}
+
+// Four means m, of which a step left `rest` off, times what takes their block to e4m3.
+// Those that are `idle` (bits of it), whose gradients were below the eighth of the
+// smallest codes they had, and whose decay is less than half the distance of codes, are rounded by chance:
+// to nearest they would stay for ever where others hold the block's scale, and move
+// their parameters as far as the root that divides them has decayed.
+__device__ __forceinline__ void round_means(const float* m, uint32_t idle, float rest, float mf, uint32_t key, float* q) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = m[i] * mf;
+    if (!__any(idle != 0)) return;
+    const uint32_t u = mix(key), w = mix(key + 1);
+    const uint32_t chance[4] = {u & 0xffff, u >> 16, w & 0xffff, w >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float y = fabsf(q[i]), half = __builtin_bit_cast(float, (octave(y) - 4) << 23);
+        if ((idle >> i & 1) && rest * y < half) q[i] = copysignf(by_chance(y, chance[i]), q[i]);
+    }
 }
 
 // One step of the chunk [from, to) of a parameter with a gradient: four elements a
 // lane, so that a wave holds a block of 256, and two blocks ahead, which leaves
-// registers for eight waves a SIMD.
+// registers for eight waves a SIMD, for seven with states of 8 bits.
 template <class P, class G, int Bits, bool Full>
 __device__ __forceinline__ void step_chunk(const AdamwArgs& a, const AdamwEntry& e, const AdamwEntry& o, const void* grad,
                                            const AdamwFactors& c, int64_t from, int64_t to) {
@@ -236,10 +264,14 @@ __device__ __forceinline__ void step_chunk(const AdamwArgs& a, const AdamwEntry&
                 values_of(vc[k], vs[k], v[k]);
             }
             float r[4];
+            uint32_t idle = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float x = g[k][i] * c.grad;
-                if constexpr (Bits == 8) v[k][i] *= v[k][i];
+                if constexpr (Bits == 8) {
+                    idle |= (uint32_t)(fabsf(x) < ms[k] * 0x1p-6f) << i;
+                    v[k][i] *= v[k][i];
+                }
                 m[k][i] = a.beta1 * m[k][i] + a.rest1 * x;
                 v[k][i] = a.beta2 * v[k][i] + a.rest2 * (x * x);
                 r[i] = sqrtf(v[k][i]);
@@ -264,11 +296,13 @@ __device__ __forceinline__ void step_chunk(const AdamwArgs& a, const AdamwEntry&
                 const float mf = e4m3_factor(mm), rf = e4m3_factor(rr);
                 // the chances of elements 2i and 2i + 1 are the halves of one number
                 const uint64_t pair = (uint64_t)at >> 1;
-                const uint32_t key = c.key + (uint32_t)pair + 0xBB67AE85u * (uint32_t)(pair >> 32);
-                const uint32_t u = mix(key), w = mix(key + 1);
-                store_codes<Full>(o.m, at, to, e4m3_of(m[k][0] * mf, m[k][1] * mf, m[k][2] * mf, m[k][3] * mf));
-                store_codes<Full>(o.v, at, to, e4m3_of(by_chance(r[0] * rf, u & 0xffff), by_chance(r[1] * rf, u >> 16),
-                                                       by_chance(r[2] * rf, w & 0xffff), by_chance(r[3] * rf, w >> 16)));
+                const uint32_t place = (uint32_t)pair + 0xBB67AE85u * (uint32_t)(pair >> 32);
+                const uint32_t u = mix(c.key + place), w = mix(c.key + place + 1);
+                float q[4];
+                round_means(m[k], idle, a.rest1, mf, (c.key ^ kOfMeans) + place, q);
+                store_codes<Full>(o.m, at, to, e4m3_of(q[0], q[1], q[2], q[3]));
+                store_codes<Full>(o.v, at, to, e4m3_of(root_by_chance(r[0] * rf, u & 0xffff), root_by_chance(r[1] * rf, u >> 16),
+                                                       root_by_chance(r[2] * rf, w & 0xffff), root_by_chance(r[3] * rf, w >> 16)));
                 if (lane_id() == 0 && (Full || at < to)) {
                     o.m_scale[block] = e4m3_scale(mm);
                     o.v_scale[block] = e4m3_scale(rr);

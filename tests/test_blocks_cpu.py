@@ -45,6 +45,54 @@ def test_adamw_by_hand():
     assert abs(p[0] - (1 - 0.05 - 0.1)) < 1e-12  # the first step's update is the gradient's sign
 
 
+def test_8bit_codes_of_means():
+    """Codes to nearest against torch's own, and those by chance: no more than a step away, right on the average."""
+    rng = np.random.default_rng(2)
+    x = np.concatenate([rng.normal(size=4000) * 10.0 ** rng.integers(-4, 3, size=4000), [0, 448, 460, 2.0 ** -9, 2.0 ** -10, 3 * 2.0 ** -10]])
+    near = torch.tensor(np.clip(x, -448, 448), dtype=torch.float64).to(torch.float32).to(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(orc.e4m3(x), near)
+    c, held = orc.mean_codes(x, np.ones_like(x), 1.0, 0.9, 0.5)
+    assert np.array_equal(c, near) and not held.any()
+    # 0.9 k rounds to k for one to four of the smallest codes; 0.95 k up to ten, and for nine and ten eighths of the 14
+    # octaves above; 0.99 k for all
+    k = np.unique(orc.e4m3(2.0 ** np.linspace(-9, 8.8, 2000)))
+    for beta, kept in ((0.9, 4), (0.95, 10 + 2 * 14), (0.99, k.size)):
+        stays = orc.e4m3(beta * k) == k
+        assert stays.sum() == kept and not (stays & ~orc.mean_codes(beta * k, 0 * k, 1.0, beta, 0.5)[1]).any()
+    y = np.full(1 << 16, -3.6 * 2.0 ** -9)
+    c, held = orc.mean_codes(y, np.zeros_like(y), 1.0, 0.9, np.arange(1 << 16) / 65536)
+    assert held.all() and set(c * 512) == {-4.0, -3.0} and abs(c.mean() / y[0] - 1) < 1e-4
+
+
+@pytest.mark.parametrize("beta1", [0.9, 0.95, 0.99])
+@pytest.mark.parametrize("steady", [True, False])
+@pytest.mark.parametrize("tiny", [0.0, 1e-9])
+def test_8bit_means_without_a_gradient_go(beta1, steady, tiny):
+    """Half a block loses its gradient after 20 steps (or keeps next to none of it); the rest go on, one of them with a
+    steady gradient that holds the scale.  To nearest the idle means would stay, and their parameters drift by up to
+    the rate and far more in every step.  By chance a mean of up to 2^18 of the smallest codes decays on the average as
+    it should, and is gone when that falls to 2^-18 codes: ln(2^36) / (1 - beta1) < 25 / (1 - beta1) steps on (a
+    chance of 256 * 2^-18 that one is left).  Its parameter stays from then on.  With 1e-9 of a gradient a mean may
+    now and then be one smallest code: 8 / 448 * 2^-9 at most, over a root whose square is 0.02 of the mean of twenty
+    squares, 0.3 or more, and decays by 0.999 a step; twice that for the root's own rounding."""
+    rng = np.random.default_rng(5)
+    idle = np.arange(256) % 2 == 1
+    state = np.zeros(256), np.zeros(256), 0.0, np.zeros(256), 0.0
+    gone = 20 + int(25 / (1 - beta1))
+    for t in range(1, gone + 2001):
+        g = rng.normal(size=256)
+        if t > 20:
+            g[idle] *= tiny
+        if steady:
+            g[0] = 8.0
+        state = orc.adamw8(state[0], g, *state[1:], t, weight_decay=0.0, betas=(beta1, 0.999))
+        if t == gone:
+            rest = state[0][idle]
+    assert (np.abs(state[1][idle]) <= (2.0 ** -9 if tiny else 0)).all() and state[1][~idle].any()
+    moved = np.abs(state[0][idle] - rest).max()
+    assert moved <= (2 * 2000 * 1e-3 * 8 / 448 * 2.0 ** -9 / (0.02 * 0.3 * 0.999 ** t) ** 0.5 if tiny else 0)
+
+
 def test_adamw_follows_torch():
     rng = np.random.default_rng(1)
     x = torch.tensor(rng.normal(size=40), dtype=torch.float64, requires_grad=True)

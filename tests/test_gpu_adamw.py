@@ -306,6 +306,67 @@ def test_chances_are_even():
     assert abs(np.corrcoef(c[:-1], c[1:])[0, 1]) < 0.01 and abs(np.corrcoef(c, orc.chances(1 << 18, 6, 1))[0, 1]) < 0.01
 
 
+@pytest.mark.parametrize("beta1", [0.9, 0.99])
+def test_codes_of_means_without_a_gradient(beta1):
+    """Every one of the smaller codes, with gradients of nothing, next to nothing, and more: by chance where the oracle
+    says, to nearest otherwise; the parameter's step is that of any other element."""
+    with session(1):
+        n = 256 * 128
+        j = torch.arange(n)
+        code = (j % 120 + 1).to(torch.uint8).view(torch.float8_e4m3fn).float() * torch.where(j // 120 % 2 == 0, 1.0, -1.0)
+        code[::256] = 448.0  # the block's scale
+        scale = 2.0 ** -4
+        g = torch.tensor([0.0, 2.0 ** -9, -2.0 ** -7, 2.0 ** -5, 40.0])[j // 240 % 5] * scale
+        g[::256] = 448.0 * scale
+        p = torch.randn(n, generator=gen(3)).to(DEV)
+        state = rr.adamw_state([{0: p}], bits=8)
+        state.step += 50
+        state.m[0][0].copy_(code.to(torch.float8_e4m3fn))
+        state.m_scale[0][0].fill_(scale)
+        state.v[0][0].copy_(torch.full((n,), 64 * 2.0 ** -9).to(torch.float8_e4m3fn))
+        state.v_scale[0][0].fill_(scale)
+        before = read(state, 0, 0)
+        rr.adamw_step(state, [{0: g.to(DEV)}], lr=0.01, betas=(beta1, 0.999), seed=77)
+        torch.cuda.synchronize()
+        want_p, m, v = orc.adamw(before[0], d64(g), before[1], before[2], 51, 0.01, (beta1, 0.999))
+        y = m / (np.abs(orc.blocks(m)).max() / 448)
+        chance = orc.chances(n, 51, 77, True)
+        want, held = orc.mean_codes(y, d64(g), scale, beta1, chance)
+        a, step = np.abs(y), orc.distance(np.abs(y))
+        part = a / step % 1
+        # the rest may fall either way: at a border of the chance or of the half, of the octaves, of the rule
+        sure = np.where(held, np.abs((part + chance + 0.5) % 1 - 0.5) > 1e-4, np.abs(part - 0.5) > 1e-4)
+        sure &= (np.abs((1 - beta1) * a / (step / 2) - 1) > 1e-5) & (np.abs(np.abs(np.log2(a)) % 1 - 0.5) < 0.4999)
+        got = d64(state.m[0][0].float())
+        assert sure.mean() > 0.8 and 0.02 < held.mean() < 0.7
+        assert np.array_equal(got[sure], want[sure])
+        assert (got != orc.e4m3(y))[held & sure].any()
+        am = np.abs(beta1 * before[1]) + np.abs((1 - beta1) * d64(g))
+        denom = np.sqrt(v / (1 - 0.999 ** 51)) + 1e-8
+        near(d64(p), want_p, 1.01 * U * (24 * 0.01 / (1 - beta1 ** 51) * am / denom + 4 * np.abs(before[0])), "p")
+
+
+def test_means_without_a_gradient_go():
+    """As on the CPU: half of each block loses its gradient, one element holds its scale; from step 300 on the idle
+    parameters have means of zero and do not move by a bit."""
+    with session(1):
+        n = 256 * 8
+        g = gen(6)
+        p = torch.zeros(n, device=DEV)
+        state = rr.adamw_state([{0: p}], bits=8)
+        idle = torch.arange(n, device=DEV) % 2 == 1
+        noise = torch.randn(64, n, generator=g).to(DEV)
+        noise[:, ::256] = 8.0
+        quiet = torch.where(idle, 0.0, noise)
+        for t in range(2000):
+            rr.adamw_step(state, [{0: (noise if t < 20 else quiet)[t % 64]}], lr=0.01, weight_decay=0.0, seed=t)
+            if t == 300:
+                rest = p.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(p[idle], rest[idle]) and p[idle].all() and not torch.equal(p, rest)
+        assert not state.m[0][0].float()[idle].any()
+
+
 def test_steps_captured_into_a_graph():
     """Replays go on counting; lr from the GPU; each replay bit for bit the eager step."""
     with session(2):
