@@ -20,10 +20,6 @@ __device__ __forceinline__ float dpp(float v) {
 }
 constexpr int kSwap1 = 0xb1, kSwap2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140;
 
-__device__ __forceinline__ float of_lane(float v, int lane) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
-}
-
 // The sum over the wave's lanes, alike in all of them: pairs, quads, eights and
 // sixteens, then the four sixteens.
 __device__ __forceinline__ float wave_sum(float v) {
@@ -31,7 +27,7 @@ __device__ __forceinline__ float wave_sum(float v) {
     v += dpp<kSwap2>(v);
     v += dpp<kHalfMirror>(v);
     v += dpp<kMirror>(v);
-    return (of_lane(v, 0) + of_lane(v, 16)) + (of_lane(v, 32) + of_lane(v, 48));
+    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 
 // The largest value of each run of `lanes` lanes (a power of two), alike in all
@@ -47,7 +43,7 @@ __device__ __forceinline__ float lanes_max(float v, int lanes) {
 }
 __device__ __forceinline__ float wave_max(float v) {
     v = lanes_max(v, 16);
-    return fmaxf(fmaxf(of_lane(v, 0), of_lane(v, 16)), fmaxf(of_lane(v, 32), of_lane(v, 48)));
+    return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
 }
 
 // rank_of without a loop: spans past the last rank begin at the total.
