@@ -532,7 +532,8 @@ enum { RC_QUANTIZE_NONE = 0, RC_QUANTIZE_E4M3 = 1 };
  *   group         elements that share a scale: 32, 64, 128 or 256 consecutive
  *                 ones (a row's last group may hold fewer), or 0 for a row
  *   width         elements of a row, in [1, RC_MAX_NORM_WIDTH]
- *   eps           >= 0 (with 0, rows of zeros give NaN)
+ *   eps           >= 0 (with 0, rows of zeros give NaN, and rows whose squares
+ *                 vanish in float32, values below 2^-75, infinities)
  *   tokens        [R] rows of each rank */
 typedef struct rc_norm_desc {
     uint32_t struct_size;
@@ -571,7 +572,8 @@ int rc_rms_norm_grad(const rc_norm_desc* desc, const void* const* d_ys, const vo
 
 /* A mixture-of-experts layer for a few tokens: what a dispatch, the experts'
  * products and a combine give, by kernels that read the chosen experts'
- * weights where they lie, once for every 64 to 128 entries of an expert.  struct_size = sizeof(rc_moe_desc).
+ * weights where they lie, once for every 64 to 128 entries of an expert.
+ * struct_size = sizeof(rc_moe_desc).
  *   dtype         of the rows xs: RC_F32, RC_F16, RC_BF16 or RC_E4M3
  *   weight_dtype  dtype, or RC_E4M3 (not with RC_F32)
  *   out_dtype     of ys: dtype; with RC_E4M3 rows RC_F32, RC_F16 or RC_BF16
@@ -682,7 +684,8 @@ int rc_adamw_table(const rc_adamw_table_desc* desc, const int* num_params, const
  *   lr, beta1, beta2, eps, weight_decay  lr >= 0, betas in [0, 1), eps >= 0
  *   lr_on_gpu   NULL, or one float32 on the GPU that is used in place of lr
  *   norms       NULL, or [R] on the GPU: the norms of the ranks' gradients.  A
- *               rank whose norm is not finite is left as it is
+ *               rank whose norm is not finite (a gradient that is not, or a
+ *               norm past float32's range) is left as it is
  *   max_norm    0, or with norms: gradients of a rank whose norm (times
  *               |grad_scale|) is larger are scaled down to it
  *   grad_scale  factor of the gradients
@@ -725,8 +728,9 @@ typedef struct rc_adamw_desc {
  * that changes by a thousandth each step), and to no less than the smallest
  * code unless it is zero.  The chance of element i, u / 2^16 <= the part above the
  * code below, is a function of seed, t and i alone (another one for m), so ranks that hold the same
- * parameters keep them alike.  A gradient that is not finite spoils its element,
- * or block of an 8-bit state; give norms to leave such a step out.
+ * parameters keep them alike.  A gradient that is not finite, or whose square is
+ * beyond float32, spoils its element, or block of an 8-bit state; give norms to
+ * leave a step with gradients that are not finite out.
  * The states are read from `table` and written to `out_table`, another
  * table of parameters of the same sizes and types that shares no buffer with it,
  * or the same one: in place.  What has no gradient, or is left as it is, is copied. */

@@ -6,7 +6,7 @@ gradient sync (whole-call form; include/rc.h, "Block operators").
     d_xs, d_weights = rr.rms_norm_grad(d_ys, sums, weights, d_sums=d_hs)
 
     weights, experts = rr.route(logits, top_k=8)
-    ys = rr.moe_layer(xs, weights, experts, gate_up, down) # a few tokens, the experts' weights read once
+    ys = rr.moe_layer(xs, weights, experts, gate_up, down) # a few tokens, no dispatch
 
     state = rr.adamw_state(params, bits=8)                 # params[r]: {id: tensor}
     rr.all_reduce_params(grads, "mean", out=grads)
@@ -187,7 +187,8 @@ def moe_layer(xs, weights, experts, gate_up, down, scales=None, gate_up_scales=N
     [experts, 2 * inner] and down_scales [experts, width], float32 factors of the
     rows.  8-bit rows (rms_norm's with a scale a row: scales [tokens, 1]) take
     8-bit weights, and give ys of `dtype` (bfloat16 unless said or as `out` has
-    it).  The chosen experts' weights are read once, where they lie."""
+    it).  The chosen experts' weights are read where they lie, once for every 64 to
+    128 entries of an expert."""
     return _call("moe_layer", stream, xs, weights, experts, gate_up, down, scales, gate_up_scales, down_scales, dtype, out)
 
 
@@ -251,12 +252,12 @@ def adamw_step(state, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay
     """One AdamW step of every parameter that has a gradient, grads[r] a map
     {parameter id: tensor} of the parameters' types or float32 (include/rc.h has
     the formulas).  norms are grad_norm's: a rank whose norm is not finite makes
-    no step, and with max_norm larger gradients are scaled down to it, both
-    decided on the GPU.  grad_scale: a factor of the gradients before all that.
+    no step, and with max_norm larger gradients are scaled down to it, both decided on the GPU.  grad_scale: a factor of the gradients before all that.
     lr: a number, or a float32 tensor of one element on the GPU, for steps
     captured into a graph.  8-bit states are rounded by chance, as `seed`, the
-    step and the element's place say.  In place, or into `out`, another state of
-    the same parameters.  Steps of one state run one after the other."""
+    step and the element's place say: v's, and m's where it has no gradient and
+    would stay.  In place, or into `out`, another state of the same parameters.
+    Steps of one state run one after the other."""
     to = state if out is None else out
     _call("adamw_step", stream, state._table, state.step, to._table, to.step, grads, lr, betas[0], betas[1], eps,
           weight_decay, norms, 0.0 if max_norm is None else max_norm, grad_scale, seed)
