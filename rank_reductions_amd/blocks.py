@@ -252,7 +252,8 @@ def adamw_step(state, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay
     """One AdamW step of every parameter that has a gradient, grads[r] a map
     {parameter id: tensor} of the parameters' types or float32 (include/rc.h has
     the formulas).  norms are grad_norm's: a rank whose norm is not finite makes
-    no step, and with max_norm larger gradients are scaled down to it, both decided on the GPU.  grad_scale: a factor of the gradients before all that.
+    no step, and with max_norm larger gradients are scaled down to it, both
+    decided on the GPU.  grad_scale: a factor of the gradients before all that.
     lr: a number, or a float32 tensor of one element on the GPU, for steps
     captured into a graph.  8-bit states are rounded by chance, as `seed`, the
     step and the element's place say: v's, and m's where it has no gradient and

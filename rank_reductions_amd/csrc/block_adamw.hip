@@ -5,8 +5,8 @@
 // one chunk of one tensor.  The step's tensors stand in a table on the GPU, made
 // once; only the gradients, which a program may allocate anew, are arguments.
 // Two ranks' 405 million float32 elements take 2155 us (11.3 GB at 5.3 TB/s; half of
-// it is written), in bfloat16 with states of 8 bits 1275 us (6.5 GB at 5.1) and
-// their norms 162 (0.8 GB at 5.0; 8 GB at 5.8).  A few small tensors wait for
+// it is written), in bfloat16 with states of 8 bits 1353 us (6.5 GB at 4.8) and
+// their norms 164 (0.8 GB at 4.9; 8 GB at 5.8).  A few small tensors wait for
 // launches: 6 us the step, 6 and 2 the norms, 2.5 the factors.
 #include "blocks_impl.h"
 

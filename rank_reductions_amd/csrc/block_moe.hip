@@ -7,10 +7,10 @@
 // instructions take: 16 rows of weights by 16 entries, 64 bytes of each row at a
 // time.  Entries of an expert share its weights' pass; a lane's column of the
 // product is one entry, so an entry's result does not hang on which others stand
-// beside it.  One token of 4096 on 8 experts (302 MB of bfloat16 weights) takes 73
-// us, 4.1 TB/s; 64 tokens on 64 experts in 8 bits (1.2 GB) 279 us, 4.3 TB/s; 256
-// tokens, bfloat16 (2.4 GB), 545 us, 4.4 TB/s, where a kernel that only reads
-// reaches 5.9.  A kernel that holds every token's sum for its columns does without
+// beside it.  One token of 4096 on 8 experts (302 MB of bfloat16 weights) takes 72
+// us, 4.2 TB/s; 64 tokens on 64 experts in 8 bits (1.2 GB) 273 us, 4.4 TB/s; 256
+// tokens, bfloat16 (2.4 GB), 550 to 583 us, 4.2 to 4.4 TB/s, where a large copy
+// reaches 6.7.  A kernel that holds every token's sum for its columns does without
 // the third, but reads the hidden values once for each 16 columns: 190 us in place
 // of 100 for 64 tokens.
 #include "blocks_impl.h"
@@ -285,7 +285,10 @@ struct Stage {
     static constexpr int kSize = kRow * Planes * N * kTile;              // of one of the two buffers
     static constexpr int kUnits = kSteps * kPlane / 16;                  // 16-byte pieces of a row
     static constexpr int kMine = kUnits * Planes * N * kTile / kManyThreads;
-    static constexpr int kAhead = N < 8 && kSteps >= 8 ? 4 : kSteps >= 4 ? 2 : 1;  // as registers allow
+    // nearly as registers allow: 31 of the first kernel's are spilled with 16-bit rows
+    // and 8-bit weights, 25 to 33 of the second's with 16-bit weights and 10 with
+    // float32 outputs of 8-bit rows, none elsewhere
+    static constexpr int kAhead = N < 8 && kSteps >= 8 ? 4 : kSteps >= 4 ? 2 : 1;
     static_assert(kSteps >= 2 && kMine * kManyThreads == kUnits * Planes * N * kTile, "parts");
 };
 
@@ -618,7 +621,7 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
     }
 }
 
-// Tiles of entries at most that a wave has registers for.
+// Tiles of entries at most, nearly as registers allow.
 template <class W>
 constexpr int kDownMost = Down<W, 2>::kH == 2 ? 4 : 8;
 
@@ -831,8 +834,8 @@ unsigned groups(int64_t n, int of) { return (unsigned)((n + of - 1) / of); }
 // them once (64 tokens on 8 of 64 experts each, 8-bit weights: 279 us, and 352
 // without; 256 tokens, bfloat16: 543 and 892; 32 on 4 of 16: 140 and 152), but wait
 // for each other and are fewer (16 on 8 of 64: 383 and 362; 16 on 2 of 8: 117 and
-// 74).  Without, entries past 64 to an expert go to workgroups of their own (1024
-// tokens on two experts).  Rows have to hold one step.
+// 74; all timed at 4096 x 1536).  Without, entries past 64 to an expert go to
+// workgroups of their own (1024 tokens on two experts).  Rows have to hold one step.
 template <class X, class W, int Parts = 2>
 int run(const MoeArgs& a, hipStream_t s) {
     const int total = a.entries.total(), experts = min(a.num_experts, total);

@@ -9,8 +9,9 @@
 // dy * n, held in registers by a workgroup over the rows it takes, then added
 // up over the workgroups in order.
 // Both stream: 16384 rows of 4096 bf16 with a residual take 85 us forward (537 MB,
-// some from the last-level cache, at 6.2 TB/s) and 119 back (4.5 TB/s: a row waits
-// for its two sums); 6404 rows of 5003 float16 to 8 bits 58 us (3.9 TB/s).
+// some from the last-level cache, at 6.2 TB/s) and 122 back (4.5 TB/s: a row waits
+// for its two sums; rows of more than 16384 elements spill 90 to 143 registers); 6404
+// rows of 5003 float16 to 8 bits 58 us (3.9 TB/s).
 #include "blocks_impl.h"
 
 #ifndef RC_ROW_TYPE
