@@ -210,11 +210,12 @@ __device__ __forceinline__ float root_by_chance(float x, uint32_t u) {
     return x > 0.0f && c < 0x1p-9f ? 0x1p-9f : c;
 }
 
-// Four means m, of which a step left `rest` off, times what takes their block to e4m3.
-// Those that are `idle` (bits of it), whose gradients were below the eighth of the
-// smallest codes they had, and whose decay is less than half the distance of codes, are rounded by chance:
-// to nearest they would stay for ever where others hold the block's scale, and move
-// their parameters as far as the root that divides them has decayed.
+// Four means m after a step, times what takes their block to e4m3, as what is to be
+// rounded to nearest.  The `idle` ones (a bit each: their gradients were below the
+// eighth of the smallest codes they had) whose decay, `rest` = 1 - beta1 of them, is
+// less than half the distance of codes are rounded here, by chance: to nearest they
+// would stay for ever where others hold the block's scale, and move their parameters
+// the further the more the root that divides them has decayed.
 __device__ __forceinline__ void round_means(const float* m, uint32_t idle, float rest, float mf, uint32_t key, float* q) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = m[i] * mf;

@@ -137,8 +137,8 @@ struct Up {
 };
 
 // The second product's: the hidden values are float32, or Parts bfloat16 each (two,
-// an eighth of a float16's half step and less of a bfloat16's; three for float32
-// outputs), and the weights taken as bfloat16 (float16 ones, of 11 bits, as the sum
+// off by a 32nd of a float16's half step at most, less of a bfloat16's; three for
+// float32 outputs), and the weights taken as bfloat16 (float16 ones, of 11 bits, as the sum
 // of two: hidden values may pass float16's range).
 template <class W, int Parts>
 struct Down {
@@ -727,6 +727,7 @@ __device__ __forceinline__ void down_many(const MoeArgs& a, const Named& e, int 
     using M = Down<W, Parts>;
     constexpr int Rows = 2, kSize = M::kWide ? 4 : 2;
     using S = Stage<64 * M::kH * M::kParts, M::kParts, N>;
+    static_assert(S::kSize <= Stage<64 * M::kH * M::kParts, M::kParts, kDownMost<W>>::kSize, "the kernel's LDS");
     const int lane = lane_id(), sub = lane / kTile;
     const int rank = e.expert / a.per_rank, local = e.expert - rank * a.per_rank;
     const int tile = (blockIdx.x * kManyWaves + threadIdx.x / kWave) * Rows * kTile;

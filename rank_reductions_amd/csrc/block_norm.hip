@@ -299,7 +299,7 @@ int norm_of(const NormArgs& a, hipStream_t s) {
     if (vectors <= 1024) return run_norm<T, W, 4, 4>(a, s);
     if (vectors <= 1536) return run_norm<T, W, 8, 3>(a, s);
     if (vectors <= 2048) return run_norm<T, W, 8, 4>(a, s);
-    if (vectors <= 3072) return run_norm<T, W, 16, 3>(a, s);
+    if (vectors <= 3 * 1024) return run_norm<T, W, 16, 3>(a, s);
     if constexpr (T::n == 4)
         if (vectors > 4096) return run_norm<T, W, 16, 8>(a, s);
     return run_norm<T, W, 16, 4>(a, s);
